@@ -1,0 +1,170 @@
+"""CPU tests of the MX4 operators: the reference's rounding on worked values,
+the host packers and size queries against it, and the refusals of every entry
+point (rejected before any HIP call: the stand-in pointers are never read)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import w2a8_gemv_amd as w2a8
+from oracle import mx4
+
+NULL, SHAPE, ALIGN, VALUE, BUFSIZE = 1, 2, 3, 4, 5
+F = ctypes.c_float
+FAKE = 0x10000
+
+
+# ---------------------------------------------------------------------------
+# the reference itself
+# ---------------------------------------------------------------------------
+def test_reference_rounding_of_worked_values():
+    # one block whose largest magnitude is 6 (e = 0): ties go to even codes
+    x = np.array([[6, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, 5.1, 0.2, 0.3, -0.25, -5, -1.75, 0, -0.3]])
+    c, s = mx4.quant(x)
+    assert s.tolist() == [[127]]
+    assert mx4.values(c, s)[0].tolist() == [6, 0, 1, 1, 2, 2, 4, 4, 6, 0, 0.5, 0, -4, -2, 0, -0.5]
+    assert c[0, 11] == 8                               # a negative tie to zero keeps its sign
+    # a = 7.9: e = 0, saturates at 6; a = 8: e = 1
+    c, s = mx4.quant(np.array([[7.9]]))
+    assert (c.tolist(), s.tolist()) == ([[7]], [[127]])
+    c, s = mx4.quant(np.array([[8.0]]))
+    assert (c.tolist(), s.tolist()) == ([[6]], [[128]])
+    # zeros, the smallest exponent, not-a-numbers
+    assert mx4.quant(np.zeros((1, 3)))[1].tolist() == [[0]]
+    c, s = mx4.quant(np.array([[2.0 ** -127, 2.0 ** -128, 2.0 ** -130]]))
+    assert (c.tolist(), s.tolist()) == ([[2, 1, 0]], [[0]])
+    for bad in (np.nan, np.inf, -np.inf):
+        c, s = mx4.quant(np.array([[1.0, bad] + [1.0] * 31]))
+        assert s.tolist() == [[255, 125]] and not c[0, :32].any() and c[0, 32] == 6
+        assert np.isnan(mx4.values(c, s)[0, :32]).all()
+
+
+def test_reference_rounding_is_nearest():
+    """At most half a step off (2^-2 of the value between 1 and 6 units), and
+    idempotent."""
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((50, 320)) * np.exp2(rng.integers(-20, 20, (50, 1)))
+    c, s = mx4.quant(x)
+    v = mx4.values(c, s)
+    unit = np.repeat(mx4.scale_values(s), 32, 1)
+    y, m = np.abs(x) / unit, np.abs(v) / unit
+    step = np.where(y < 2, 0.5, np.where(y < 4, 1, 2))
+    assert (np.abs(y - m) <= np.where(y > 6, 2, step / 2)).all()
+    # (a block whose largest value saturated or rounded down keeps its unit)
+    c2, s2 = mx4.quant(v)
+    np.testing.assert_array_equal(mx4.values(c2, s2), v)
+
+
+# ---------------------------------------------------------------------------
+# sizes and host packers
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("R,K", [(1, 1), (3, 31), (16, 128), (17, 129), (33, 512), (5, 513), (40, 2560)])
+def test_sizes_and_packers_match_the_reference(R, K):
+    rng = np.random.default_rng(R * K)
+    codes = rng.integers(0, 16, (R, K)).astype(np.uint8)
+    scales = rng.integers(0, 256, (R, -(-K // 32))).astype(np.uint8)
+    q, s = mx4.rows_layout(codes, scales)
+    assert w2a8.mx4_act_bytes(R, K) == q.size and w2a8.mx4_scale_bytes(R, K) == s.size
+    inter = torch.from_numpy(mx4.interchange(codes))
+    packed = w2a8.pack_mx4(inter, torch.from_numpy(scales), R, K)
+    want = mx4.packed_layout(codes, scales)
+    assert packed.numel() == want.size == w2a8.mx4_packed_bytes(R, K)
+    np.testing.assert_array_equal(packed.numpy(), want)
+    c, sc = w2a8.unpack_mx4(packed, R, K)
+    np.testing.assert_array_equal(c.numpy(), inter.numpy())
+    np.testing.assert_array_equal(sc.numpy(), scales)
+
+
+def test_size_queries_refuse():
+    L = w2a8.lib()
+    for f in (L.mx4_act_bytes, L.mx4_scale_bytes, L.mx4_packed_bytes):
+        assert f(0, 5) == -1 and f(5, 0) == -1 and f(5, 1048449) == -1 and f(5, 1048448) > 0
+    assert L.mx4_act_bytes((1 << 20) + 1, 5) == -1 and L.mx4_packed_bytes((1 << 30) + 1, 5) == -1
+    for f in (w2a8.mx4_act_bytes, w2a8.mx4_scale_bytes, w2a8.mx4_packed_bytes):
+        with pytest.raises(w2a8.W2A8Error) as e:
+            f(0, 16)
+        assert e.value.status == SHAPE
+
+
+def test_packers_refuse():
+    L = w2a8.lib()
+    c, s = np.zeros((4, 20), np.uint8), np.zeros((4, 2), np.uint8)
+    out = np.zeros(w2a8.mx4_packed_bytes(4, 40), np.uint8)
+    cp, sp, op, n = c.ctypes.data, s.ctypes.data, out.ctypes.data, out.size
+    for args in ((None, sp, 4, 40, op, n), (cp, None, 4, 40, op, n), (cp, sp, 4, 40, None, n)):
+        assert L.pack_mx4(*args) == NULL
+    assert L.pack_mx4(cp, sp, 0, 40, op, n) == SHAPE
+    assert L.pack_mx4(cp, sp, 4, 40, op, n - 1) == BUFSIZE
+    assert L.pack_mx4(cp, sp, 4, 40, op, n) == 0
+    assert L.unpack_mx4(op, n - 1, 4, 40, cp, sp) == BUFSIZE
+    assert L.unpack_mx4(op, n, 4, 0, cp, sp) == SHAPE
+    assert L.unpack_mx4(None, n, 4, 40, cp, sp) == NULL
+    t = torch.zeros
+    with pytest.raises(ValueError):
+        w2a8.pack_mx4(t((4, 19), dtype=torch.uint8), t((4, 2), dtype=torch.uint8), 4, 40)
+    with pytest.raises(ValueError):
+        w2a8.pack_mx4(t((4, 20), dtype=torch.uint8), t((4, 1), dtype=torch.uint8), 4, 40)
+    with pytest.raises(TypeError):
+        w2a8.pack_mx4(t((4, 20)), t((4, 2), dtype=torch.uint8), 4, 40)
+    with pytest.raises(w2a8.W2A8Error):
+        w2a8.unpack_mx4(t(n - 1, dtype=torch.uint8), 4, 40)
+
+
+# ---------------------------------------------------------------------------
+# refusals of the device entry points
+# ---------------------------------------------------------------------------
+def test_row_entry_points_refuse():
+    L = w2a8.lib()
+    q = lambda x=FAKE, t=1, M=3, K=40, xq=FAKE, xs=FAKE: L.quant_act_mx4(x, t, M, K, xq, xs, None)
+    d = lambda y=FAKE, t=1, M=3, K=40, xq=FAKE, xs=FAKE: L.dequant_act_mx4(xq, xs, M, K, y, t, None)
+    for f, first in ((q, "x"), (d, "y")):
+        assert f(**{first: None}) == NULL and f(xq=None) == NULL and f(xs=None) == NULL
+        assert f(M=0) == SHAPE and f(K=0) == SHAPE and f(K=1048449) == SHAPE
+        assert f(M=(1 << 20) + 1) == SHAPE
+        assert f(t=-1) == VALUE and f(t=3) == VALUE
+        assert f(**{first: FAKE + 2}) == ALIGN and f(xq=FAKE + 8) == ALIGN and f(xs=FAKE + 4) == ALIGN
+    need = w2a8.mx4_packed_bytes(20, 300)
+    p = lambda W=FAKE, t=0, N=20, K=300, o=FAKE, n=need: L.quant_pack_mx4(W, t, N, K, o, n, None)
+    assert p(W=None) == NULL and p(o=None) == NULL and p(N=0) == SHAPE and p(t=7) == VALUE
+    assert p(W=FAKE + 4) == ALIGN and p(o=FAKE + 8) == ALIGN and p(n=need - 1) == BUFSIZE
+
+
+@pytest.mark.parametrize("kind", ["w4mx4", "w2mx4"])
+def test_products_refuse(kind):
+    L = w2a8.lib()
+    sw = (F(1.0),) if kind == "w2mx4" else ()
+
+    def g(w=FAKE, xq=FAKE, xs=FAKE, M=3, N=40, K=200, yf=FAKE, yb=FAKE):
+        return getattr(L, kind + "_gemm")(w, xq, xs, M, N, K, *sw, yf, yb, None)
+
+    def v(w=FAKE, x=FAKE, t=1, N=40, K=200, yf=FAKE, yb=FAKE):
+        return getattr(L, kind + "_linear_gemv")(w, x, t, N, K, *sw, yf, yb, None)
+    for f in (g, v):
+        assert f(w=None) == NULL and f(yf=None, yb=None) == NULL
+        assert f(N=0) == SHAPE and f(K=0) == SHAPE and f(N=(1 << 30) + 1) == SHAPE
+        assert f(K=1048449) == SHAPE
+        assert f(w=FAKE + 8) == ALIGN and f(yf=FAKE + 4) == ALIGN and f(yb=FAKE + 2) == ALIGN
+    assert g(xq=None) == NULL and g(xs=None) == NULL and g(M=0) == SHAPE
+    assert g(M=(1 << 20) + 1) == SHAPE and g(xq=FAKE + 8) == ALIGN and g(xs=FAKE + 4) == ALIGN
+    assert v(x=None) == NULL and v(x=FAKE + 2) == ALIGN
+    assert v(t=-1) == VALUE and v(t=3) == VALUE
+
+
+def test_binding_refuses_host_tensors_and_wrong_types():
+    x = torch.zeros((2, 64), dtype=torch.bfloat16)
+    u8 = torch.zeros(4096, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        w2a8.quant_act_mx4(x)
+    with pytest.raises(ValueError):
+        w2a8.linear_w4mx4(x, u8, 16, 64)
+    with pytest.raises(ValueError):
+        w2a8.linear_w2mx4(x, u8, 1.0, 16, 64)
+    with pytest.raises(ValueError):
+        w2a8.gemm_w4mx4(u8, u8.view(2, -1), u8, 16, 64)
+    with pytest.raises(ValueError):
+        w2a8.quant_pack_mx4(x.float())
+    with pytest.raises(TypeError):
+        w2a8.quant_act_mx4(x.double())
+    with pytest.raises(TypeError):
+        w2a8.quant_act_mx4([1.0])

@@ -26,6 +26,10 @@ __all__ = [
     "tune_gemm", "tune_gemm_ring", "tune_gemm_pipe",
     "act4_bytes", "pack_act_int4", "quant_act_int4", "w2a4_gemv", "w2a4_linear_gemv",
     "linear_a4", "w2a8_gemv_grouped", "w2a8_linear_gemv_grouped", "linear_grouped",
+    "mx4_act_bytes", "mx4_scale_bytes", "mx4_packed_bytes", "pack_mx4", "unpack_mx4",
+    "quant_act_mx4", "dequant_act_mx4", "quant_pack_mx4", "w4mx4_gemm", "w2mx4_gemm",
+    "w4mx4_linear_gemv", "w2mx4_linear_gemv", "gemm_w4mx4", "gemm_w2mx4", "linear_w4mx4",
+    "linear_w2mx4",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw2a8.so")
@@ -93,6 +97,20 @@ def lib():
         L.w2a8_gemv_grouped.restype = I32
         L.w2a8_linear_gemv_grouped.argtypes = [I32, P, P, I64, P, P, P, P, P, I64, P]
         L.w2a8_linear_gemv_grouped.restype = I32
+        for name in ("mx4_act_bytes", "mx4_scale_bytes", "mx4_packed_bytes"):
+            getattr(L, name).argtypes = [I64, I64]
+            getattr(L, name).restype = I64
+        for name, args in (("pack_mx4", [P, P, I64, I64, P, I64]),
+                           ("unpack_mx4", [P, I64, I64, I64, P, P]),
+                           ("quant_act_mx4", [P, I32, I64, I64, P, P, P]),
+                           ("dequant_act_mx4", [P, P, I64, I64, P, I32, P]),
+                           ("quant_pack_mx4", [P, I32, I64, I64, P, I64, P]),
+                           ("w4mx4_gemm", [P, P, P, I64, I64, I64, P, P, P]),
+                           ("w2mx4_gemm", [P, P, P, I64, I64, I64, F32, P, P, P]),
+                           ("w4mx4_linear_gemv", [P, P, I32, I64, I64, P, P, P]),
+                           ("w2mx4_linear_gemv", [P, P, I32, I64, I64, F32, P, P, P])):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = I32
         L.w2a8_tune_gemv.argtypes = [I32, I32, I32, I32, I32]
         L.w2a8_tune_gemv.restype = I32
         L.w2a8_gemv_plan.argtypes = [I64, I64, I32, P, P, P, P]
@@ -557,6 +575,290 @@ def linear(x_bf16, w_packed, s_w, N, K, stream=None, fused=True):
     else:
         w2a8_gemm(w_packed, xq, M, N, K, s_a=sa, s_w=s_w, y_f32=y, stream=stream)
     return y
+
+
+# ---------------------------------------------------------------------------
+# MX4: 4-bit floats in blocks of 32 with a power-of-two scale (see
+# include/w2a8_mx4.h)
+# ---------------------------------------------------------------------------
+_MX4_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _mx4_size(name, a, b):
+    v = int(getattr(lib(), name)(a, b))
+    if v < 0:
+        raise W2A8Error(2, name)
+    return v
+
+
+def mx4_act_bytes(M: int, K: int) -> int:
+    """Code bytes of M rows of K values (MX4R)."""
+    return _mx4_size("mx4_act_bytes", M, K)
+
+
+def mx4_scale_bytes(M: int, K: int) -> int:
+    """Scale bytes of M rows of K values (MX4R)."""
+    return _mx4_size("mx4_scale_bytes", M, K)
+
+
+def mx4_packed_bytes(N: int, K: int) -> int:
+    """Bytes of packed MX4 weights (MX16x128)."""
+    return _mx4_size("mx4_packed_bytes", N, K)
+
+
+def pack_mx4(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int) -> torch.Tensor:
+    """Interchange form (CPU): codes uint8 [N, ceil(K/2)], two values a byte, the lower k in
+    the lower half, and scales uint8 [N, ceil(K/32)] -> packed uint8 [mx4_packed_bytes] (CPU)."""
+    _need(codes, "codes", torch.uint8, "cpu", (N, -(-K // 2)))
+    _need(scales, "scales", torch.uint8, "cpu", (N, -(-K // 32)))
+    out = torch.empty(mx4_packed_bytes(N, K), dtype=torch.uint8)
+    _check(lib().pack_mx4(_ptr(codes), _ptr(scales), N, K, _ptr(out), out.numel()), "pack_mx4")
+    return out
+
+
+def unpack_mx4(packed: torch.Tensor, N: int, K: int):
+    """Packed MX4 weights (CPU) -> (codes, scales) in the interchange form."""
+    _need(packed, "packed", torch.uint8, "cpu")
+    mx4_packed_bytes(N, K)
+    codes = torch.empty((N, -(-K // 2)), dtype=torch.uint8)
+    scales = torch.empty((N, -(-K // 32)), dtype=torch.uint8)
+    _check(lib().unpack_mx4(_ptr(packed), packed.numel(), N, K, _ptr(codes), _ptr(scales)),
+           "unpack_mx4")
+    return codes, scales
+
+
+def _mx4_need(t, name, device, dtype=torch.uint8, numel=None, least=None):
+    """A contiguous tensor of `dtype` on `device`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the first argument on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+    if least is not None and t.numel() < least:
+        raise ValueError(f"{name} must have at least {least} elements, got {t.numel()}")
+
+
+def _mx4_float(t, name):
+    """The w2a8_mx4_type of a contiguous float tensor, and its device (the current one)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _MX4_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return code, _mx4_device(t, name)
+
+
+def _mx4_device(t, name):
+    """The device of a tensor, which has to be the current GPU."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return t.device
+
+
+def _mx4_stream(stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return stream.cuda_stream
+
+
+def _mx4_empty(shape, dtype, device, stream):
+    """Uninitialised memory that belongs to the stream of the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _mx4_rows(x, name):
+    if x.dim() == 1:
+        return 1, x.shape[0]
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [M, K] or [K]")
+    return x.shape
+
+
+def quant_act_mx4(x: torch.Tensor, x_q=None, x_s=None, stream=None):
+    """x fp32, bf16 or fp16 [M, K] (or [K]: one row; device) -> (x_q uint8 [M, 64 * KT] codes,
+    x_s uint8 [M, 16 * KU] scale bytes), the MX4R layout.  x_q and x_s may be given (any shape
+    of at least mx4_act_bytes / mx4_scale_bytes elements)."""
+    code, dev = _mx4_float(x, "x")
+    M, K = _mx4_rows(x, "x")
+    nq, ns = mx4_act_bytes(M, K), mx4_scale_bytes(M, K)
+    if x_q is None:
+        x_q = _mx4_empty((M, nq // M), torch.uint8, dev, stream)
+    else:
+        _mx4_need(x_q, "x_q", dev, least=nq)
+    if x_s is None:
+        x_s = _mx4_empty((M, ns // M), torch.uint8, dev, stream)
+    else:
+        _mx4_need(x_s, "x_s", dev, least=ns)
+    _check(lib().quant_act_mx4(x.data_ptr(), code, M, K, x_q.data_ptr(), x_s.data_ptr(),
+                               _mx4_stream(stream, dev)), "quant_act_mx4")
+    return x_q, x_s
+
+
+def _mx4_act(x_q, x_s, M, K):
+    """The device of MX4R rows; M None: as many as x_q has (a 2-d tensor)."""
+    if not isinstance(x_q, torch.Tensor):
+        raise TypeError("x_q must be a torch.Tensor")
+    if M is None:
+        if x_q.dim() != 2:
+            raise ValueError("x_q must be [M, bytes of a row] where M is not given")
+        M = x_q.shape[0]
+    dev = _mx4_device(x_q, "x_q")
+    _mx4_need(x_q, "x_q", dev, least=mx4_act_bytes(M, K))
+    _mx4_need(x_s, "x_s", dev, least=mx4_scale_bytes(M, K))
+    return M, dev
+
+
+def dequant_act_mx4(x_q, x_s, K: int, M=None, dtype=torch.float32, y=None, stream=None):
+    """MX4R rows -> their values [M, K] in fp32, bf16 or fp16 (device).  M defaults to the
+    rows of a 2-d x_q; y may be given (M * K elements of dtype)."""
+    M, dev = _mx4_act(x_q, x_s, M, K)
+    code = _MX4_TYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    if y is None:
+        y = _mx4_empty((M, K), dtype, dev, stream)
+    else:
+        _mx4_need(y, "y", dev, dtype, numel=M * K)
+    _check(lib().dequant_act_mx4(x_q.data_ptr(), x_s.data_ptr(), M, K, y.data_ptr(), code,
+                                 _mx4_stream(stream, dev)), "dequant_act_mx4")
+    return y
+
+
+def quant_pack_mx4(W: torch.Tensor, packed=None, stream=None) -> torch.Tensor:
+    """Float weights [N, K] (device) -> packed MX4 weights uint8 [mx4_packed_bytes(N, K)]."""
+    code, dev = _mx4_float(W, "W")
+    if W.dim() != 2:
+        raise ValueError("W must be [N, K]")
+    N, K = W.shape
+    nb = mx4_packed_bytes(N, K)
+    if packed is None:
+        packed = _mx4_empty(nb, torch.uint8, dev, stream)
+    else:
+        _mx4_need(packed, "packed", dev, least=nb)
+    _check(lib().quant_pack_mx4(W.data_ptr(), code, N, K, packed.data_ptr(), packed.numel(),
+                                _mx4_stream(stream, dev)), "quant_pack_mx4")
+    return packed
+
+
+def _mx4_outputs(y_f32, y_bf16, dev, count):
+    for t, nm, dt in ((y_f32, "y_f32", torch.float32), (y_bf16, "y_bf16", torch.bfloat16)):
+        if t is not None:
+            _mx4_need(t, nm, dev, dt, numel=count)
+    return (None if y_f32 is None else y_f32.data_ptr(),
+            None if y_bf16 is None else y_bf16.data_ptr())
+
+
+def w4mx4_gemm(w_packed, x_q, x_s, M, N, K, y_f32=None, y_bf16=None, stream=None):
+    """Raw C-ABI call: MX4 rows times MX4 weights (outputs must be given); returns nothing."""
+    M, dev = _mx4_act(x_q, x_s, M, K)
+    _mx4_need(w_packed, "w_packed", dev, least=mx4_packed_bytes(N, K))
+    yf, yb = _mx4_outputs(y_f32, y_bf16, dev, M * N)
+    _check(lib().w4mx4_gemm(w_packed.data_ptr(), x_q.data_ptr(), x_s.data_ptr(), M, N, K, yf, yb,
+                            _mx4_stream(stream, dev)), "w4mx4_gemm")
+
+
+def w2mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w=1.0, y_f32=None, y_bf16=None, stream=None):
+    """Raw C-ABI call: MX4 rows times packed ternary weights; returns nothing."""
+    M, dev = _mx4_act(x_q, x_s, M, K)
+    _mx4_need(w_packed, "w_packed", dev, least=packed_bytes(N, K))
+    yf, yb = _mx4_outputs(y_f32, y_bf16, dev, M * N)
+    _check(lib().w2mx4_gemm(w_packed.data_ptr(), x_q.data_ptr(), x_s.data_ptr(), M, N, K, s_w, yf,
+                            yb, _mx4_stream(stream, dev)), "w2mx4_gemm")
+
+
+def w4mx4_linear_gemv(w_packed, x, N, K, y_f32=None, y_bf16=None, stream=None):
+    """Raw C-ABI call: one float row, rounded to MX4 and multiplied in one launch."""
+    code, dev = _mx4_float(x, "x")
+    if x.numel() != K:
+        raise ValueError("x must have K elements")
+    _mx4_need(w_packed, "w_packed", dev, least=mx4_packed_bytes(N, K))
+    yf, yb = _mx4_outputs(y_f32, y_bf16, dev, N)
+    _check(lib().w4mx4_linear_gemv(w_packed.data_ptr(), x.data_ptr(), code, N, K, yf, yb,
+                                   _mx4_stream(stream, dev)), "w4mx4_linear_gemv")
+
+
+def w2mx4_linear_gemv(w_packed, x, N, K, s_w=1.0, y_f32=None, y_bf16=None, stream=None):
+    """Raw C-ABI call: w4mx4_linear_gemv with packed ternary weights."""
+    code, dev = _mx4_float(x, "x")
+    if x.numel() != K:
+        raise ValueError("x must have K elements")
+    _mx4_need(w_packed, "w_packed", dev, least=packed_bytes(N, K))
+    yf, yb = _mx4_outputs(y_f32, y_bf16, dev, N)
+    _check(lib().w2mx4_linear_gemv(w_packed.data_ptr(), x.data_ptr(), code, N, K, s_w, yf, yb,
+                                   _mx4_stream(stream, dev)), "w2mx4_linear_gemv")
+
+
+def _mx4_out(dtype, shape, dev, stream):
+    """A new output and its place among the outputs of a raw call."""
+    if dtype is torch.float32:
+        y = _mx4_empty(shape, dtype, dev, stream)
+        return y, {"y_f32": y}
+    if dtype is torch.bfloat16:
+        y = _mx4_empty(shape, dtype, dev, stream)
+        return y, {"y_bf16": y}
+    raise TypeError(f"out_dtype must be float32 or bfloat16, got {dtype}")
+
+
+def gemm_w4mx4(w_packed, x_q, x_s, N, K, out_dtype=torch.float32, stream=None):
+    """MX4R rows (x_q [M, bytes of a row]) times MX4 weights -> fp32 or bf16 [M, N]."""
+    M, dev = _mx4_act(x_q, x_s, None, K)
+    y, out = _mx4_out(out_dtype, (M, N), dev, stream)
+    w4mx4_gemm(w_packed, x_q, x_s, M, N, K, stream=stream, **out)
+    return y
+
+
+def gemm_w2mx4(w_packed, x_q, x_s, s_w, N, K, out_dtype=torch.float32, stream=None):
+    """MX4R rows (x_q [M, bytes of a row]) times ternary weights -> fp32 or bf16 [M, N]."""
+    M, dev = _mx4_act(x_q, x_s, None, K)
+    y, out = _mx4_out(out_dtype, (M, N), dev, stream)
+    w2mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w, stream=stream, **out)
+    return y
+
+
+def _linear_mx4(x, N, K, out_dtype, stream, fused, gemv, gemm):
+    _, dev = _mx4_float(x, "x")
+    M, k = _mx4_rows(x, "x")
+    if k != K:
+        raise ValueError(f"x must have rows of {K} values, got {k}")
+    y, out = _mx4_out(out_dtype, (M, N), dev, stream)
+    if M == 1 and fused:
+        gemv(x, out)
+    else:
+        gemm(*quant_act_mx4(x, stream=stream), M, out)
+    return y
+
+
+def linear_w4mx4(x, w_packed, N, K, out_dtype=torch.float32, stream=None, fused=True):
+    """Linear layer with MX4 weights: float rows [M, K] (or [K]) -> fp32 or bf16 [M, N].
+
+    M == 1 with fused=True: w4mx4_linear_gemv (one launch).  Otherwise quant_act_mx4, then
+    w4mx4_gemm.  Both routes give bit-identical results."""
+    return _linear_mx4(
+        x, N, K, out_dtype, stream, fused,
+        lambda row, out: w4mx4_linear_gemv(w_packed, row, N, K, stream=stream, **out),
+        lambda q, s, M, out: w4mx4_gemm(w_packed, q, s, M, N, K, stream=stream, **out))
+
+
+def linear_w2mx4(x, w_packed, s_w, N, K, out_dtype=torch.float32, stream=None, fused=True):
+    """Linear layer with packed ternary weights and MX4 activations (as linear_w4mx4)."""
+    return _linear_mx4(
+        x, N, K, out_dtype, stream, fused,
+        lambda row, out: w2mx4_linear_gemv(w_packed, row, N, K, s_w, stream=stream, **out),
+        lambda q, s, M, out: w2mx4_gemm(w_packed, q, s, M, N, K, s_w, stream=stream, **out))
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,199 @@
+// C ABI of the MX4 rows, weights and products (w2a8_mx4.h): size queries,
+// host packers and device entry points.  Validation happens on the host
+// before any HIP call.
+#include <cstring>
+
+#include "mx4.h"
+
+namespace w2a8 {
+namespace {
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool rows_ok(int64_t M, int64_t K) { return M >= 1 && M <= kMaxM && K >= 1 && K <= W2A8_MAX_K; }
+bool matrix_ok(int64_t N, int64_t K) { return N >= 1 && N <= kMaxN && K >= 1 && K <= W2A8_MAX_K; }
+bool type_ok(int t) { return t == W2A8_F32 || t == W2A8_BF16 || t == W2A8_F16; }
+
+// Byte and half of value i (0..31) of a block's 16 code bytes.
+int code_byte(int i) { return (i / 16) * 8 + (i % 16 / 4 % 2) * 4 + i % 4; }
+int code_shift(int i) { return i % 16 >= 8 ? 4 : 0; }
+
+// Offsets in the packed weights of a block's codes and scale byte.
+struct Place {
+    int64_t codes, scale;
+};
+Place place(int64_t n, int64_t b, int64_t NS, int64_t KT, int64_t KU) {
+    const int64_t s = n / kMxRows, t = b / 4, l = 16 * (b % 4) + n % kMxRows;
+    return {(s * KT + t) * kMxTileBytes + 16 * l,
+            NS * KT * kMxTileBytes + (s * KU + t / kMxQuad) * 256 + 4 * l + t % kMxQuad};
+}
+
+hipError_t rows_launch(const Mx4Launch &a, const DeviceInfo &dev, hipStream_t stream) {
+    return launch_mx4_stream(a, dev.cus, stream);
+}
+
+// Shared by the four product entry points.  x_type < 0: MX4R rows.
+int product(const void *w, bool ternary, const uint8_t *xq, const uint8_t *xs, const void *x,
+            int x_type, int64_t M, int64_t N, int64_t K, float s_w, float *y_f32, uint16_t *y_bf16,
+            void *stream) {
+    const bool rows = x_type < 0;
+    if (!w || (rows ? !xq || !xs : !x) || (!y_f32 && !y_bf16)) return W2A8_ERR_NULL;
+    if (!rows_ok(M, K) || !matrix_ok(N, K)) return W2A8_ERR_SHAPE;
+    if (!rows && !type_ok(x_type)) return W2A8_ERR_VALUE;
+    if (!aligned16(w) || !aligned16(xq) || !aligned16(xs) || !aligned16(x) || !aligned16(y_f32) ||
+        !aligned16(y_bf16))
+        return W2A8_ERR_ALIGN;
+    DeviceInfo dev;
+    const int st = current_device(&dev);
+    if (st != W2A8_OK) return st;
+    Mx4Launch a;
+    a.KT = int(mx4_tiles(K));
+    a.KU = int(mx4_quads(K));
+    a.w = static_cast<const uint8_t *>(w);
+    a.ws = ternary ? nullptr : a.w + ceil_div(N, kMxRows) * a.KT * kMxTileBytes;
+    a.xq = xq;
+    a.xs = xs;
+    a.x = x;
+    a.y_f32 = y_f32;
+    a.y_bf16 = y_bf16;
+    a.sw = s_w;
+    a.M = int(M);
+    a.N = int(N);
+    a.K = int(K);
+    a.strips = 0;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const hipError_t e = rows ? rows_launch(a, dev, s) : launch_mx4_fused(a, x_type, dev.cus, s);
+    return e == hipSuccess ? W2A8_OK : W2A8_ERR_LAUNCH;
+}
+
+}  // namespace
+}  // namespace w2a8
+
+using namespace w2a8;
+
+extern "C" {
+
+int64_t mx4_act_bytes(int64_t M, int64_t K) {
+    return rows_ok(M, K) ? M * mx4_tiles(K) * kMxRowTile : -1;
+}
+
+int64_t mx4_scale_bytes(int64_t M, int64_t K) { return rows_ok(M, K) ? M * mx4_quads(K) * 16 : -1; }
+
+int64_t mx4_packed_bytes(int64_t N, int64_t K) {
+    if (!matrix_ok(N, K)) return -1;
+    return ceil_div(N, kMxRows) * (mx4_tiles(K) * kMxTileBytes + mx4_quads(K) * 256);
+}
+
+int pack_mx4(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t K, void *packed,
+             int64_t packed_bytes) {
+    if (!codes || !scales || !packed) return W2A8_ERR_NULL;
+    const int64_t need = mx4_packed_bytes(N, K);
+    if (need < 0) return W2A8_ERR_SHAPE;
+    if (packed_bytes < need) return W2A8_ERR_BUFSIZE;
+    uint8_t *out = static_cast<uint8_t *>(packed);
+    memset(out, 0, size_t(need));
+    const int64_t NS = ceil_div(N, kMxRows), KT = mx4_tiles(K), KU = mx4_quads(K);
+    const int64_t blocks = ceil_div(K, 32), row = ceil_div(K, 2);
+    for (int64_t n = 0; n < N; ++n)
+        for (int64_t b = 0; b < blocks; ++b) {
+            const Place p = place(n, b, NS, KT, KU);
+            out[p.scale] = scales[n * blocks + b];
+            for (int i = 0; i < 32 && 32 * b + i < K; ++i) {
+                const int64_t k = 32 * b + i;
+                const unsigned c = (codes[n * row + k / 2] >> (4 * (k & 1))) & 15u;
+                out[p.codes + code_byte(i)] |= uint8_t(c << code_shift(i));
+            }
+        }
+    return W2A8_OK;
+}
+
+int unpack_mx4(const void *packed, int64_t packed_bytes, int64_t N, int64_t K, uint8_t *codes,
+               uint8_t *scales) {
+    if (!codes || !scales || !packed) return W2A8_ERR_NULL;
+    const int64_t need = mx4_packed_bytes(N, K);
+    if (need < 0) return W2A8_ERR_SHAPE;
+    if (packed_bytes < need) return W2A8_ERR_BUFSIZE;
+    const uint8_t *in = static_cast<const uint8_t *>(packed);
+    const int64_t NS = ceil_div(N, kMxRows), KT = mx4_tiles(K), KU = mx4_quads(K);
+    const int64_t blocks = ceil_div(K, 32), row = ceil_div(K, 2);
+    memset(codes, 0, size_t(N * row));
+    for (int64_t n = 0; n < N; ++n)
+        for (int64_t b = 0; b < blocks; ++b) {
+            const Place p = place(n, b, NS, KT, KU);
+            scales[n * blocks + b] = in[p.scale];
+            for (int i = 0; i < 32 && 32 * b + i < K; ++i) {
+                const int64_t k = 32 * b + i;
+                const unsigned c = (in[p.codes + code_byte(i)] >> code_shift(i)) & 15u;
+                codes[n * row + k / 2] |= uint8_t(c << (4 * (k & 1)));
+            }
+        }
+    return W2A8_OK;
+}
+
+int quant_act_mx4(const void *x, int x_type, int64_t M, int64_t K, uint8_t *x_q, uint8_t *x_s,
+                  void *stream) {
+    if (!x || !x_q || !x_s) return W2A8_ERR_NULL;
+    if (!rows_ok(M, K)) return W2A8_ERR_SHAPE;
+    if (!type_ok(x_type)) return W2A8_ERR_VALUE;
+    if (!aligned16(x) || !aligned16(x_q) || !aligned16(x_s)) return W2A8_ERR_ALIGN;
+    DeviceInfo dev;
+    const int st = current_device(&dev);
+    if (st != W2A8_OK) return st;
+    const hipError_t e =
+        launch_quant_mx4(x, x_type, M, int(K), x_q, x_s, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? W2A8_OK : W2A8_ERR_LAUNCH;
+}
+
+int dequant_act_mx4(const uint8_t *x_q, const uint8_t *x_s, int64_t M, int64_t K, void *y,
+                    int y_type, void *stream) {
+    if (!x_q || !x_s || !y) return W2A8_ERR_NULL;
+    if (!rows_ok(M, K)) return W2A8_ERR_SHAPE;
+    if (!type_ok(y_type)) return W2A8_ERR_VALUE;
+    if (!aligned16(x_q) || !aligned16(x_s) || !aligned16(y)) return W2A8_ERR_ALIGN;
+    DeviceInfo dev;
+    const int st = current_device(&dev);
+    if (st != W2A8_OK) return st;
+    const hipError_t e =
+        launch_dequant_mx4(x_q, x_s, M, int(K), y, y_type, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? W2A8_OK : W2A8_ERR_LAUNCH;
+}
+
+int quant_pack_mx4(const void *W, int w_type, int64_t N, int64_t K, void *w_packed,
+                   int64_t packed_bytes, void *stream) {
+    if (!W || !w_packed) return W2A8_ERR_NULL;
+    const int64_t need = mx4_packed_bytes(N, K);
+    if (need < 0) return W2A8_ERR_SHAPE;
+    if (!type_ok(w_type)) return W2A8_ERR_VALUE;
+    if (!aligned16(W) || !aligned16(w_packed)) return W2A8_ERR_ALIGN;
+    if (packed_bytes < need) return W2A8_ERR_BUFSIZE;
+    DeviceInfo dev;
+    const int st = current_device(&dev);
+    if (st != W2A8_OK) return st;
+    const hipError_t e = launch_quant_pack_mx4(W, w_type, N, int(K), static_cast<uint8_t *>(w_packed),
+                                               static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? W2A8_OK : W2A8_ERR_LAUNCH;
+}
+
+int w4mx4_gemm(const void *w_packed, const uint8_t *x_q, const uint8_t *x_s, int64_t M, int64_t N,
+               int64_t K, float *y_f32, uint16_t *y_bf16, void *stream) {
+    return product(w_packed, false, x_q, x_s, nullptr, -1, M, N, K, 1.0f, y_f32, y_bf16, stream);
+}
+
+int w2mx4_gemm(const void *w_packed, const uint8_t *x_q, const uint8_t *x_s, int64_t M, int64_t N,
+               int64_t K, float s_w, float *y_f32, uint16_t *y_bf16, void *stream) {
+    return product(w_packed, true, x_q, x_s, nullptr, -1, M, N, K, s_w, y_f32, y_bf16, stream);
+}
+
+int w4mx4_linear_gemv(const void *w_packed, const void *x, int x_type, int64_t N, int64_t K,
+                      float *y_f32, uint16_t *y_bf16, void *stream) {
+    // An unknown type must not read as "rows".
+    return product(w_packed, false, nullptr, nullptr, x, x_type < 0 ? 99 : x_type, 1, N, K, 1.0f,
+                   y_f32, y_bf16, stream);
+}
+
+int w2mx4_linear_gemv(const void *w_packed, const void *x, int x_type, int64_t N, int64_t K,
+                      float s_w, float *y_f32, uint16_t *y_bf16, void *stream) {
+    return product(w_packed, true, nullptr, nullptr, x, x_type < 0 ? 99 : x_type, 1, N, K, s_w,
+                   y_f32, y_bf16, stream);
+}
+
+}  // extern "C"
