@@ -13,6 +13,7 @@ tensors on the current device and enqueue work on the current stream (or on
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -584,6 +585,7 @@ def linear(x_bf16, w_packed, s_w, N, K, stream=None, fused=True):
 _MX4_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
+@functools.lru_cache(maxsize=4096)
 def _mx4_size(name, a, b):
     v = int(getattr(lib(), name)(a, b))
     if v < 0:
@@ -627,24 +629,41 @@ def unpack_mx4(packed: torch.Tensor, N: int, K: int):
     return codes, scales
 
 
-def _mx4_need(t, name, device, dtype=torch.uint8, numel=None, least=None):
-    """A contiguous tensor of `dtype` on `device`."""
+# The calls below cost the host about as much as their kernels take at one
+# row, so each argument is checked once and by one expression.
+def _mx4_gpu(t, name):
+    """The index of a tensor's device, which has to be the current GPU."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    if index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return index
+
+
+def _mx4_ptr(t, name, index, dtype, least, most=None):
+    """The address of a contiguous tensor of `dtype` on device `index` with `least` elements
+    or more (`most` at most)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.is_contiguous() and least <= t.numel()
+            and (most is None or t.numel() <= most)):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the first argument on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the first argument on cuda:{index}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
-    if least is not None and t.numel() < least:
-        raise ValueError(f"{name} must have at least {least} elements, got {t.numel()}")
+    raise ValueError(f"{name} must have {'at least ' if most is None else ''}{least} elements, "
+                     f"got {t.numel()}")
 
 
-def _mx4_float(t, name):
-    """The w2a8_mx4_type of a contiguous float tensor, and its device (the current one)."""
+def _mx4_type(t, name):
+    """The w2a8_mx4_type of a contiguous float tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     code = _MX4_TYPES.get(t.dtype)
@@ -652,32 +671,23 @@ def _mx4_float(t, name):
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return code, _mx4_device(t, name)
+    return code
 
 
-def _mx4_device(t, name):
-    """The device of a tensor, which has to be the current GPU."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    return t.device
-
-
-def _mx4_stream(stream, device):
+def _mx4_stream(stream, index):
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        return torch._C._cuda_getCurrentRawStream(index)   # current_stream(index).cuda_stream
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
     return stream.cuda_stream
 
 
-def _mx4_empty(shape, dtype, device, stream):
+def _mx4_empty(like, shape, dtype, stream):
     """Uninitialised memory that belongs to the stream of the call."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _mx4_rows(x, name):
@@ -692,154 +702,150 @@ def quant_act_mx4(x: torch.Tensor, x_q=None, x_s=None, stream=None):
     """x fp32, bf16 or fp16 [M, K] (or [K]: one row; device) -> (x_q uint8 [M, 64 * KT] codes,
     x_s uint8 [M, 16 * KU] scale bytes), the MX4R layout.  x_q and x_s may be given (any shape
     of at least mx4_act_bytes / mx4_scale_bytes elements)."""
-    code, dev = _mx4_float(x, "x")
+    code, dev = _mx4_type(x, "x"), _mx4_gpu(x, "x")
     M, K = _mx4_rows(x, "x")
     nq, ns = mx4_act_bytes(M, K), mx4_scale_bytes(M, K)
     if x_q is None:
-        x_q = _mx4_empty((M, nq // M), torch.uint8, dev, stream)
-    else:
-        _mx4_need(x_q, "x_q", dev, least=nq)
+        x_q = _mx4_empty(x, (M, nq // M), torch.uint8, stream)
     if x_s is None:
-        x_s = _mx4_empty((M, ns // M), torch.uint8, dev, stream)
-    else:
-        _mx4_need(x_s, "x_s", dev, least=ns)
-    _check(lib().quant_act_mx4(x.data_ptr(), code, M, K, x_q.data_ptr(), x_s.data_ptr(),
+        x_s = _mx4_empty(x, (M, ns // M), torch.uint8, stream)
+    _check(lib().quant_act_mx4(x.data_ptr(), code, M, K, _mx4_ptr(x_q, "x_q", dev, torch.uint8, nq),
+                               _mx4_ptr(x_s, "x_s", dev, torch.uint8, ns),
                                _mx4_stream(stream, dev)), "quant_act_mx4")
     return x_q, x_s
 
 
-def _mx4_act(x_q, x_s, M, K):
-    """The device of MX4R rows; M None: as many as x_q has (a 2-d tensor)."""
+def _mx4_count(x_q):
+    """The rows of a 2-d x_q."""
     if not isinstance(x_q, torch.Tensor):
         raise TypeError("x_q must be a torch.Tensor")
-    if M is None:
-        if x_q.dim() != 2:
-            raise ValueError("x_q must be [M, bytes of a row] where M is not given")
-        M = x_q.shape[0]
-    dev = _mx4_device(x_q, "x_q")
-    _mx4_need(x_q, "x_q", dev, least=mx4_act_bytes(M, K))
-    _mx4_need(x_s, "x_s", dev, least=mx4_scale_bytes(M, K))
-    return M, dev
+    if x_q.dim() != 2:
+        raise ValueError("x_q must be [M, bytes of a row] where M is not given")
+    return x_q.shape[0]
 
 
 def dequant_act_mx4(x_q, x_s, K: int, M=None, dtype=torch.float32, y=None, stream=None):
     """MX4R rows -> their values [M, K] in fp32, bf16 or fp16 (device).  M defaults to the
     rows of a 2-d x_q; y may be given (M * K elements of dtype)."""
-    M, dev = _mx4_act(x_q, x_s, M, K)
+    if M is None:
+        M = _mx4_count(x_q)
+    dev = _mx4_gpu(x_q, "x_q")
     code = _MX4_TYPES.get(dtype)
     if code is None:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    pq = _mx4_ptr(x_q, "x_q", dev, torch.uint8, mx4_act_bytes(M, K))
+    ps = _mx4_ptr(x_s, "x_s", dev, torch.uint8, mx4_scale_bytes(M, K))
     if y is None:
-        y = _mx4_empty((M, K), dtype, dev, stream)
-    else:
-        _mx4_need(y, "y", dev, dtype, numel=M * K)
-    _check(lib().dequant_act_mx4(x_q.data_ptr(), x_s.data_ptr(), M, K, y.data_ptr(), code,
+        y = _mx4_empty(x_q, (M, K), dtype, stream)
+    _check(lib().dequant_act_mx4(pq, ps, M, K, _mx4_ptr(y, "y", dev, dtype, M * K, M * K), code,
                                  _mx4_stream(stream, dev)), "dequant_act_mx4")
     return y
 
 
 def quant_pack_mx4(W: torch.Tensor, packed=None, stream=None) -> torch.Tensor:
     """Float weights [N, K] (device) -> packed MX4 weights uint8 [mx4_packed_bytes(N, K)]."""
-    code, dev = _mx4_float(W, "W")
+    code, dev = _mx4_type(W, "W"), _mx4_gpu(W, "W")
     if W.dim() != 2:
         raise ValueError("W must be [N, K]")
     N, K = W.shape
     nb = mx4_packed_bytes(N, K)
     if packed is None:
-        packed = _mx4_empty(nb, torch.uint8, dev, stream)
-    else:
-        _mx4_need(packed, "packed", dev, least=nb)
-    _check(lib().quant_pack_mx4(W.data_ptr(), code, N, K, packed.data_ptr(), packed.numel(),
+        packed = _mx4_empty(W, (nb,), torch.uint8, stream)
+    _check(lib().quant_pack_mx4(W.data_ptr(), code, N, K,
+                                _mx4_ptr(packed, "packed", dev, torch.uint8, nb), packed.numel(),
                                 _mx4_stream(stream, dev)), "quant_pack_mx4")
     return packed
 
 
 def _mx4_outputs(y_f32, y_bf16, dev, count):
-    for t, nm, dt in ((y_f32, "y_f32", torch.float32), (y_bf16, "y_bf16", torch.bfloat16)):
-        if t is not None:
-            _mx4_need(t, nm, dev, dt, numel=count)
-    return (None if y_f32 is None else y_f32.data_ptr(),
-            None if y_bf16 is None else y_bf16.data_ptr())
+    return (None if y_f32 is None else _mx4_ptr(y_f32, "y_f32", dev, torch.float32, count, count),
+            None if y_bf16 is None else _mx4_ptr(y_bf16, "y_bf16", dev, torch.bfloat16, count, count))
 
 
 def w4mx4_gemm(w_packed, x_q, x_s, M, N, K, y_f32=None, y_bf16=None, stream=None):
     """Raw C-ABI call: MX4 rows times MX4 weights (outputs must be given); returns nothing."""
-    M, dev = _mx4_act(x_q, x_s, M, K)
-    _mx4_need(w_packed, "w_packed", dev, least=mx4_packed_bytes(N, K))
+    dev, u8 = _mx4_gpu(x_q, "x_q"), torch.uint8
     yf, yb = _mx4_outputs(y_f32, y_bf16, dev, M * N)
-    _check(lib().w4mx4_gemm(w_packed.data_ptr(), x_q.data_ptr(), x_s.data_ptr(), M, N, K, yf, yb,
-                            _mx4_stream(stream, dev)), "w4mx4_gemm")
+    st = lib().w4mx4_gemm(_mx4_ptr(w_packed, "w_packed", dev, u8, mx4_packed_bytes(N, K)),
+                          _mx4_ptr(x_q, "x_q", dev, u8, mx4_act_bytes(M, K)),
+                          _mx4_ptr(x_s, "x_s", dev, u8, mx4_scale_bytes(M, K)), M, N, K, yf, yb,
+                          _mx4_stream(stream, dev))
+    if st:
+        raise W2A8Error(st, "w4mx4_gemm")
 
 
 def w2mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w=1.0, y_f32=None, y_bf16=None, stream=None):
     """Raw C-ABI call: MX4 rows times packed ternary weights; returns nothing."""
-    M, dev = _mx4_act(x_q, x_s, M, K)
-    _mx4_need(w_packed, "w_packed", dev, least=packed_bytes(N, K))
+    dev, u8 = _mx4_gpu(x_q, "x_q"), torch.uint8
     yf, yb = _mx4_outputs(y_f32, y_bf16, dev, M * N)
-    _check(lib().w2mx4_gemm(w_packed.data_ptr(), x_q.data_ptr(), x_s.data_ptr(), M, N, K, s_w, yf,
-                            yb, _mx4_stream(stream, dev)), "w2mx4_gemm")
+    st = lib().w2mx4_gemm(
+        _mx4_ptr(w_packed, "w_packed", dev, u8, _mx4_size("w2a8_packed_bytes", N, K)),
+        _mx4_ptr(x_q, "x_q", dev, u8, mx4_act_bytes(M, K)),
+        _mx4_ptr(x_s, "x_s", dev, u8, mx4_scale_bytes(M, K)), M, N, K, s_w, yf, yb,
+        _mx4_stream(stream, dev))
+    if st:
+        raise W2A8Error(st, "w2mx4_gemm")
 
 
 def w4mx4_linear_gemv(w_packed, x, N, K, y_f32=None, y_bf16=None, stream=None):
     """Raw C-ABI call: one float row, rounded to MX4 and multiplied in one launch."""
-    code, dev = _mx4_float(x, "x")
+    code, dev = _mx4_type(x, "x"), _mx4_gpu(x, "x")
     if x.numel() != K:
         raise ValueError("x must have K elements")
-    _mx4_need(w_packed, "w_packed", dev, least=mx4_packed_bytes(N, K))
     yf, yb = _mx4_outputs(y_f32, y_bf16, dev, N)
-    _check(lib().w4mx4_linear_gemv(w_packed.data_ptr(), x.data_ptr(), code, N, K, yf, yb,
-                                   _mx4_stream(stream, dev)), "w4mx4_linear_gemv")
+    st = lib().w4mx4_linear_gemv(
+        _mx4_ptr(w_packed, "w_packed", dev, torch.uint8, mx4_packed_bytes(N, K)), x.data_ptr(),
+        code, N, K, yf, yb, _mx4_stream(stream, dev))
+    if st:
+        raise W2A8Error(st, "w4mx4_linear_gemv")
 
 
 def w2mx4_linear_gemv(w_packed, x, N, K, s_w=1.0, y_f32=None, y_bf16=None, stream=None):
     """Raw C-ABI call: w4mx4_linear_gemv with packed ternary weights."""
-    code, dev = _mx4_float(x, "x")
+    code, dev = _mx4_type(x, "x"), _mx4_gpu(x, "x")
     if x.numel() != K:
         raise ValueError("x must have K elements")
-    _mx4_need(w_packed, "w_packed", dev, least=packed_bytes(N, K))
     yf, yb = _mx4_outputs(y_f32, y_bf16, dev, N)
-    _check(lib().w2mx4_linear_gemv(w_packed.data_ptr(), x.data_ptr(), code, N, K, s_w, yf, yb,
-                                   _mx4_stream(stream, dev)), "w2mx4_linear_gemv")
+    st = lib().w2mx4_linear_gemv(
+        _mx4_ptr(w_packed, "w_packed", dev, torch.uint8, _mx4_size("w2a8_packed_bytes", N, K)),
+        x.data_ptr(), code, N, K, s_w, yf, yb, _mx4_stream(stream, dev))
+    if st:
+        raise W2A8Error(st, "w2mx4_linear_gemv")
 
 
-def _mx4_out(dtype, shape, dev, stream):
-    """A new output and its place among the outputs of a raw call."""
+def _mx4_out(like, dtype, shape, stream):
+    """A new output, and (y_f32, y_bf16) of a raw call that writes it."""
     if dtype is torch.float32:
-        y = _mx4_empty(shape, dtype, dev, stream)
-        return y, {"y_f32": y}
+        y = _mx4_empty(like, shape, dtype, stream)
+        return y, y, None
     if dtype is torch.bfloat16:
-        y = _mx4_empty(shape, dtype, dev, stream)
-        return y, {"y_bf16": y}
+        y = _mx4_empty(like, shape, dtype, stream)
+        return y, None, y
     raise TypeError(f"out_dtype must be float32 or bfloat16, got {dtype}")
 
 
 def gemm_w4mx4(w_packed, x_q, x_s, N, K, out_dtype=torch.float32, stream=None):
     """MX4R rows (x_q [M, bytes of a row]) times MX4 weights -> fp32 or bf16 [M, N]."""
-    M, dev = _mx4_act(x_q, x_s, None, K)
-    y, out = _mx4_out(out_dtype, (M, N), dev, stream)
-    w4mx4_gemm(w_packed, x_q, x_s, M, N, K, stream=stream, **out)
+    M = _mx4_count(x_q)
+    y, yf, yb = _mx4_out(x_q, out_dtype, (M, N), stream)
+    w4mx4_gemm(w_packed, x_q, x_s, M, N, K, yf, yb, stream)
     return y
 
 
 def gemm_w2mx4(w_packed, x_q, x_s, s_w, N, K, out_dtype=torch.float32, stream=None):
     """MX4R rows (x_q [M, bytes of a row]) times ternary weights -> fp32 or bf16 [M, N]."""
-    M, dev = _mx4_act(x_q, x_s, None, K)
-    y, out = _mx4_out(out_dtype, (M, N), dev, stream)
-    w2mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w, stream=stream, **out)
+    M = _mx4_count(x_q)
+    y, yf, yb = _mx4_out(x_q, out_dtype, (M, N), stream)
+    w2mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w, yf, yb, stream)
     return y
 
 
-def _linear_mx4(x, N, K, out_dtype, stream, fused, gemv, gemm):
-    _, dev = _mx4_float(x, "x")
+def _mx4_layer_rows(x, K):
+    _mx4_type(x, "x")
     M, k = _mx4_rows(x, "x")
     if k != K:
         raise ValueError(f"x must have rows of {K} values, got {k}")
-    y, out = _mx4_out(out_dtype, (M, N), dev, stream)
-    if M == 1 and fused:
-        gemv(x, out)
-    else:
-        gemm(*quant_act_mx4(x, stream=stream), M, out)
-    return y
+    return M
 
 
 def linear_w4mx4(x, w_packed, N, K, out_dtype=torch.float32, stream=None, fused=True):
@@ -847,18 +853,26 @@ def linear_w4mx4(x, w_packed, N, K, out_dtype=torch.float32, stream=None, fused=
 
     M == 1 with fused=True: w4mx4_linear_gemv (one launch).  Otherwise quant_act_mx4, then
     w4mx4_gemm.  Both routes give bit-identical results."""
-    return _linear_mx4(
-        x, N, K, out_dtype, stream, fused,
-        lambda row, out: w4mx4_linear_gemv(w_packed, row, N, K, stream=stream, **out),
-        lambda q, s, M, out: w4mx4_gemm(w_packed, q, s, M, N, K, stream=stream, **out))
+    M = _mx4_layer_rows(x, K)
+    y, yf, yb = _mx4_out(x, out_dtype, (M, N), stream)
+    if M == 1 and fused:
+        w4mx4_linear_gemv(w_packed, x, N, K, yf, yb, stream)
+    else:
+        x_q, x_s = quant_act_mx4(x, stream=stream)
+        w4mx4_gemm(w_packed, x_q, x_s, M, N, K, yf, yb, stream)
+    return y
 
 
 def linear_w2mx4(x, w_packed, s_w, N, K, out_dtype=torch.float32, stream=None, fused=True):
     """Linear layer with packed ternary weights and MX4 activations (as linear_w4mx4)."""
-    return _linear_mx4(
-        x, N, K, out_dtype, stream, fused,
-        lambda row, out: w2mx4_linear_gemv(w_packed, row, N, K, s_w, stream=stream, **out),
-        lambda q, s, M, out: w2mx4_gemm(w_packed, q, s, M, N, K, s_w, stream=stream, **out))
+    M = _mx4_layer_rows(x, K)
+    y, yf, yb = _mx4_out(x, out_dtype, (M, N), stream)
+    if M == 1 and fused:
+        w2mx4_linear_gemv(w_packed, x, N, K, s_w, yf, yb, stream)
+    else:
+        x_q, x_s = quant_act_mx4(x, stream=stream)
+        w2mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w, yf, yb, stream)
+    return y
 
 
 # ---------------------------------------------------------------------------
