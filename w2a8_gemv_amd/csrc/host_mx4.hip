@@ -27,8 +27,17 @@ Place place(int64_t n, int64_t b, int64_t NS, int64_t KT, int64_t KU) {
             NS * KT * kMxTileBytes + (s * KU + t / kMxQuad) * 256 + 4 * l + t % kMxQuad};
 }
 
-hipError_t rows_launch(const Mx4Launch &a, const DeviceInfo &dev, hipStream_t stream) {
-    return launch_mx4_stream(a, dev.cus, stream);
+// Rows of activations up to which the weight stream serves a product.  It
+// reads every weight once, but every strip reads all rows: with many weight
+// rows to a CU the tiles of the other kernel share them.  Measured (MI355X,
+// us, stream and tiles): 13824 x 2560, M = 32: MX4 6.8 and 7.6, ternary 6.2
+// and 6.8; 55296 x 5120: MX4, M = 4, 16 and 32: 31.4 and 31.4, 34.9 and 30.1,
+// 44.4 and 30.8; ternary, M = 16 and 32: 16.4 and 17.7, 26.9 and 21.0; 5120 x
+// 27648 MX4, M = 17: 32.0 and 25.8.
+int stream_rows(const Mx4Launch &a, int cus) {
+    const bool ternary = !a.ws;
+    if (a.N >= 160 * int64_t(cus)) return ternary ? 16 : 4;
+    return !ternary && a.KU >= 40 ? 16 : kMx4StreamRows;
 }
 
 // Shared by the four product entry points.  x_type < 0: MX4R rows.
@@ -59,9 +68,11 @@ int product(const void *w, bool ternary, const uint8_t *xq, const uint8_t *xs, c
     a.M = int(M);
     a.N = int(N);
     a.K = int(K);
-    a.strips = 0;
+    a.strips = a.stages = 0;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = rows ? rows_launch(a, dev, s) : launch_mx4_fused(a, x_type, dev.cus, s);
+    const hipError_t e = !rows                             ? launch_mx4_fused(a, x_type, dev.cus, s)
+                         : M <= stream_rows(a, dev.cus) ? launch_mx4_stream(a, dev.cus, s)
+                                                        : launch_mx4_gemm(a, dev.cus, s);
     return e == hipSuccess ? W2A8_OK : W2A8_ERR_LAUNCH;
 }
 

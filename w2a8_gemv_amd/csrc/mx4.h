@@ -34,6 +34,13 @@ __device__ __forceinline__ v8i fp4_operand(v4u v) {
     return v8i{int(v[0]), int(v[1]), int(v[2]), int(v[3]), 0, 0, 0, 0};
 }
 
+// acc + a * b over one tile of 128 k; TILE picks the scale bytes.
+template <int TILE>
+__device__ __forceinline__ v4f mx4_mfma(v4u a, v4u b, v4f acc, uint32_t as, uint32_t bs) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(a), fp4_operand(b), acc, 4, 4,
+                                                            TILE, int(as), TILE, int(bs));
+}
+
 // The two T32x128 words of a ternary row's block of 32 values -> the block as
 // 4-bit floats of twice the weight, A4I order, to be used with the scale 2^-1.
 // A word's codes c = w + 1 sit at bits 8b + 2j: with the bits inverted, bit 0
@@ -90,12 +97,15 @@ __device__ __forceinline__ float mx4_load1(const void *p, int64_t i) {
         return float(static_cast<const _Float16 *>(p)[i]);
 }
 
-// fp32 -> bf16 bits, half to even; a NaN stays one.
-__device__ __forceinline__ uint32_t bf16_bits(float v) {
-    const uint32_t u = __float_as_uint(v);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
-    return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+// Two fp32 -> two bf16 in one word, half to even; a NaN stays one
+// (v_cvt_pk_bf16_f32: one instruction, where the integer form of the rounding
+// took as long as a third of a 256 x 256 x 5120 product's instructions).
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2bf));
 }
+__device__ __forceinline__ uint32_t bf16_bits(float v) { return bf16_pair(v, 0.0f) & 0xFFFFu; }
 
 // A product of MX4 rows (launch arguments by value).
 struct Mx4Launch {
@@ -108,24 +118,29 @@ struct Mx4Launch {
     uint16_t *y_bf16;
     float sw;
     int M, N, K, KT, KU;
-    int strips;            // row groups of the grid
+    int strips, stages;    // stream kernel: row groups of the grid, LDS stages of a wave
 };
 
-// Stores y[m][n..n+3] = v * sw where in range.
+// Result stores.  Rows of y start wherever N puts them, and global stores of
+// 16 bytes need no more than their elements' alignment.
+typedef v4f v4f_any __attribute__((aligned(4)));
+typedef v4u v4u_any __attribute__((aligned(2)));
+typedef v2u v2u_any __attribute__((aligned(2)));
+
+// y[m][n..n+3] = v * sw where in range.
 __device__ __forceinline__ void mx4_store4(const Mx4Launch &a, int m, int n, v4f v) {
     if (m >= a.M || n >= a.N) return;
     const int64_t at = int64_t(m) * a.N + n;
     v = v4f{v[0] * a.sw, v[1] * a.sw, v[2] * a.sw, v[3] * a.sw};
-    // N a multiple of 4: n + 3 < N, and rows keep the base's alignment.
-    if ((a.N & 3) == 0) {
-        if (a.y_f32) *reinterpret_cast<v4f *>(a.y_f32 + at) = v;
+    if (n + 3 < a.N) {
+        if (a.y_f32) *reinterpret_cast<v4f_any *>(a.y_f32 + at) = v;
         if (a.y_bf16)
-            *reinterpret_cast<v2u *>(a.y_bf16 + at) = v2u{bf16_bits(v[0]) | (bf16_bits(v[1]) << 16),
-                                                          bf16_bits(v[2]) | (bf16_bits(v[3]) << 16)};
+            *reinterpret_cast<v2u_any *>(a.y_bf16 + at) =
+                v2u{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
         return;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 3; ++e) {
         if (n + e >= a.N) break;
         if (a.y_f32) a.y_f32[at + e] = v[e];
         if (a.y_bf16) a.y_bf16[at + e] = uint16_t(bf16_bits(v[e]));
@@ -138,8 +153,13 @@ hipError_t launch_dequant_mx4(const uint8_t *xq, const uint8_t *xs, int64_t M, i
                               int type, hipStream_t stream);
 hipError_t launch_quant_pack_mx4(const void *W, int type, int64_t N, int K, uint8_t *packed,
                                  hipStream_t stream);
-// Weights streamed straight into registers (mx4_stream.hip), any M.
+// Weights streamed through LDS by single waves (mx4_stream.hip), M <= 32.
+constexpr int kMx4StreamRows = 32;
 hipError_t launch_mx4_stream(const Mx4Launch &a, int cus, hipStream_t stream);
+// Activations through LDS (mx4_gemm.hip), any M.
+hipError_t launch_mx4_gemm(const Mx4Launch &a, int cus, hipStream_t stream);
+// Its 256 x 256 form for MX4 weights (mx4_gemm_wide.hip), any M.
+hipError_t launch_mx4_gemm_wide(const Mx4Launch &a, hipStream_t stream);
 // One float row (x_type), rounded inside (M = 1).
 hipError_t launch_mx4_fused(const Mx4Launch &a, int x_type, int cus, hipStream_t stream);
 
