@@ -186,6 +186,14 @@ def assert_product(kind, M, N, K, seed, low=126, high=128, exact=True):
 
 
 KINDS = ["w4", "w2"]
+# one size for every output tile that the launch plans of 256 compute units
+# choose among (rows x columns over k-groups), and the largest over several
+# turns of the ring: 16 x 64 over 8, 32 x 64 over 4 (MX4) and 32 x 256
+# (ternary), 64 x 64 and 32 x 128 over 4, 64 x 128 over 2, 32 x 256 (MX4), 64 x
+# 256, 128 x 256, 256 x 256 (MX4) and 128 x 256 (ternary)
+PLANS = [(74, 102, 2064), (36, 100, 130), (64, 100, 514), (2100, 235, 1048), (2052, 196, 523),
+         (2084, 213, 137), (2083, 863, 132), (2105, 962, 132), (2071, 1812, 132), (2008, 6186, 133),
+         (1967, 6454, 1100)]
 # every edge of rows, columns and k: blocks of 32, tiles of 128, groups of 512
 SMALL = [(1, 1, 1), (1, 16, 31), (2, 17, 32), (1, 33, 33), (3, 15, 127), (16, 16, 128), (17, 32, 129),
          (31, 100, 257), (33, 7, 384), (16, 48, 511), (1, 64, 512), (5, 65, 513), (64, 33, 640),
@@ -198,7 +206,7 @@ LARGE = [(1, 2560, 2560), (1, 5120, 6912), (1, 3000, 13825), (8, 2560, 2560), (1
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("M,N,K", SMALL + LARGE)
+@pytest.mark.parametrize("M,N,K", SMALL + LARGE + PLANS)
 def test_product_is_exact(M, N, K, kind):
     assert_product(kind, M, N, K, seed=M + 3 * N + 5 * K)
 

@@ -629,8 +629,17 @@ def unpack_mx4(packed: torch.Tensor, N: int, K: int):
     return codes, scales
 
 
-# The calls below cost the host about as much as their kernels take at one
-# row, so each argument is checked once and by one expression.
+# At one row the calls below cost the host more than their kernels take, so
+# each argument is checked once and by one expression, sizes are remembered,
+# and outputs made here are not checked again (8.1 us a product call before,
+# 3.8 of them ctypes, launch and kernel).
+@functools.lru_cache(maxsize=4096)
+def _mx4_sizes(M, N, K, ternary):
+    """Bytes of the rows' codes and scales and of the weights of a product."""
+    return (mx4_act_bytes(M, K), mx4_scale_bytes(M, K),
+            _mx4_size("w2a8_packed_bytes" if ternary else "mx4_packed_bytes", N, K))
+
+
 def _mx4_gpu(t, name):
     """The index of a tensor's device, which has to be the current GPU."""
     if not isinstance(t, torch.Tensor):
@@ -638,7 +647,7 @@ def _mx4_gpu(t, name):
     index = t.get_device()
     if index < 0:
         raise ValueError(f"{name} must be a device tensor")
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():               # torch.cuda.current_device()
         raise ValueError(f"{name} is on {t.device}, which is not the current device")
     return index
 
@@ -646,11 +655,11 @@ def _mx4_gpu(t, name):
 def _mx4_ptr(t, name, index, dtype, least, most=None):
     """The address of a contiguous tensor of `dtype` on device `index` with `least` elements
     or more (`most` at most)."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
-            and t.is_contiguous() and least <= t.numel()
-            and (most is None or t.numel() <= most)):
-        return t.data_ptr()
-    if not isinstance(t, torch.Tensor):
+    if isinstance(t, torch.Tensor):
+        if (t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+                and least <= t.numel() and (most is None or t.numel() <= most)):
+            return t.data_ptr()
+    else:
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -685,9 +694,9 @@ def _mx4_stream(stream, index):
 def _mx4_empty(like, shape, dtype, stream):
     """Uninitialised memory that belongs to the stream of the call."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _mx4_rows(x, name):
@@ -707,11 +716,17 @@ def quant_act_mx4(x: torch.Tensor, x_q=None, x_s=None, stream=None):
     nq, ns = mx4_act_bytes(M, K), mx4_scale_bytes(M, K)
     if x_q is None:
         x_q = _mx4_empty(x, (M, nq // M), torch.uint8, stream)
+        pq = x_q.data_ptr()
+    else:
+        pq = _mx4_ptr(x_q, "x_q", dev, torch.uint8, nq)
     if x_s is None:
         x_s = _mx4_empty(x, (M, ns // M), torch.uint8, stream)
-    _check(lib().quant_act_mx4(x.data_ptr(), code, M, K, _mx4_ptr(x_q, "x_q", dev, torch.uint8, nq),
-                               _mx4_ptr(x_s, "x_s", dev, torch.uint8, ns),
-                               _mx4_stream(stream, dev)), "quant_act_mx4")
+        ps = x_s.data_ptr()
+    else:
+        ps = _mx4_ptr(x_s, "x_s", dev, torch.uint8, ns)
+    st = lib().quant_act_mx4(x.data_ptr(), code, M, K, pq, ps, _mx4_stream(stream, dev))
+    if st:
+        raise W2A8Error(st, "quant_act_mx4")
     return x_q, x_s
 
 
@@ -737,8 +752,12 @@ def dequant_act_mx4(x_q, x_s, K: int, M=None, dtype=torch.float32, y=None, strea
     ps = _mx4_ptr(x_s, "x_s", dev, torch.uint8, mx4_scale_bytes(M, K))
     if y is None:
         y = _mx4_empty(x_q, (M, K), dtype, stream)
-    _check(lib().dequant_act_mx4(pq, ps, M, K, _mx4_ptr(y, "y", dev, dtype, M * K, M * K), code,
-                                 _mx4_stream(stream, dev)), "dequant_act_mx4")
+        py = y.data_ptr()
+    else:
+        py = _mx4_ptr(y, "y", dev, dtype, M * K, M * K)
+    st = lib().dequant_act_mx4(pq, ps, M, K, py, code, _mx4_stream(stream, dev))
+    if st:
+        raise W2A8Error(st, "dequant_act_mx4")
     return y
 
 
@@ -762,29 +781,52 @@ def _mx4_outputs(y_f32, y_bf16, dev, count):
             None if y_bf16 is None else _mx4_ptr(y_bf16, "y_bf16", dev, torch.bfloat16, count, count))
 
 
+def _mx4_new(like, dtype, shape, stream):
+    """A new output and its two addresses (y_f32, y_bf16), one of them None."""
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise TypeError(f"out_dtype must be float32 or bfloat16, got {dtype}")
+    y = _mx4_empty(like, shape, dtype, stream)
+    return (y, y.data_ptr(), None) if dtype is torch.float32 else (y, None, y.data_ptr())
+
+
+def _mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w, yf, yb, dev, stream):
+    """A product (s_w None: MX4 weights) into the addresses yf and yb."""
+    na, ns, nw = _mx4_sizes(M, N, K, s_w is not None)
+    pw = _mx4_ptr(w_packed, "w_packed", dev, torch.uint8, nw)
+    pq = _mx4_ptr(x_q, "x_q", dev, torch.uint8, na)
+    ps = _mx4_ptr(x_s, "x_s", dev, torch.uint8, ns)
+    if s_w is None:
+        st = lib().w4mx4_gemm(pw, pq, ps, M, N, K, yf, yb, _mx4_stream(stream, dev))
+    else:
+        st = lib().w2mx4_gemm(pw, pq, ps, M, N, K, s_w, yf, yb, _mx4_stream(stream, dev))
+    if st:
+        raise W2A8Error(st, "w4mx4_gemm" if s_w is None else "w2mx4_gemm")
+
+
+def _mx4_gemv(w_packed, x, code, N, K, s_w, yf, yb, dev, stream):
+    """A one-launch layer (s_w None: MX4 weights) into the addresses yf and yb."""
+    pw = _mx4_ptr(w_packed, "w_packed", dev, torch.uint8, _mx4_sizes(1, N, K, s_w is not None)[2])
+    if s_w is None:
+        st = lib().w4mx4_linear_gemv(pw, x.data_ptr(), code, N, K, yf, yb, _mx4_stream(stream, dev))
+    else:
+        st = lib().w2mx4_linear_gemv(pw, x.data_ptr(), code, N, K, s_w, yf, yb,
+                                     _mx4_stream(stream, dev))
+    if st:
+        raise W2A8Error(st, "w4mx4_linear_gemv" if s_w is None else "w2mx4_linear_gemv")
+
+
 def w4mx4_gemm(w_packed, x_q, x_s, M, N, K, y_f32=None, y_bf16=None, stream=None):
     """Raw C-ABI call: MX4 rows times MX4 weights (outputs must be given); returns nothing."""
-    dev, u8 = _mx4_gpu(x_q, "x_q"), torch.uint8
+    dev = _mx4_gpu(x_q, "x_q")
     yf, yb = _mx4_outputs(y_f32, y_bf16, dev, M * N)
-    st = lib().w4mx4_gemm(_mx4_ptr(w_packed, "w_packed", dev, u8, mx4_packed_bytes(N, K)),
-                          _mx4_ptr(x_q, "x_q", dev, u8, mx4_act_bytes(M, K)),
-                          _mx4_ptr(x_s, "x_s", dev, u8, mx4_scale_bytes(M, K)), M, N, K, yf, yb,
-                          _mx4_stream(stream, dev))
-    if st:
-        raise W2A8Error(st, "w4mx4_gemm")
+    _mx4_gemm(w_packed, x_q, x_s, M, N, K, None, yf, yb, dev, stream)
 
 
 def w2mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w=1.0, y_f32=None, y_bf16=None, stream=None):
     """Raw C-ABI call: MX4 rows times packed ternary weights; returns nothing."""
-    dev, u8 = _mx4_gpu(x_q, "x_q"), torch.uint8
+    dev = _mx4_gpu(x_q, "x_q")
     yf, yb = _mx4_outputs(y_f32, y_bf16, dev, M * N)
-    st = lib().w2mx4_gemm(
-        _mx4_ptr(w_packed, "w_packed", dev, u8, _mx4_size("w2a8_packed_bytes", N, K)),
-        _mx4_ptr(x_q, "x_q", dev, u8, mx4_act_bytes(M, K)),
-        _mx4_ptr(x_s, "x_s", dev, u8, mx4_scale_bytes(M, K)), M, N, K, s_w, yf, yb,
-        _mx4_stream(stream, dev))
-    if st:
-        raise W2A8Error(st, "w2mx4_gemm")
+    _mx4_gemm(w_packed, x_q, x_s, M, N, K, float(s_w), yf, yb, dev, stream)
 
 
 def w4mx4_linear_gemv(w_packed, x, N, K, y_f32=None, y_bf16=None, stream=None):
@@ -793,11 +835,7 @@ def w4mx4_linear_gemv(w_packed, x, N, K, y_f32=None, y_bf16=None, stream=None):
     if x.numel() != K:
         raise ValueError("x must have K elements")
     yf, yb = _mx4_outputs(y_f32, y_bf16, dev, N)
-    st = lib().w4mx4_linear_gemv(
-        _mx4_ptr(w_packed, "w_packed", dev, torch.uint8, mx4_packed_bytes(N, K)), x.data_ptr(),
-        code, N, K, yf, yb, _mx4_stream(stream, dev))
-    if st:
-        raise W2A8Error(st, "w4mx4_linear_gemv")
+    _mx4_gemv(w_packed, x, code, N, K, None, yf, yb, dev, stream)
 
 
 def w2mx4_linear_gemv(w_packed, x, N, K, s_w=1.0, y_f32=None, y_bf16=None, stream=None):
@@ -806,46 +844,37 @@ def w2mx4_linear_gemv(w_packed, x, N, K, s_w=1.0, y_f32=None, y_bf16=None, strea
     if x.numel() != K:
         raise ValueError("x must have K elements")
     yf, yb = _mx4_outputs(y_f32, y_bf16, dev, N)
-    st = lib().w2mx4_linear_gemv(
-        _mx4_ptr(w_packed, "w_packed", dev, torch.uint8, _mx4_size("w2a8_packed_bytes", N, K)),
-        x.data_ptr(), code, N, K, s_w, yf, yb, _mx4_stream(stream, dev))
-    if st:
-        raise W2A8Error(st, "w2mx4_linear_gemv")
-
-
-def _mx4_out(like, dtype, shape, stream):
-    """A new output, and (y_f32, y_bf16) of a raw call that writes it."""
-    if dtype is torch.float32:
-        y = _mx4_empty(like, shape, dtype, stream)
-        return y, y, None
-    if dtype is torch.bfloat16:
-        y = _mx4_empty(like, shape, dtype, stream)
-        return y, None, y
-    raise TypeError(f"out_dtype must be float32 or bfloat16, got {dtype}")
+    _mx4_gemv(w_packed, x, code, N, K, float(s_w), yf, yb, dev, stream)
 
 
 def gemm_w4mx4(w_packed, x_q, x_s, N, K, out_dtype=torch.float32, stream=None):
     """MX4R rows (x_q [M, bytes of a row]) times MX4 weights -> fp32 or bf16 [M, N]."""
-    M = _mx4_count(x_q)
-    y, yf, yb = _mx4_out(x_q, out_dtype, (M, N), stream)
-    w4mx4_gemm(w_packed, x_q, x_s, M, N, K, yf, yb, stream)
+    M, dev = _mx4_count(x_q), _mx4_gpu(x_q, "x_q")
+    y, yf, yb = _mx4_new(x_q, out_dtype, (M, N), stream)
+    _mx4_gemm(w_packed, x_q, x_s, M, N, K, None, yf, yb, dev, stream)
     return y
 
 
 def gemm_w2mx4(w_packed, x_q, x_s, s_w, N, K, out_dtype=torch.float32, stream=None):
     """MX4R rows (x_q [M, bytes of a row]) times ternary weights -> fp32 or bf16 [M, N]."""
-    M = _mx4_count(x_q)
-    y, yf, yb = _mx4_out(x_q, out_dtype, (M, N), stream)
-    w2mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w, yf, yb, stream)
+    M, dev = _mx4_count(x_q), _mx4_gpu(x_q, "x_q")
+    y, yf, yb = _mx4_new(x_q, out_dtype, (M, N), stream)
+    _mx4_gemm(w_packed, x_q, x_s, M, N, K, float(s_w), yf, yb, dev, stream)
     return y
 
 
-def _mx4_layer_rows(x, K):
-    _mx4_type(x, "x")
+def _mx4_linear(x, w_packed, s_w, N, K, out_dtype, stream, fused):
+    code, dev = _mx4_type(x, "x"), _mx4_gpu(x, "x")
     M, k = _mx4_rows(x, "x")
     if k != K:
         raise ValueError(f"x must have rows of {K} values, got {k}")
-    return M
+    y, yf, yb = _mx4_new(x, out_dtype, (M, N), stream)
+    if M == 1 and fused:
+        _mx4_gemv(w_packed, x, code, N, K, s_w, yf, yb, dev, stream)
+    else:
+        x_q, x_s = quant_act_mx4(x, stream=stream)
+        _mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w, yf, yb, dev, stream)
+    return y
 
 
 def linear_w4mx4(x, w_packed, N, K, out_dtype=torch.float32, stream=None, fused=True):
@@ -853,26 +882,12 @@ def linear_w4mx4(x, w_packed, N, K, out_dtype=torch.float32, stream=None, fused=
 
     M == 1 with fused=True: w4mx4_linear_gemv (one launch).  Otherwise quant_act_mx4, then
     w4mx4_gemm.  Both routes give bit-identical results."""
-    M = _mx4_layer_rows(x, K)
-    y, yf, yb = _mx4_out(x, out_dtype, (M, N), stream)
-    if M == 1 and fused:
-        w4mx4_linear_gemv(w_packed, x, N, K, yf, yb, stream)
-    else:
-        x_q, x_s = quant_act_mx4(x, stream=stream)
-        w4mx4_gemm(w_packed, x_q, x_s, M, N, K, yf, yb, stream)
-    return y
+    return _mx4_linear(x, w_packed, None, N, K, out_dtype, stream, fused)
 
 
 def linear_w2mx4(x, w_packed, s_w, N, K, out_dtype=torch.float32, stream=None, fused=True):
     """Linear layer with packed ternary weights and MX4 activations (as linear_w4mx4)."""
-    M = _mx4_layer_rows(x, K)
-    y, yf, yb = _mx4_out(x, out_dtype, (M, N), stream)
-    if M == 1 and fused:
-        w2mx4_linear_gemv(w_packed, x, N, K, s_w, yf, yb, stream)
-    else:
-        x_q, x_s = quant_act_mx4(x, stream=stream)
-        w2mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w, yf, yb, stream)
-    return y
+    return _mx4_linear(x, w_packed, float(s_w), N, K, out_dtype, stream, fused)
 
 
 # ---------------------------------------------------------------------------
