@@ -5,7 +5,9 @@
  * keeps state between calls, so any number of calls may be in flight on any
  * streams, and all may be recorded into HIP graphs (kernels only).  Results
  * do not depend on timing: every sum has a fixed order, which depends on the
- * shape and the device alone.
+ * shape and the device alone.  An output of a device entry point must not
+ * share bytes with another buffer of the call (W2A8_ERR_VALUE): the kernels
+ * write results while others of their workgroups still read.
  *
  * The format is the MXFP4 of the OCP Microscaling Formats specification
  * (version 1.0): 4-bit floats of 1 sign, 2 exponent and 1 mantissa bits
@@ -73,8 +75,9 @@ int quant_act_mx4(const void *x, int x_type, int64_t M, int64_t K, uint8_t *x_q,
                   void *stream);
 
 /* Device: the values of MX4R rows as floats, y: [M][K] of y_type, 16-byte
- * aligned.  Exact in fp32 and bf16 (but for results below their smallest
- * normal number), rounded half to even in fp16 (beyond 65504: infinity). */
+ * aligned.  Exact in fp32 and bf16, rounded half to even in fp16; magnitudes
+ * past the type's range (65504 for fp16, some of scale bytes 253 and 254 for
+ * the others) become infinity. */
 int dequant_act_mx4(const uint8_t *x_q, const uint8_t *x_s, int64_t M, int64_t K, void *y,
                     int y_type, void *stream);
 

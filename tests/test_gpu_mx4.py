@@ -13,6 +13,8 @@ multiplied in once; each of these rounds or cuts off at most one unit 2^-23 of
 a magnitude that the sum of magnitudes S bounds, so |error| <= (4 KT + 9) *
 2^-23 * S.  A bf16 output is the fp32 one rounded half to even: equal bits.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -273,6 +275,26 @@ def test_one_output_and_outputs_of_both(kind):
     assert torch.equal(f, yf) and torch.equal(b, yb)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M,N,K", PLANS + [(1, 40, 300), (9, 90, 700), (29, 1000, 300)])
+def test_each_output_alone_equals_both(M, N, K, kind):
+    """A product into one of its outputs, at every output tile, from rows in a
+    buffer made for more of them."""
+    c, s = mx_rows(M + 3, K, 5)
+    q, sc = on_device(c, s)
+    wp, _ = weights(kind, N, K, 6)
+    yf, yb = gemm(kind, wp, q, sc, M, N, K)
+    f = torch.full((M, N), 77.0, device=dev())
+    b = torch.full((M, N), 77.0, device=dev(), dtype=torch.bfloat16)
+    for out in ({"y_f32": f}, {"y_bf16": b}):
+        if kind == "w4":
+            w2a8.w4mx4_gemm(wp, q, sc, M, N, K, **out)
+        else:
+            w2a8.w2mx4_gemm(wp, q, sc, M, N, K, 1.0, **out)
+    torch.cuda.synchronize()
+    assert torch.equal(f, yf) and torch.equal(b, yb)
+
+
 # ---------------------------------------------------------------------------
 # whole layers
 # ---------------------------------------------------------------------------
@@ -395,6 +417,49 @@ def test_calls_on_several_streams_at_once(kind):
     torch.cuda.synchronize()
     for i, y in enumerate(got):
         assert torch.equal(y, want[i % 4])
+
+
+def test_calls_from_several_host_threads():
+    """Threads with streams of their own, each over all operators."""
+    N, K = 300, 1000
+    packed = {kind: weights(kind, N, K, 40)[0] for kind in KINDS}
+    xs = [float_rows(M, K, 50 + M, torch.bfloat16)[0].to(dev()) for M in (1, 7, 50, 130)]
+    want = [[layer(kind, x, packed[kind], N, K) for kind in KINDS] + [w2a8.quant_act_mx4(x)] for x in xs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        st = torch.cuda.Stream()
+        for _ in range(20):
+            got = [layer(kind, xs[i], packed[kind], N, K, stream=st) for kind in KINDS]
+            q, s = w2a8.quant_act_mx4(xs[i], stream=st)
+            st.synchronize()
+            same = [torch.equal(a, b) for a, b in zip(got + [q, s], want[i][:2] + list(want[i][2]))]
+            if not all(same):
+                wrong.append((i, same))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_outputs_over_inputs_are_refused():
+    x = torch.ones((1, 64), device=dev())
+    wp = w2a8.quant_pack_mx4(torch.ones((64, 64), device=dev()))
+    wt = packed_on_device(np.ones((64, 64), np.int8))
+    with pytest.raises(w2a8.W2A8Error):
+        w2a8.w4mx4_linear_gemv(wp, x, 64, 64, y_f32=x)
+    with pytest.raises(w2a8.W2A8Error):
+        w2a8.w2mx4_linear_gemv(wt, x, 64, 64, y_f32=x)
+    q, s = w2a8.quant_act_mx4(x)
+    with pytest.raises(w2a8.W2A8Error):
+        w2a8.dequant_act_mx4(q, s, 16, 1, y=q.view(torch.float32).view(-1)[:16])
+    with pytest.raises(w2a8.W2A8Error):
+        w2a8.quant_act_mx4(x, x.view(torch.uint8))
+    torch.cuda.synchronize()
+    assert bool((x == 1).all())
 
 
 def test_device_refusals():

@@ -151,6 +151,47 @@ def test_products_refuse(kind):
     assert v(t=-1) == VALUE and v(t=3) == VALUE
 
 
+def test_outputs_that_share_bytes_with_another_buffer_are_refused():
+    """Each output against each other buffer of its call: over its first and
+    its last 16 bytes."""
+    L = w2a8.lib()
+    M, N, K = 3, 40, 200
+    at = {}
+
+    def placed(sizes, out, other):
+        """Buffers far apart, but `out` begins in the last 16 bytes of `other`."""
+        for i, n in enumerate(sizes):
+            at[n] = 0x1000000 * (i + 1)
+        first = dict(at, **{out: at[other] + (sizes[other] - 1) // 16 * 16})
+        last = dict(at, **{other: at[out] + (sizes[out] - 1) // 16 * 16})
+        return first, last
+
+    nq, ns = w2a8.mx4_act_bytes(M, K), w2a8.mx4_scale_bytes(M, K)
+    for t, e in ((0, 4), (1, 2), (2, 2)):
+        rows = {"x": M * K * e, "q": nq, "s": ns}
+        for out, other in (("q", "x"), ("s", "x"), ("q", "s")):
+            for b in placed(rows, out, other):
+                assert L.quant_act_mx4(b["x"], t, M, K, b["q"], b["s"], None) == VALUE
+        for other in "qs":
+            for b in placed(rows, "x", other):
+                assert L.dequant_act_mx4(b["q"], b["s"], M, K, b["x"], t, None) == VALUE
+        nb = w2a8.mx4_packed_bytes(N, K)
+        for b in placed({"W": N * K * e, "p": nb}, "p", "W"):
+            assert L.quant_pack_mx4(b["W"], t, N, K, b["p"], nb, None) == VALUE
+    for kind, nw in (("w4mx4", w2a8.mx4_packed_bytes(N, K)), ("w2mx4", w2a8.packed_bytes(N, K))):
+        sw = (F(1.0),) if kind == "w2mx4" else ()
+        sizes = {"w": nw, "q": nq, "s": ns, "f": M * N * 4, "b": M * N * 2}
+        for out, other in (("f", "w"), ("f", "q"), ("f", "s"), ("b", "w"), ("b", "q"), ("b", "s"), ("f", "b")):
+            for b in placed(sizes, out, other):
+                assert getattr(L, kind + "_gemm")(b["w"], b["q"], b["s"], M, N, K, *sw, b["f"], b["b"],
+                                                  None) == VALUE
+        sizes = {"w": nw, "x": K * 4, "f": N * 4, "b": N * 2}
+        for out, other in (("f", "w"), ("f", "x"), ("b", "w"), ("b", "x"), ("f", "b")):
+            for b in placed(sizes, out, other):
+                assert getattr(L, kind + "_linear_gemv")(b["w"], b["x"], 0, N, K, *sw, b["f"], b["b"],
+                                                         None) == VALUE
+
+
 def test_binding_refuses_host_tensors_and_wrong_types():
     x = torch.zeros((2, 64), dtype=torch.bfloat16)
     u8 = torch.zeros(4096, dtype=torch.uint8)

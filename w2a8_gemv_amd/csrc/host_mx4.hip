@@ -13,6 +13,14 @@ bool rows_ok(int64_t M, int64_t K) { return M >= 1 && M <= kMaxM && K >= 1 && K 
 bool matrix_ok(int64_t N, int64_t K) { return N >= 1 && N <= kMaxN && K >= 1 && K <= W2A8_MAX_K; }
 bool type_ok(int t) { return t == W2A8_F32 || t == W2A8_BF16 || t == W2A8_F16; }
 
+// Do two buffers share bytes?  A kernel reads what others of its workgroups
+// have written by then, so outputs have to be apart from all other buffers.
+bool meet(const void *a, int64_t na, const void *b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + uint64_t(nb) && y < x + uint64_t(na);
+}
+int64_t type_bytes(int type) { return type == W2A8_F32 ? 4 : 2; }
+
 // Byte and half of value i (0..31) of a block's 16 code bytes.
 int code_byte(int i) { return (i / 16) * 8 + (i % 16 / 4 % 2) * 4 + i % 4; }
 int code_shift(int i) { return i % 16 >= 8 ? 4 : 0; }
@@ -51,6 +59,16 @@ int product(const void *w, bool ternary, const uint8_t *xq, const uint8_t *xs, c
     if (!aligned16(w) || !aligned16(xq) || !aligned16(xs) || !aligned16(x) || !aligned16(y_f32) ||
         !aligned16(y_bf16))
         return W2A8_ERR_ALIGN;
+    const int64_t nw = ternary ? ceil_div(N, kTileRows) * mx4_tiles(K) * 1024 : mx4_packed_bytes(N, K);
+    const int64_t nq = M * mx4_tiles(K) * kMxRowTile, ns = M * mx4_quads(K) * 16;
+    const int64_t nx = rows ? 0 : K * type_bytes(x_type);
+    const auto clear = [&](const void *y, int64_t ny) {
+        return !meet(y, ny, w, nw) && !meet(y, ny, xq, nq) && !meet(y, ny, xs, ns) &&
+               !meet(y, ny, x, nx);
+    };
+    if (!clear(y_f32, M * N * 4) || !clear(y_bf16, M * N * 2) ||
+        meet(y_f32, M * N * 4, y_bf16, M * N * 2))
+        return W2A8_ERR_VALUE;
     DeviceInfo dev;
     const int st = current_device(&dev);
     if (st != W2A8_OK) return st;
@@ -146,6 +164,8 @@ int quant_act_mx4(const void *x, int x_type, int64_t M, int64_t K, uint8_t *x_q,
     if (!rows_ok(M, K)) return W2A8_ERR_SHAPE;
     if (!type_ok(x_type)) return W2A8_ERR_VALUE;
     if (!aligned16(x) || !aligned16(x_q) || !aligned16(x_s)) return W2A8_ERR_ALIGN;
+    const int64_t nx = M * K * type_bytes(x_type), nq = mx4_act_bytes(M, K), ns = mx4_scale_bytes(M, K);
+    if (meet(x, nx, x_q, nq) || meet(x, nx, x_s, ns) || meet(x_q, nq, x_s, ns)) return W2A8_ERR_VALUE;
     DeviceInfo dev;
     const int st = current_device(&dev);
     if (st != W2A8_OK) return st;
@@ -160,6 +180,9 @@ int dequant_act_mx4(const uint8_t *x_q, const uint8_t *x_s, int64_t M, int64_t K
     if (!rows_ok(M, K)) return W2A8_ERR_SHAPE;
     if (!type_ok(y_type)) return W2A8_ERR_VALUE;
     if (!aligned16(x_q) || !aligned16(x_s) || !aligned16(y)) return W2A8_ERR_ALIGN;
+    const int64_t ny = M * K * type_bytes(y_type);
+    if (meet(y, ny, x_q, mx4_act_bytes(M, K)) || meet(y, ny, x_s, mx4_scale_bytes(M, K)))
+        return W2A8_ERR_VALUE;
     DeviceInfo dev;
     const int st = current_device(&dev);
     if (st != W2A8_OK) return st;
@@ -176,6 +199,7 @@ int quant_pack_mx4(const void *W, int w_type, int64_t N, int64_t K, void *w_pack
     if (!type_ok(w_type)) return W2A8_ERR_VALUE;
     if (!aligned16(W) || !aligned16(w_packed)) return W2A8_ERR_ALIGN;
     if (packed_bytes < need) return W2A8_ERR_BUFSIZE;
+    if (meet(W, N * K * type_bytes(w_type), w_packed, need)) return W2A8_ERR_VALUE;
     DeviceInfo dev;
     const int st = current_device(&dev);
     if (st != W2A8_OK) return st;

@@ -26,7 +26,6 @@ inline int64_t mx4_quads(int64_t K) { return ceil_div(mx4_tiles(K), kMxQuad); }
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
-typedef float v16f __attribute__((ext_vector_type(16)));
 
 // Operand register block of a scaled MFMA on 4-bit floats: the instruction
 // reads the first four registers.
@@ -83,10 +82,7 @@ __device__ __forceinline__ uint32_t mx4_codes4(const float (&lo)[4], const float
     return scale == scale ? w : 0u;
 }
 
-// Four consecutive values of a float row as fp32; TYPE is a w2a8_mx4_type.
-// p: the row, k a multiple of 4.  ALIGNED: the four are in the row and at an
-// aligned address.  Otherwise values at k >= K are 0 and the row may start
-// anywhere its type allows.
+// Value i of a float row as fp32; TYPE is a w2a8_mx4_type.
 template <int TYPE>
 __device__ __forceinline__ float mx4_load1(const void *p, int64_t i) {
     if constexpr (TYPE == W2A8_F32)

@@ -133,7 +133,7 @@ __device__ __forceinline__ void mx4_store_bf16(const Mx4Launch &a, int m, int n,
 // bytes a lane (at any alignment of the rows; single elements where a lane's
 // columns pass the row's end).  The stores of a wave are whole lines that are
 // not read again here: non-temporal (8192 x 13824 bf16: 325 against 346 us for
-// the product).  Loops, not unrolled: the code runs once for every 16 rows.
+// the product).
 template <int COLS, bool SWIZZLE>
 __device__ __forceinline__ void mx4_store_rows(const Mx4Launch &a, const uint8_t *lds, int mb, int n0,
                                                int lane) {
