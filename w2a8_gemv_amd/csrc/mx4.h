@@ -47,9 +47,12 @@ __device__ __forceinline__ v4f mx4_mfma(v4u a, v4u b, v4f acc, uint32_t as, uint
 // bits 2 and 3 of a nibble is 2.0, -2.0 or -0.  The codes at bits 8b and
 // 8b + 4 are values b and 8 + b of the chunk, those at 8b + 2 and 8b + 6
 // values 4 + b and 12 + b.
+// (Truth table 0x0C: not the first and the second operand.)
+__device__ __forceinline__ uint32_t ternary_word(uint32_t w) {
+    return __builtin_amdgcn_bitop3_b32(int(w), int(0xCCCCCCCCu), 0, 0x0C);
+}
 __device__ __forceinline__ v4u ternary_fp4(uint32_t w0, uint32_t w1) {
-    return v4u{~(w0 << 2) & 0xCCCCCCCCu, ~w0 & 0xCCCCCCCCu, ~(w1 << 2) & 0xCCCCCCCCu,
-               ~w1 & 0xCCCCCCCCu};
+    return v4u{ternary_word(w0 << 2), ternary_word(w0), ternary_word(w1 << 2), ternary_word(w1)};
 }
 constexpr uint32_t kTernaryScale = 0x7E7E7E7Eu;   // 2^-1 in every byte
 

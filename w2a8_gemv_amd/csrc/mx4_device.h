@@ -64,9 +64,9 @@ __device__ __forceinline__ void mx4_wait_lds() {
     __asm__ volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 }
-// ... and all waves are here (what their waits covered is then visible).
+// All waves are here (what they waited for before is then visible).
 __device__ __forceinline__ void mx4_barrier() {
-    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __asm__ volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     __asm__ volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);

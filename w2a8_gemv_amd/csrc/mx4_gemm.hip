@@ -28,7 +28,12 @@
 //    a time, the operand reads of the blocks after them (at the end those of
 //    the next tile, so that no wave waits for LDS behind the barrier) and the
 //    loads of later tiles: issued together, the loads of all waves would hold
-//    up every wave's instructions.
+//    up every wave's instructions.  The barrier waits for no LDS read: what a
+//    stage held has been used before the barrier ahead of its next load.
+//  * Ternary words become 4-bit floats between the instructions, one weight
+//    block ahead of its use (for all blocks at the start of a tile they kept the
+//    matrix pipe waiting: a tile of 64 x 128 over two groups 0.29 us, now
+//    0.22, operands in the L2; 1024 x 2560 x 6912 20.2 us, now 18.6).
 //  * KS > 1 (grids smaller than the device): the groups take the quads of
 //    tiles in turn and add up through LDS at the end, in group order.
 //  * Results pass through LDS, 16 rows x 64 columns at a time, so that the
@@ -139,9 +144,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS, (Tile<KIND, WM, WN, MB, KS>::EU)
         for (int j = 0; j < kNB; ++j) acc[b][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
     v4u w[kStages][kNB];               // MX4: operands of tiles t .. t + 3
-    uint32_t ws[kNB], wsn[kNB];
-#pragma unroll
-    for (int j = 0; j < kNB; ++j) ws[j] = wsn[j] = kTernaryScale;
+    uint32_t ws[kNB], wsn[kNB];        // scales of this quad and the next
 
     // Load d of tile t's weights (past the last tile: of the last) into
     // register set or stage i, and of its activations into stage i.
@@ -174,26 +177,25 @@ __global__ __launch_bounds__(64 * WM * WN * KS, (Tile<KIND, WM, WN, MB, KS>::EU)
     const int xfrag = wm * MB * 1024 + 16 * (4 * r + (g ^ ((r >> 1) & 3)));
     const int wfrag = (T::XPART + 2 * wn + (r >> 3)) * 1024 + 128 * (r & 7);
 
-    // Operands in registers ahead of their instructions: kPre activation
-    // blocks, and for ternary weights the lane's words.
-    constexpr int kPre = MB < 4 ? MB : 4;
-    v4u x[kPre], half[2];
-    uint32_t xs[MB];
-    auto read_x = [&](int st, int b) __attribute__((always_inline)) {
-        x[b % kPre] = *reinterpret_cast<const v4u *>(lds + st * T::STAGE + xfrag + b * 1024);
+    // Operands in registers ahead of their instructions.  MX4: kPre activation
+    // blocks.  Ternary: all of them, of this tile and the next if MB <= 4, the
+    // lane's words of both tiles, and two blocks' weights.
+    constexpr int kPre = KIND == kTernary || MB < 4 ? MB : 4, kSets = KIND == kTernary && MB <= 4 ? 2 : 1;
+    v4u x[kSets][kPre], half[2][2], wf[2];
+    uint32_t xs[MB], xsn[MB];
+    auto read_x = [&](int set, int st, int b) __attribute__((always_inline)) {
+        x[set][b % kPre] = *reinterpret_cast<const v4u *>(lds + st * T::STAGE + xfrag + b * 1024);
     };
-    auto read_half = [&](int st) __attribute__((always_inline)) {
-        if constexpr (KIND == kTernary) {
+    auto read_half = [&](int set, int st) __attribute__((always_inline)) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                half[h] = *reinterpret_cast<const v4u *>(lds + st * T::STAGE + wfrag +
-                                                         16 * ((2 * g + h) ^ (r & 7)));
-        }
+        for (int h = 0; h < 2; ++h)
+            half[set][h] = *reinterpret_cast<const v4u *>(lds + st * T::STAGE + wfrag +
+                                                          16 * ((2 * g + h) ^ (r & 7)));
     };
-    auto read_scales = [&](int i) __attribute__((always_inline)) {
+    auto read_scales = [&](int i, uint32_t (&s)[MB]) __attribute__((always_inline)) {
         const uint8_t *sc = lds + kStages * T::STAGE + i * T::SBUF + wm * MB * 256 + 16 * r + 4 * g;
 #pragma unroll
-        for (int b = 0; b < MB; ++b) xs[b] = *reinterpret_cast<const uint32_t *>(sc + 256 * b);
+        for (int b = 0; b < MB; ++b) s[b] = *reinterpret_cast<const uint32_t *>(sc + 256 * b);
     };
 
     // One tile: quad u's tile TT; `next` is the group's quad after u.
@@ -209,15 +211,9 @@ __global__ __launch_bounds__(64 * WM * WN * KS, (Tile<KIND, WM, WN, MB, KS>::EU)
 #pragma unroll
             for (int j = 0; j < kNB; ++j) __asm__ volatile("" ::"v"(w[NEXT][j]));
         }
+        // (What a wave has read of the stage that is loaded next, it has used,
+        // but for reads past the last tile, whose values nobody uses.)
         mx4_barrier();
-        v4u wf[kNB];
-#pragma unroll
-        for (int j = 0; j < kNB; ++j) {
-            if constexpr (KIND == kTernary)
-                wf[j] = ternary_fp4(half[0][j], half[1][j]);
-            else
-                wf[j] = w[TT][j];
-        }
         // Loads between the blocks of instructions, three tiles ahead (the
         // weights last: waiting for them covers the activations).
         auto load = [&](int i) __attribute__((always_inline)) {
@@ -229,26 +225,59 @@ __global__ __launch_bounds__(64 * WM * WN * KS, (Tile<KIND, WM, WN, MB, KS>::EU)
         };
         constexpr int kLoads = T::WD + T::XD, kEach = (kLoads + MB - 1) / MB;
         const bool live = FULL || 4 * u + TT <= last;
+        if constexpr (KIND == kTernary) {
+            constexpr int SET = TT & 1, XSET = kSets > 1 ? SET : 0, XNEXT = kSets > 1 ? SET ^ 1 : 0;
+            // Weight block j with all activations, and between the
+            // instructions the next weight block (of the next tile at last).
 #pragma unroll
-        for (int b = 0; b < MB; ++b) {
-            if (live) {
+            for (int j = 0; j < kNB; ++j) {
 #pragma unroll
-                for (int j = 0; j < kNB; ++j)
-                    acc[b][j] = mx4_mfma<TT>(wf[j], x[b % kPre], acc[b][j], ws[j], xs[b]);
+                for (int b = 0; b < MB; ++b) {
+                    if (live)
+                        acc[b][j] = mx4_mfma<TT>(wf[j & 1], x[XSET][b], acc[b][j], kTernaryScale, xs[b]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    constexpr int kWords = MB < 4 ? 4 / MB : 1;
+#pragma unroll
+                    for (int e = b * kWords; e < (b + 1) * kWords; ++e)
+                        if (e < 4) {
+                            const uint32_t c = j < 3 ? half[SET][e >> 1][j < 3 ? j + 1 : 0]
+                                                     : half[SET ^ 1][e >> 1][0];
+                            wf[(j + 1) & 1][e] = ternary_word(e & 1 ? c : c << 2);
+                        }
+                    if (j == (kSets > 1 ? 0 : 3)) read_x(XNEXT, NEXT, b);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (j == 0) read_half(SET ^ 1, NEXT);
+                if (j == 0 && TT == 3) read_scales((q + 1) & 1, xsn);
+#pragma unroll
+                for (int i = j; i < kLoads; i += 4) load(i);
             }
-            __builtin_amdgcn_sched_barrier(0);
-            read_x(b + kPre < MB ? TT : NEXT, (b + kPre) % MB);
-            if (b == 0) read_half(NEXT);
+        } else {
 #pragma unroll
-            for (int i = b * kEach; i < (b + 1) * kEach; ++i) load(i);
+            for (int b = 0; b < MB; ++b) {
+                if (live) {
+#pragma unroll
+                    for (int j = 0; j < kNB; ++j)
+                        acc[b][j] = mx4_mfma<TT>(w[TT][j], x[0][b % kPre], acc[b][j], ws[j], xs[b]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                read_x(0, b + kPre < MB ? TT : NEXT, (b + kPre) % MB);
+#pragma unroll
+                for (int i = b * kEach; i < (b + 1) * kEach; ++i) load(i);
+            }
         }
-        // (Behind this tile's barrier: the other buffer's readers are done;
-        // ahead of the loads that the quad's third tile waits for.)
+        // (The other buffer's readers are done; ahead of the loads that the
+        // quad's third tile waits for.)
         if constexpr (TT == 0) scales(next, (q + 1) & 1, wsn);
         if constexpr (TT == 3) {
-            read_scales((q + 1) & 1);
+            if constexpr (KIND == kTernary) {
 #pragma unroll
-            for (int j = 0; j < kNB; ++j) ws[j] = wsn[j];
+                for (int b = 0; b < MB; ++b) xs[b] = xsn[b];
+            } else {
+                read_scales((q + 1) & 1, xs);
+#pragma unroll
+                for (int j = 0; j < kNB; ++j) ws[j] = wsn[j];
+            }
         }
     };
 
@@ -271,9 +300,12 @@ __global__ __launch_bounds__(64 * WM * WN * KS, (Tile<KIND, WM, WN, MB, KS>::EU)
     }
     mx4_barrier();
 #pragma unroll
-    for (int b = 0; b < kPre; ++b) read_x(0, b);
-    read_half(0);
-    read_scales(0);
+    for (int b = 0; b < kPre; ++b) read_x(0, 0, b);
+    read_scales(0, xs);
+    if constexpr (KIND == kTernary) {
+        read_half(0, 0);
+        wf[0] = ternary_fp4(half[0][0][0], half[0][1][0]);
+    }
 
     auto quad = [&](auto full, int q) __attribute__((always_inline)) {
         const int u = q * KS + grp, next = u + KS;
@@ -372,11 +404,15 @@ hipError_t gemm_launch(const Mx4Launch &a, hipStream_t stream) {
 // the larger of L (a lone workgroup's latency) and B a workgroup (what the
 // compute unit gets through).  The numbers are fitted to all tile shapes at
 // 150 sizes (M 33 to 4096, N 512 to 55296, K 512 to 27648, cold weights); the
-// choice by them is 1.3% (MX4) and 1.8% (ternary) behind the best tile on
+// choice by them is 0.9% (MX4) and 0.4% (ternary) behind the best tile on
 // average.  Both sides, us: MX4 512 x 2560 x 6912: 64 x 128 split over two
-// groups 14.2, 64 x 256 19.3, 128 x 256 26.2; 512 x 13824 x 2560: 128 x 256
-// 18.7, 64 x 256 23.2, 32 x 256 34.2; 64 x 5120 x 27648: 32 x 64 over four
-// groups 36.9, 64 x 256 104.
+// groups 14.0, 64 x 256 19.4, 128 x 256 26.1; 512 x 13824 x 2560: 128 x 256
+// 18.7, 64 x 256 23.3, 32 x 256 34.3; 64 x 5120 x 27648: 32 x 64 over four
+// groups 37.2, 64 x 256 104.  Ternary 512 x 2560 x 6912: 64 x 128 over two
+// 12.2, 64 x 256 18.3; 4001 x 13824 x 2560: 128 x 256 73.8, 64 x 256 80.7; 33 x
+// 5120 x 27648: 16 x 64 over eight 16.8, 32 x 64 over four 24.4.  (A ring of
+// eight stages, six tiles ahead and a barrier for every second tile: 512 x 2560
+// x 6912 11.5, but MX4 14.8, and 4001 x 13824 x 2560 104.)
 struct Plan {
     int BM, BN, KS, Q;
     float A, E, L, B;

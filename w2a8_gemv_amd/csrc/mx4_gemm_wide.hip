@@ -3,12 +3,15 @@
 // 128, one workgroup to a compute unit.
 //
 // The other tiles (mx4_gemm.hip) load a weight byte once for every 128 rows
-// or fewer; 8192 x 13824 x 5120 takes them 310 us (128 x 256), and this kernel
-// 293 us, 2048 x 5120 x 27648 187 and 161 us.  The loop reaches 5.4 PFLOP/s of
-// the 7.3 that the instruction sustains on random operands (power), and a
-// tile's start and results take 10 us that nothing hides: one workgroup fills
-// the compute unit.  Keeping workgroups and starting the next tile's loads
-// ahead of the results was tried: the registers of both do not fit (350 us).
+// or fewer; 8192 x 13824 x 5120 takes them 315 us (128 x 256), and this kernel
+// 292 us, 2048 x 5120 x 27648 217 and 161 us.  What bounds it is power first
+// (the same product of zeros takes 227 us): twice the k adds 2560 k in 121 us,
+// 6.0 PFLOP/s of the 7.35 that the instruction alone sustains on random
+// operands.  A tile's start and results, 7 us, are hidden by nothing: one
+// workgroup fills the compute unit.  Keeping workgroups and starting the next
+// tile's loads ahead of the results was tried (the registers of both do not
+// fit, 350 us), as were results straight from the registers (fp32 324 against
+// 313 us) and all of a wave's results through LDS at once (no change).
 //
 //  * Both operands go through LDS (each byte is loaded once per workgroup; a
 //    wave's 128 x 128 needs 16 KiB of LDS reads per 64 instructions, half of
@@ -188,6 +191,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx4_gemm_wide_kernel(Mx4Launch
     // The repeats of the last tile have landed and every wave has read its
     // last operands; the ring is free.
     mx4_wait_loads<0>();
+    mx4_wait_lds();
     mx4_barrier();
     // 16 rows of 128 columns at a time; lane (r, g) holds columns 16j + 4g .. of
     // row r.  fp32: chunks of 16 bytes (four columns), chunk c of row i at c ^
