@@ -195,7 +195,7 @@ KINDS = ["w4", "w2"]
 # 256, 128 x 256, 256 x 256 (MX4) and 128 x 256 (ternary)
 PLANS = [(74, 102, 2064), (36, 100, 130), (64, 100, 514), (2100, 235, 1048), (2052, 196, 523),
          (2084, 213, 137), (2083, 863, 132), (2105, 962, 132), (2071, 1812, 132), (2008, 6186, 133),
-         (1967, 6454, 1100)]
+         (1967, 6454, 1100), (2157, 203, 1153)]
 # every edge of rows, columns and k: blocks of 32, tiles of 128, groups of 512
 SMALL = [(1, 1, 1), (1, 16, 31), (2, 17, 32), (1, 33, 33), (3, 15, 127), (16, 16, 128), (17, 32, 129),
          (31, 100, 257), (33, 7, 384), (16, 48, 511), (1, 64, 512), (5, 65, 513), (64, 33, 640),

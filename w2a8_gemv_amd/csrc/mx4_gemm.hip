@@ -34,6 +34,8 @@
 //    block ahead of its use (for all blocks at the start of a tile they kept the
 //    matrix pipe waiting: a tile of 64 x 128 over two groups 0.29 us, now
 //    0.22, operands in the L2; 1024 x 2560 x 6912 20.2 us, now 18.6).
+//  * Tiles that a short last quad lacks are not stepped through (4001 x 13824 x
+//    2688 ternary 83.6 us, 92 before).
 //  * KS > 1 (grids smaller than the device): the groups take the quads of
 //    tiles in turn and add up through LDS at the end, in group order.
 //  * Results pass through LDS, 16 rows x 64 columns at a time, so that the
@@ -224,7 +226,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS, (Tile<KIND, WM, WN, MB, KS>::EU)
                 load_w(i - T::XD, t, (TT + 3) % kStages);
         };
         constexpr int kLoads = T::WD + T::XD, kEach = (kLoads + MB - 1) / MB;
-        const bool live = FULL || 4 * u + TT <= last;
+        // (Without other groups, only tiles that exist are stepped through.)
+        const bool live = FULL || KS == 1 || 4 * u + TT <= last;
         if constexpr (KIND == kTernary) {
             constexpr int SET = TT & 1, XSET = kSets > 1 ? SET : 0, XNEXT = kSets > 1 ? SET ^ 1 : 0;
             // Weight block j with all activations, and between the
@@ -282,7 +285,6 @@ __global__ __launch_bounds__(64 * WM * WN * KS, (Tile<KIND, WM, WN, MB, KS>::EU)
     };
 
     // The group's quads: grp, grp + KS, ...; all groups take as many steps.
-    const int steps = (a.KU + KS - 1) / KS;
     scales(grp, 0, ws);
 #pragma unroll
     for (int t = 0; t < 3; ++t) {
@@ -308,18 +310,19 @@ __global__ __launch_bounds__(64 * WM * WN * KS, (Tile<KIND, WM, WN, MB, KS>::EU)
     }
 
     auto quad = [&](auto full, int q) __attribute__((always_inline)) {
+        // (All groups take the steps of the first, which has the most tiles.)
         const int u = q * KS + grp, next = u + KS;
+        const int n = decltype(full)::value ? 4 : a.KT - 4 * q * KS;
         tile(std::integral_constant<int, 0>{}, full, q, u, next);
-        tile(std::integral_constant<int, 1>{}, full, q, u, next);
-        tile(std::integral_constant<int, 2>{}, full, q, u, next);
-        tile(std::integral_constant<int, 3>{}, full, q, u, next);
+        if (n > 1) tile(std::integral_constant<int, 1>{}, full, q, u, next);
+        if (n > 2) tile(std::integral_constant<int, 2>{}, full, q, u, next);
+        if (n > 3) tile(std::integral_constant<int, 3>{}, full, q, u, next);
     };
-    // Quads that are whole in every group, then the others.
+    // Rounds of quads that are whole in every group, then the last one.
     const int whole = a.KT / (4 * KS);
 #pragma unroll 1
     for (int q = 0; q < whole; ++q) quad(std::true_type{}, q);
-#pragma unroll 1
-    for (int q = whole; q < steps; ++q) quad(std::false_type{}, q);
+    if (4 * whole * KS < a.KT) quad(std::false_type{}, whole);
 
     // The repeats of the last tile are still on their way into LDS; then every
     // operand has been read.
@@ -423,7 +426,8 @@ float plan_us(const Plan &p, const Mx4Launch &a, int cus) {
     const int64_t units = ceil_div(a.M, p.BM) * ceil_div(a.N, p.BN);
     const int64_t turn = int64_t(cus) * p.Q, full = units / turn;
     const int64_t m = ceil_div(units - full * turn, cus);
-    const float tiles = 4.0f * float(ceil_div(a.KU, p.KS));
+    const int round = kMxQuad * p.KS;
+    const float tiles = float(a.KT / round * kMxQuad + std::min(a.KT % round, kMxQuad));
     const auto take = [&](float wgs) { return p.E * wgs + tiles * std::max(p.L, p.B * wgs); };
     return p.A + float(full) * take(float(p.Q)) + (m ? take(float(m)) : 0.0f);
 }

@@ -116,24 +116,20 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx4_gemm_wide_kernel(Mx4Launch
     };
 
     // One step: tile TT of quad u (its operands' first part is in registers).
-    auto tile = [&](auto tt, auto full, int u) __attribute__((always_inline)) {
+    auto tile = [&](auto tt, int u) __attribute__((always_inline)) {
         constexpr int TT = decltype(tt)::value, NEXT = (TT + 1) % 4;
-        constexpr bool FULL = decltype(full)::value;
         // Tile t + 1 has landed: issued since are one tile's loads, and before
         // the second and third tile of a quad the next quad's scales.
         mx4_wait_loads<kLoads + (TT == 1 || TT == 2 ? kScaleLoads : 0)>();
         mx4_barrier();
-        const bool live = FULL || 4 * u + TT <= last;
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-                if (live) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int j = 2 * p + e;
-                        acc[b][j] = mx4_mfma<TT>(wf[TT & 1][j], x[b & 3], acc[b][j], ws[0][j], xs[0][b]);
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    const int j = 2 * p + e;
+                    acc[b][j] = mx4_mfma<TT>(wf[TT & 1][j], x[b & 3], acc[b][j], ws[0][j], xs[0][b]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 // Between each two: activations two blocks ahead, a load of
@@ -156,11 +152,12 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx4_gemm_wide_kernel(Mx4Launch
         }
     };
     static_assert(kLoads == kB, "one load a block");
-    auto quad = [&](auto full, int u) __attribute__((always_inline)) {
-        tile(std::integral_constant<int, 0>{}, full, u);
-        tile(std::integral_constant<int, 1>{}, full, u);
-        tile(std::integral_constant<int, 2>{}, full, u);
-        tile(std::integral_constant<int, 3>{}, full, u);
+    // n of quad u's tiles.
+    auto quad = [&](int u, int n) __attribute__((always_inline)) {
+        tile(std::integral_constant<int, 0>{}, u);
+        if (n > 1) tile(std::integral_constant<int, 1>{}, u);
+        if (n > 2) tile(std::integral_constant<int, 2>{}, u);
+        if (n > 3) tile(std::integral_constant<int, 3>{}, u);
     };
 
     load_scales(0, 0);
@@ -185,8 +182,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx4_gemm_wide_kernel(Mx4Launch
     read_x(0, 1);
     const int whole = a.KT / 4;
 #pragma unroll 1
-    for (int u = 0; u < whole; ++u) quad(std::true_type{}, u);
-    if (whole < a.KU) quad(std::false_type{}, whole);
+    for (int u = 0; u < whole; ++u) quad(u, 4);
+    if (whole < a.KU) quad(whole, a.KT - 4 * whole);
 
     // The repeats of the last tile have landed and every wave has read its
     // last operands; the ring is free.
