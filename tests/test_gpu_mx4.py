@@ -196,6 +196,9 @@ KINDS = ["w4", "w2"]
 PLANS = [(74, 102, 2064), (36, 100, 130), (64, 100, 514), (2100, 235, 1048), (2052, 196, 523),
          (2084, 213, 137), (2083, 863, 132), (2105, 962, 132), (2071, 1812, 132), (2008, 6186, 133),
          (1967, 6454, 1100), (2157, 203, 1153)]
+# the largest tiles with the other kind of result stores (whole lines or long k
+# against large outputs of odd rows)
+STORES = [(2574, 4672, 387), (3920, 1091, 128), (548, 7698, 133), (3277, 3712, 648), (1415, 5490, 129)]
 # every edge of rows, columns and k: blocks of 32, tiles of 128, groups of 512
 SMALL = [(1, 1, 1), (1, 16, 31), (2, 17, 32), (1, 33, 33), (3, 15, 127), (16, 16, 128), (17, 32, 129),
          (31, 100, 257), (33, 7, 384), (16, 48, 511), (1, 64, 512), (5, 65, 513), (64, 33, 640),
@@ -208,9 +211,22 @@ LARGE = [(1, 2560, 2560), (1, 5120, 6912), (1, 3000, 13825), (8, 2560, 2560), (1
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("M,N,K", SMALL + LARGE + PLANS)
+@pytest.mark.parametrize("M,N,K", SMALL + LARGE + PLANS + STORES)
 def test_product_is_exact(M, N, K, kind):
     assert_product(kind, M, N, K, seed=M + 3 * N + 5 * K)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_large_outputs_of_odd_rows(kind):
+    """Outputs of more than 24 MiB whose rows are no whole lines, with a short k
+    (every row of results equals that of a product of few rows)."""
+    M, N, K = 1300, 6151, 100
+    c, s = mx_rows(M, K, 8)
+    wp, _ = weights(kind, N, K, 9)
+    yf, yb = gemm(kind, wp, *on_device(c, s), M, N, K)
+    for m in (0, 1, 640, 1277):
+        f, b = gemm(kind, wp, *on_device(c[m:m + 23], s[m:m + 23]), 23, N, K)
+        assert torch.equal(yf[m:m + 23], f) and torch.equal(yb[m:m + 23], b)
 
 
 @pytest.mark.parametrize("kind", KINDS)

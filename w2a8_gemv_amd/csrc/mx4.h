@@ -157,8 +157,9 @@ constexpr int kMx4StreamRows = 32;
 hipError_t launch_mx4_stream(const Mx4Launch &a, int cus, hipStream_t stream);
 // Activations through LDS (mx4_gemm.hip), any M.
 hipError_t launch_mx4_gemm(const Mx4Launch &a, int cus, hipStream_t stream);
-// Its 256 x 256 form for MX4 weights (mx4_gemm_wide.hip), any M.
-hipError_t launch_mx4_gemm_wide(const Mx4Launch &a, hipStream_t stream);
+// Its 256 x 256 form for MX4 weights (mx4_gemm_wide.hip), any M.  pass:
+// results pass the caches.
+hipError_t launch_mx4_gemm_wide(const Mx4Launch &a, bool pass, hipStream_t stream);
 // One float row (x_type), rounded inside (M = 1).
 hipError_t launch_mx4_fused(const Mx4Launch &a, int x_type, int cus, hipStream_t stream);
 

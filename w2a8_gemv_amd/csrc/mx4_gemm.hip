@@ -77,7 +77,7 @@ struct Tile {
     static constexpr int EU = THREADS <= 256 ? 2 : THREADS / 256;
 };
 
-template <int KIND, int WM, int WN, int MB, int KS>
+template <int KIND, int WM, int WN, int MB, int KS, bool PASS>
 __global__ __launch_bounds__(64 * WM * WN * KS, (Tile<KIND, WM, WN, MB, KS>::EU))
     void mx4_gemm_kernel(Mx4Launch a, Mx4Grid gr) {
     using T = Tile<KIND, WM, WN, MB, KS>;
@@ -383,13 +383,13 @@ __global__ __launch_bounds__(64 * WM * WN * KS, (Tile<KIND, WM, WN, MB, KS>::EU)
         default: if (MB > 7) dump(MB > 7 ? 7 : 0); break;
         }
         mx4_wave_sync();
-        mx4_store_rows<64, false>(a, out, mb, n0, lane);
+        mx4_store_rows<64, false, PASS>(a, out, mb, n0, lane);
         mx4_wave_sync();
     }
 }
 
 template <int KIND, int WM, int WN, int MB, int KS>
-hipError_t gemm_launch(const Mx4Launch &a, hipStream_t stream) {
+hipError_t gemm_launch(const Mx4Launch &a, bool pass, hipStream_t stream) {
     using T = Tile<KIND, WM, WN, MB, KS>;
     Mx4Grid gr;
     if (!gr.set(a.M, a.N, T::BM, T::BN)) return hipErrorInvalidValue;
@@ -397,8 +397,13 @@ hipError_t gemm_launch(const Mx4Launch &a, hipStream_t stream) {
     const int64_t gx = std::min<int64_t>(blocks, int64_t(1) << 20);
     const dim3 grid(unsigned(gx), unsigned(ceil_div(blocks, gx)));
     void *args[] = {const_cast<Mx4Launch *>(&a), &gr};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&mx4_gemm_kernel<KIND, WM, WN, MB, KS>),
-                           grid, dim3(T::THREADS), args, 0, stream);
+    // (Grids of split k are small: their results always pass.)
+    const void *kernel = reinterpret_cast<const void *>(&mx4_gemm_kernel<KIND, WM, WN, MB, KS, true>);
+    if constexpr (KS == 1) {
+        if (!pass)
+            kernel = reinterpret_cast<const void *>(&mx4_gemm_kernel<KIND, WM, WN, MB, KS, false>);
+    }
+    return hipLaunchKernel(kernel, grid, dim3(T::THREADS), args, 0, stream);
 }
 
 // What a launch takes in us, from its tiles and the device alone: workgroups
@@ -419,7 +424,7 @@ hipError_t gemm_launch(const Mx4Launch &a, hipStream_t stream) {
 struct Plan {
     int BM, BN, KS, Q;
     float A, E, L, B;
-    hipError_t (*launch)(const Mx4Launch &, hipStream_t);
+    hipError_t (*launch)(const Mx4Launch &, bool, hipStream_t);
 };
 
 float plan_us(const Plan &p, const Mx4Launch &a, int cus) {
@@ -452,12 +457,26 @@ constexpr Plan kTernaryPlans[] = {
     {128, 256, 1, 2, 2.61f, 2.97f, 0.438f, 0.366f, &gemm_launch<kTernary, 1, 4, 8, 1>},
 };
 
+// Whether results pass the caches (non-temporal stores).  That leaves the
+// caches to the operands, but where rows of results are no whole lines, the
+// parts of a line that two workgroups write no longer meet in them.  Measured
+// (MI355X, us, staying and passing): whole lines, 4001 x 13824 x 2560 fp32: MX4
+// 123 and 93, ternary 104 and 81.  Parts of lines, 4001 x 13825 fp32, ternary:
+// k = 256 54 and 88, 1280 82 and 94, 2560 110 and 105, 5120 165 and 139; MX4
+// 256 56 and 80, 2560 133 and 115; 1500 x 13825 bf16, 1920: 31 and 37 ternary;
+// small outputs, 1024 x 5121 x 256 fp32: 9.9 and 9.3.
+bool results_pass(const Mx4Launch &a) {
+    const int64_t bytes = int64_t(a.M) * a.N * ((a.y_f32 ? 4 : 0) + (a.y_bf16 ? 2 : 0));
+    const bool lines = a.N % (a.y_bf16 ? 64 : 32) == 0;
+    return lines || a.K >= 2048 || bytes < 24 << 20;
+}
+
 template <size_t N>
 hipError_t run_plan(const Plan (&plans)[N], const Mx4Launch &a, int cus, hipStream_t stream) {
     const Plan *best = plans;
     for (const Plan &p : plans)
         if (plan_us(p, a, cus) < plan_us(*best, a, cus)) best = &p;
-    return best->launch(a, stream);
+    return best->launch(a, results_pass(a), stream);
 }
 
 }  // namespace

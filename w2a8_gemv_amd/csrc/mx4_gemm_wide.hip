@@ -44,6 +44,7 @@ constexpr int kLds = kScales + 2 * kScaleBuf;
 static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
 static_assert(kWaves * 16 * 128 * 4 <= kScales, "results pass through the ring");
 
+template <bool PASS>
 __global__ __launch_bounds__(64 * kWaves, 1) void mx4_gemm_wide_kernel(Mx4Launch a, Mx4Grid gr) {
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
     const int lane = int(threadIdx.x) & 63;
@@ -206,6 +207,19 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx4_gemm_wide_kernel(Mx4Launch
                 *reinterpret_cast<v4f *>(out + 4 * mx4_out_at<128, true>(r, 4 * j + g)) = v;
         }
     };
+    auto store = [&](int b) __attribute__((always_inline)) {
+        if (only_bf16) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 4 * i + (lane >> 4), c = lane & 15;
+                mx4_store_bf16<PASS>(a, m0 + 16 * b + row, n0 + 8 * c,
+                                     *reinterpret_cast<const v4u *>(out + 256 * row +
+                                                                    16 * (c ^ (row & 7))));
+            }
+        } else {
+            mx4_store_rows<128, true, PASS>(a, out, m0 + 16 * b, n0, lane);
+        }
+    };
 #pragma unroll 1
     for (int b = 0; b < kB; ++b) {
         switch (b) {
@@ -219,31 +233,23 @@ __global__ __launch_bounds__(64 * kWaves, 1) void mx4_gemm_wide_kernel(Mx4Launch
         default: dump(7); break;
         }
         mx4_wave_sync();
-        if (only_bf16) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 4 * i + (lane >> 4), c = lane & 15;
-                mx4_store_bf16(a, m0 + 16 * b + row, n0 + 8 * c,
-                               *reinterpret_cast<const v4u *>(out + 256 * row + 16 * (c ^ (row & 7))));
-            }
-        } else {
-            mx4_store_rows<128, true>(a, out, m0 + 16 * b, n0, lane);
-        }
+        store(b);
         mx4_wave_sync();
     }
 }
 
 }  // namespace
 
-hipError_t launch_mx4_gemm_wide(const Mx4Launch &a, hipStream_t stream) {
+hipError_t launch_mx4_gemm_wide(const Mx4Launch &a, bool pass, hipStream_t stream) {
     Mx4Grid gr;
     if (!gr.set(a.M, a.N, kTileM, kTileN)) return hipErrorInvalidValue;
     const int64_t blocks = round_up(int64_t(gr.units), 8);
     const int64_t gx = std::min<int64_t>(blocks, int64_t(1) << 20);
     void *args[] = {const_cast<Mx4Launch *>(&a), &gr};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&mx4_gemm_wide_kernel),
-                           dim3(unsigned(gx), unsigned(ceil_div(blocks, gx))), dim3(64 * kWaves), args,
-                           0, stream);
+    const void *kernel = pass ? reinterpret_cast<const void *>(&mx4_gemm_wide_kernel<true>)
+                              : reinterpret_cast<const void *>(&mx4_gemm_wide_kernel<false>);
+    return hipLaunchKernel(kernel, dim3(unsigned(gx), unsigned(ceil_div(blocks, gx))), dim3(64 * kWaves),
+                           args, 0, stream);
 }
 
 }  // namespace w2a8
