@@ -199,6 +199,10 @@ PLANS = [(74, 102, 2064), (36, 100, 130), (64, 100, 514), (2100, 235, 1048), (20
 # the largest tiles with the other kind of result stores (whole lines or long k
 # against large outputs of odd rows)
 STORES = [(2574, 4672, 387), (3920, 1091, 128), (548, 7698, 133), (3277, 3712, 648), (1415, 5490, 129)]
+# strips of weights as many as compute units, a few more and more than two for
+# each, at the weight stream's two kinds of short batches; long k
+STREAMS = [(1, 4096, 4100), (9, 4096, 4100), (24, 4096, 4100), (24, 4112, 3000), (32, 8200, 2100),
+           (24, 8300, 1100), (17, 16500, 520), (16, 9000, 1030), (17, 4100, 20500), (20, 8200, 20480)]
 # every edge of rows, columns and k: blocks of 32, tiles of 128, groups of 512
 SMALL = [(1, 1, 1), (1, 16, 31), (2, 17, 32), (1, 33, 33), (3, 15, 127), (16, 16, 128), (17, 32, 129),
          (31, 100, 257), (33, 7, 384), (16, 48, 511), (1, 64, 512), (5, 65, 513), (64, 33, 640),
@@ -211,7 +215,7 @@ LARGE = [(1, 2560, 2560), (1, 5120, 6912), (1, 3000, 13825), (8, 2560, 2560), (1
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("M,N,K", SMALL + LARGE + PLANS + STORES)
+@pytest.mark.parametrize("M,N,K", SMALL + LARGE + PLANS + STORES + STREAMS)
 def test_product_is_exact(M, N, K, kind):
     assert_product(kind, M, N, K, seed=M + 3 * N + 5 * K)
 

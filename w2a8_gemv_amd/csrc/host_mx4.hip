@@ -37,15 +37,19 @@ Place place(int64_t n, int64_t b, int64_t NS, int64_t KT, int64_t KU) {
 
 // Rows of activations up to which the weight stream serves a product.  It
 // reads every weight once, but every strip reads all rows: with many weight
-// rows to a CU the tiles of the other kernel share them.  Measured (MI355X,
-// us, stream and tiles): 13824 x 2560, M = 32: MX4 6.8 and 7.6, ternary 6.2
-// and 6.8; 55296 x 5120: MX4, M = 4, 16 and 32: 31.4 and 31.4, 34.9 and 30.1,
-// 44.4 and 30.8; ternary, M = 16 and 32: 16.4 and 17.7, 26.9 and 21.0; 5120 x
-// 27648 MX4, M = 17: 32.0 and 25.8.
+// rows to a CU the tiles of the other kernel share them, and where strips
+// are a few more than CUs, and long, they fall behind its split of k.
+// Measured (MI355X, us, stream and tiles): 13824 x 2560, M = 32: MX4 7.5 and
+// 9.1, ternary 5.7 and 6.9; 55296 x 5120: MX4, M = 4, 16 and 32: 32.2 and 32.3,
+// 36.7 and 33.0, 46.0 and 34.4; ternary, M = 16, 17 and 32: 16.7 and 19.9, 21.7
+// and 20.2, 27.1 and 20.5; 27648 columns, MX4, 320 strips, M = 16, 24 and 32:
+// 25.4 and 32.3, 32.0 and 29.9, 35.8 and 31.2, 256 strips: 17.1 and 30.8, 19.5
+// and 27.5, 20.9 and 29.4; ternary, 320 strips, M = 32: 34.7 and 31.1.
 int stream_rows(const Mx4Launch &a, int cus) {
     const bool ternary = !a.ws;
     if (a.N >= 160 * int64_t(cus)) return ternary ? 16 : 4;
-    return !ternary && a.KU >= 40 ? 16 : kMx4StreamRows;
+    const int64_t strips = ceil_div(a.N, ternary ? kTileRows : kMxRows);
+    return a.KU >= 40 && strips > cus && strips <= 2 * cus ? 16 : kMx4StreamRows;
 }
 
 // Shared by the four product entry points.  x_type < 0: MX4R rows.

@@ -304,20 +304,22 @@ __global__ __launch_bounds__(64 * kMaxWaves) void mx4_stream_kernel(Mx4Launch a)
 }
 
 // Waves of a workgroup.  A CU holds as many waves as its LDS holds pairs of
-// stages (16, 8 or 5 by M), and what helps beyond filling it is few waves to
-// a strip (shorter sums, and a wave that streams on); with fewer strips than
-// CUs the waves of a strip are all there is to keep loads on their way.
-// Measured (MI355X, us, cold weights): M = 1, 5120 x 27648 MX4, 320 strips: 3
-// waves 16.7, 8 waves 17.9; 55296 x 5120 28.4 against 30.9; ternary, 160
-// strips: 8 waves 10.2, 4 waves 11.7.  M = 16, 55296 x 5120 ternary: 1 wave
-// 16.7, 2 waves 19.6, 5 waves 27 or more; 13824 x 2560 MX4: 2 waves 6.6, 5
-// waves 7.8.  M = 32, 13824 x 2560 MX4: 1 wave 7.3, 2 waves 9.7; 5120 x
-// 27648 ternary, 160 strips: 3 waves 17.2, 1 wave over 20.
+// stages (16, 8 or 5 by M).  With a strip or less for every CU the waves of a
+// strip are all there is to keep loads on their way; beyond, few waves to a
+// strip (shorter sums, and a wave that streams on), but no more than let all
+// strips start at once.  Measured (MI355X, us, cold weights): M = 1, 5120 x
+// 27648 MX4, 320 strips: 3 waves 16.7, 8 waves 17.9; 55296 x 5120 28.4 against
+// 30.9; ternary, 160 strips: 8 waves 10.2, 4 waves 11.7.  M = 16, 55296 x 5120
+// ternary: 1 wave 16.7, 2 waves 19.6, 5 waves 27 or more; 13824 x 2560 MX4: 2
+// waves 6.6, 5 waves 7.8; 8192 x 27648 ternary, 256 strips: 5 waves 15.8, 2
+// waves 18.5.  M = 17, 256 strips: 8192 x 13824 ternary: 3 waves 9.8, 2 waves
+// 11.7, 1 wave 17.4; 290 strips, 9280 x 5120: 2 waves 7.4, 1 wave 8.6, 3 waves
+// 9.4; 563 strips, 9000 x 2560 MX4: 1 wave 6.2, 2 waves 7.6.
 int stream_waves(int M, int strips, int KU, int cus) {
-    const bool many = strips >= cus;
+    const bool many = strips > cus;
     const int nw = M == 1    ? (many ? 3 : kMaxWaves)
                    : M <= 16 ? (strips >= 4 * cus ? 1 : many ? 2 : 5)
-                             : (many ? 1 : 3);
+                             : (strips > 2 * cus ? 1 : many ? 2 : 3);
     return std::min(nw, KU);
 }
 
