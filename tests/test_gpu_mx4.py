@@ -520,3 +520,29 @@ def test_device_refusals():
         w2a8.linear_w4mx4(x, wp, 16, 65)
     with pytest.raises(ValueError):
         w2a8.w4mx4_linear_gemv(wp, x, 16, 64, y_f32=torch.empty(16, device=dev()))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_rows_of_another_k_are_refused(kind):
+    """Rows counted by their first dimension have to be rows of the K given;
+    larger buffers are taken where M is given or, for scales, where flat."""
+    M, N, K = 3, 40, 300
+    c, s = mx_rows(M, 700, 70)
+    wp, _ = weights(kind, N, K, 71)
+    long_q, long_s = on_device(c, s)
+    q, sc = on_device(c[:, :K], s[:, :10])
+    call = lambda a, b: (w2a8.gemm_w4mx4(wp, a, b, N, K) if kind == "w4"
+                         else w2a8.gemm_w2mx4(wp, a, b, 1.0, N, K))
+    for a, b in ((long_q, long_s), (long_q, sc), (q, long_s)):
+        with pytest.raises(ValueError):
+            call(a, b)
+        with pytest.raises(ValueError):
+            w2a8.dequant_act_mx4(a, b, K)
+    want, _ = gemm(kind, wp, q, sc, M, N, K)
+    flat = torch.cat([sc.view(-1), torch.zeros(64, dtype=torch.uint8, device=dev())])
+    more = torch.cat([sc, sc])
+    for b in (sc, flat, more):
+        assert torch.equal(call(q, b), want)
+    values = w2a8.dequant_act_mx4(q, sc, K)
+    assert torch.equal(w2a8.dequant_act_mx4(torch.cat([q, q]).view(-1), flat, K, M), values)
+    assert torch.equal(w2a8.dequant_act_mx4(q, flat, K), values)

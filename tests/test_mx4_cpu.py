@@ -209,3 +209,26 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         w2a8.quant_act_mx4(x.double())
     with pytest.raises(TypeError):
         w2a8.quant_act_mx4([1.0])
+
+
+def test_binding_refuses_rows_of_another_k(monkeypatch):
+    """Rows of a longer K are a larger buffer, so their bytes alone do not tell
+    them from rows of this one (refused before the library is called)."""
+    monkeypatch.setattr(w2a8, "_mx4_gpu", lambda t, name: t.get_device())
+    u8 = torch.uint8
+    M, N, K = 3, 16, 64
+    w = torch.zeros(w2a8.mx4_packed_bytes(N, K), dtype=u8)
+    t = torch.zeros(w2a8.packed_bytes(N, K), dtype=u8)
+    rows = lambda k: (torch.zeros((M, w2a8.mx4_act_bytes(1, k)), dtype=u8),
+                      torch.zeros((M, w2a8.mx4_scale_bytes(1, k)), dtype=u8))
+    q, s = rows(K)
+    for k in (256, 640):                       # other codes; other codes and scales
+        q2, s2 = rows(k)
+        pairs = [(q2, s2), (q2, s)] + ([(q, s2)] if s2.shape != s.shape else [])
+        for a, b in pairs:
+            with pytest.raises(ValueError, match="x_[qs] must have"):
+                w2a8.dequant_act_mx4(a, b, K)
+            with pytest.raises(ValueError, match="x_[qs] must have"):
+                w2a8.gemm_w4mx4(w, a, b, N, K)
+            with pytest.raises(ValueError, match="x_[qs] must have"):
+                w2a8.gemm_w2mx4(t, a, b, 1.0, N, K)

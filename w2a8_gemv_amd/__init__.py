@@ -739,17 +739,29 @@ def _mx4_count(x_q):
     return x_q.shape[0]
 
 
+def _mx4_scale_rows(x_s, row):
+    """Refuses rows of x_s that are not `row` bytes (a flat x_s is a buffer)."""
+    if x_s.dim() > 1 and x_s.shape[-1] != row:
+        raise ValueError(f"x_s must have rows of {row} bytes, got {x_s.shape[-1]}")
+
+
 def dequant_act_mx4(x_q, x_s, K: int, M=None, dtype=torch.float32, y=None, stream=None):
     """MX4R rows -> their values [M, K] in fp32, bf16 or fp16 (device).  M defaults to the
-    rows of a 2-d x_q; y may be given (M * K elements of dtype)."""
-    if M is None:
+    rows of x_q [M, mx4_act_bytes(1, K)] (x_s: [M, mx4_scale_bytes(1, K)], or flat); with M
+    given, x_q and x_s are buffers of at least M rows.  y may be given (M * K elements of
+    dtype)."""
+    counted = M is None
+    if counted:
         M = _mx4_count(x_q)
     dev = _mx4_gpu(x_q, "x_q")
     code = _MX4_TYPES.get(dtype)
     if code is None:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-    pq = _mx4_ptr(x_q, "x_q", dev, torch.uint8, mx4_act_bytes(M, K))
-    ps = _mx4_ptr(x_s, "x_s", dev, torch.uint8, mx4_scale_bytes(M, K))
+    na, ns = mx4_act_bytes(M, K), mx4_scale_bytes(M, K)
+    pq = _mx4_ptr(x_q, "x_q", dev, torch.uint8, na, na if counted else None)
+    ps = _mx4_ptr(x_s, "x_s", dev, torch.uint8, ns)
+    if counted and x_s.numel() != ns:
+        _mx4_scale_rows(x_s, ns // M)
     if y is None:
         y = _mx4_empty(x_q, (M, K), dtype, stream)
         py = y.data_ptr()
@@ -789,12 +801,16 @@ def _mx4_new(like, dtype, shape, stream):
     return (y, y.data_ptr(), None) if dtype is torch.float32 else (y, None, y.data_ptr())
 
 
-def _mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w, yf, yb, dev, stream):
+def _mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w, yf, yb, dev, stream, counted):
     """A product (s_w None: MX4 weights) into the addresses yf and yb."""
     na, ns, nw = _mx4_sizes(M, N, K, s_w is not None)
     pw = _mx4_ptr(w_packed, "w_packed", dev, torch.uint8, nw)
-    pq = _mx4_ptr(x_q, "x_q", dev, torch.uint8, na)
+    # Rows that were counted have to be rows of K values: those of a longer K are a larger
+    # buffer, but lie elsewhere in it.
+    pq = _mx4_ptr(x_q, "x_q", dev, torch.uint8, na, na if counted else None)
     ps = _mx4_ptr(x_s, "x_s", dev, torch.uint8, ns)
+    if counted and x_s.numel() != ns:
+        _mx4_scale_rows(x_s, ns // M)
     if s_w is None:
         st = lib().w4mx4_gemm(pw, pq, ps, M, N, K, yf, yb, _mx4_stream(stream, dev))
     else:
@@ -819,14 +835,14 @@ def w4mx4_gemm(w_packed, x_q, x_s, M, N, K, y_f32=None, y_bf16=None, stream=None
     """Raw C-ABI call: MX4 rows times MX4 weights (outputs must be given); returns nothing."""
     dev = _mx4_gpu(x_q, "x_q")
     yf, yb = _mx4_outputs(y_f32, y_bf16, dev, M * N)
-    _mx4_gemm(w_packed, x_q, x_s, M, N, K, None, yf, yb, dev, stream)
+    _mx4_gemm(w_packed, x_q, x_s, M, N, K, None, yf, yb, dev, stream, False)
 
 
 def w2mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w=1.0, y_f32=None, y_bf16=None, stream=None):
     """Raw C-ABI call: MX4 rows times packed ternary weights; returns nothing."""
     dev = _mx4_gpu(x_q, "x_q")
     yf, yb = _mx4_outputs(y_f32, y_bf16, dev, M * N)
-    _mx4_gemm(w_packed, x_q, x_s, M, N, K, float(s_w), yf, yb, dev, stream)
+    _mx4_gemm(w_packed, x_q, x_s, M, N, K, float(s_w), yf, yb, dev, stream, False)
 
 
 def w4mx4_linear_gemv(w_packed, x, N, K, y_f32=None, y_bf16=None, stream=None):
@@ -848,18 +864,20 @@ def w2mx4_linear_gemv(w_packed, x, N, K, s_w=1.0, y_f32=None, y_bf16=None, strea
 
 
 def gemm_w4mx4(w_packed, x_q, x_s, N, K, out_dtype=torch.float32, stream=None):
-    """MX4R rows (x_q [M, bytes of a row]) times MX4 weights -> fp32 or bf16 [M, N]."""
+    """MX4R rows, x_q [M, mx4_act_bytes(1, K)] and x_s [M, mx4_scale_bytes(1, K)] (or flat),
+    times MX4 weights -> fp32 or bf16 [M, N]."""
     M, dev = _mx4_count(x_q), _mx4_gpu(x_q, "x_q")
     y, yf, yb = _mx4_new(x_q, out_dtype, (M, N), stream)
-    _mx4_gemm(w_packed, x_q, x_s, M, N, K, None, yf, yb, dev, stream)
+    _mx4_gemm(w_packed, x_q, x_s, M, N, K, None, yf, yb, dev, stream, True)
     return y
 
 
 def gemm_w2mx4(w_packed, x_q, x_s, s_w, N, K, out_dtype=torch.float32, stream=None):
-    """MX4R rows (x_q [M, bytes of a row]) times ternary weights -> fp32 or bf16 [M, N]."""
+    """MX4R rows, x_q [M, mx4_act_bytes(1, K)] and x_s [M, mx4_scale_bytes(1, K)] (or flat),
+    times ternary weights -> fp32 or bf16 [M, N]."""
     M, dev = _mx4_count(x_q), _mx4_gpu(x_q, "x_q")
     y, yf, yb = _mx4_new(x_q, out_dtype, (M, N), stream)
-    _mx4_gemm(w_packed, x_q, x_s, M, N, K, float(s_w), yf, yb, dev, stream)
+    _mx4_gemm(w_packed, x_q, x_s, M, N, K, float(s_w), yf, yb, dev, stream, True)
     return y
 
 
@@ -873,7 +891,7 @@ def _mx4_linear(x, w_packed, s_w, N, K, out_dtype, stream, fused):
         _mx4_gemv(w_packed, x, code, N, K, s_w, yf, yb, dev, stream)
     else:
         x_q, x_s = quant_act_mx4(x, stream=stream)
-        _mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w, yf, yb, dev, stream)
+        _mx4_gemm(w_packed, x_q, x_s, M, N, K, s_w, yf, yb, dev, stream, False)
     return y
 
 
