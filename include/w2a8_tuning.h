@@ -116,6 +116,18 @@ int w2a8_gemv_plan(int64_t N, int64_t K, int cus, int *kernel, int *waves_per_wg
 int w2a8_linear_plan(int64_t N, int64_t K, int cus, int int4, int *kernel, int *waves_per_wg,
                      int *wgs_per_strip, int *run, int *depth);
 
+/* What w4mx4_gemm (ternary = 0) or w2mx4_gemm (ternary = 1; w2a8_mx4.h) runs
+ * for (M, N, K) into fp32 (outputs = 1), bf16 (2) or both (3) on a device with
+ * `cus` compute units.  *kernel: 1 the weight stream (*rows 1, 16 or 32
+ * activation rows of the kernel's form, *cols weight rows of a strip, *groups
+ * waves that share a strip's k), 2 output tiles (*rows x *cols results of a
+ * workgroup, *groups wave groups that split k; 256 x 256 is a kernel of its
+ * own).  *pass: 1 if results pass the caches (non-temporal stores).  Every
+ * choice computes every shape.  Returns W2A8_OK, W2A8_ERR_NULL,
+ * W2A8_ERR_SHAPE or W2A8_ERR_VALUE (cus, outputs). */
+int w2a8_mx4_plan(int64_t M, int64_t N, int64_t K, int ternary, int outputs, int cus, int *kernel,
+                  int *rows, int *cols, int *groups, int *pass);
+
 #ifdef __cplusplus
 }
 #endif

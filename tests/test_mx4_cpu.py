@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+import mx4_sizes
 import w2a8_gemv_amd as w2a8
 from oracle import mx4
 
@@ -232,3 +233,62 @@ def test_binding_refuses_rows_of_another_k(monkeypatch):
                 w2a8.gemm_w4mx4(w, a, b, N, K)
             with pytest.raises(ValueError, match="x_[qs] must have"):
                 w2a8.gemm_w2mx4(t, a, b, 1.0, N, K)
+
+
+# ---------------------------------------------------------------------------
+# launch plans
+# ---------------------------------------------------------------------------
+OUTPUTS = [(True, False), (False, True), (True, True)]
+
+
+def test_plan_query_refuses():
+    L = w2a8.lib()
+    out = [ctypes.byref(ctypes.c_int()) for _ in range(5)]
+    ok = (40, 100, 200, 0, 1, 256)
+    assert L.w2a8_mx4_plan(*ok, *out) == 0
+    for i in range(5):
+        assert L.w2a8_mx4_plan(*ok, *out[:i], None, *out[i + 1:]) == NULL
+    for i, bad in ((0, 0), (1, 0), (2, 0), (0, (1 << 20) + 1), (1, (1 << 30) + 1), (2, 1048449)):
+        assert L.w2a8_mx4_plan(*ok[:i], bad, *ok[i + 1:], *out) == SHAPE
+    for i, bad in ((4, 0), (4, 4), (5, 0)):
+        assert L.w2a8_mx4_plan(*ok[:i], bad, *ok[i + 1:], *out) == VALUE
+    with pytest.raises(w2a8.W2A8Error):
+        w2a8.mx4_plan(40, 100, 200, 256, f32=False)
+
+
+@pytest.mark.parametrize("kind", ["w4", "w2"])
+def test_test_sizes_reach_every_tile_and_store(kind):
+    """The sizes that the GPU tests run take every output tile, for each
+    selection of outputs, with rounds to spare, and both kinds of stores
+    wherever sizes at random find them."""
+    plan = lambda size, out: w2a8.mx4_plan(*size, mx4_sizes.CUS, kind == "w2", *out)
+    tiles = mx4_sizes.TILES[kind]
+    for i, size in enumerate(mx4_sizes.ROUNDS[kind]):
+        kernel, rows, cols, groups, _ = plan(size, OUTPUTS[0])
+        assert kernel == 2
+        if i < len(tiles):
+            assert (rows, cols, groups) == tiles[i], size
+        KT = -(-size[2] // 128)
+        left = KT % (4 * groups)
+        assert KT >= 12 * groups and (left > 4 if groups > 1 else left % 4), size
+    seen = {(plan(size, out)[1:], out) for out in OUTPUTS
+            for size in mx4_sizes.ROUNDS[kind] + mx4_sizes.STAY[kind]}
+    for size in mx4_sizes.STAY[kind]:
+        assert all(plan(size, out)[4] == 0 for out in OUTPUTS), size
+    rng = np.random.default_rng(1)
+    top = np.log([60000, 60000, 27648])
+    for size in np.exp(rng.uniform(0, 1, (60000, 3)) * top).round().astype(int).tolist():
+        if size[0] * size[1] <= 2 ** 25:
+            for out in OUTPUTS:
+                p = plan(size, out)
+                if p[0] == 2:
+                    assert p[1:4] in tiles, size
+                    assert (p[1:], out) in seen, (size, p, out)
+
+
+@pytest.mark.parametrize("kind", ["w4", "w2"])
+def test_test_sizes_reach_every_form_of_the_stream(kind):
+    for size, (rows, waves) in zip(mx4_sizes.STREAM[kind], mx4_sizes.STREAM_FORMS, strict=True):
+        p = w2a8.mx4_plan(*size, mx4_sizes.CUS, kind == "w2")
+        assert p == (1, rows, 32 if kind == "w2" else 16, waves, 0), size
+        assert -(-size[2] // 512) >= 3 * waves, size

@@ -23,7 +23,7 @@ __all__ = [
     "W2A8Error", "lib", "packed_bytes", "workspace_bytes", "layout_version",
     "ternarize_absmean", "pack_ternary", "unpack_ternary", "quant_act_int8",
     "w2a8_gemv", "w2a8_gemv_noalloc", "w2a8_gemm", "gemv", "gemm", "linear", "Workspace",
-    "w2a8_linear_gemv", "tune_gemv", "tune_gemv_force", "gemv_plan", "linear_plan", "DEFAULT_GEMV_POLICY",
+    "w2a8_linear_gemv", "tune_gemv", "tune_gemv_force", "gemv_plan", "linear_plan", "mx4_plan", "DEFAULT_GEMV_POLICY",
     "tune_gemm", "tune_gemm_ring", "tune_gemm_pipe",
     "act4_bytes", "pack_act_int4", "quant_act_int4", "w2a4_gemv", "w2a4_linear_gemv",
     "linear_a4", "w2a8_gemv_grouped", "w2a8_linear_gemv_grouped", "linear_grouped",
@@ -117,6 +117,8 @@ def lib():
         L.w2a8_gemv_plan.argtypes = [I64, I64, I32, P, P, P, P]
         L.w2a8_linear_plan.argtypes = [I64, I64, I32, I32, P, P, P, P, P]
         L.w2a8_linear_plan.restype = I32
+        L.w2a8_mx4_plan.argtypes = [I64, I64, I64, I32, I32, I32, P, P, P, P, P]
+        L.w2a8_mx4_plan.restype = I32
         L.w2a8_tune_gemv_force.argtypes = [I32, I32, I32, I32, I32]
         L.w2a8_tune_gemv_force.restype = I32
         L.w2a8_tune_gemm.argtypes = [I32]
@@ -953,6 +955,16 @@ def linear_plan(N: int, K: int, cus: int, int4: bool = False):
     v = [ctypes.c_int(0) for _ in range(5)]
     _check(lib().w2a8_linear_plan(N, K, cus, int(bool(int4)), *[ctypes.byref(x) for x in v]),
            "w2a8_linear_plan")
+    return tuple(x.value for x in v)
+
+
+def mx4_plan(M: int, N: int, K: int, cus: int, ternary: bool = False, f32: bool = True,
+             bf16: bool = False):
+    """What gemm_w4mx4 (or gemm_w2mx4) runs for (M, N, K) on `cus` compute units into an fp32
+    and/or a bf16 output: (kernel, rows, cols, groups, pass), see w2a8_tuning.h."""
+    v = [ctypes.c_int() for _ in range(5)]
+    _check(lib().w2a8_mx4_plan(M, N, K, int(bool(ternary)), int(bool(f32)) + 2 * int(bool(bf16)), cus,
+                               *[ctypes.byref(x) for x in v]), "w2a8_mx4_plan")
     return tuple(x.value for x in v)
 
 

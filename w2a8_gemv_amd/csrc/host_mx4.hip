@@ -4,6 +4,7 @@
 #include <cstring>
 
 #include "mx4.h"
+#include "w2a8_tuning.h"
 
 namespace w2a8 {
 namespace {
@@ -220,6 +221,39 @@ int w4mx4_gemm(const void *w_packed, const uint8_t *x_q, const uint8_t *x_s, int
 int w2mx4_gemm(const void *w_packed, const uint8_t *x_q, const uint8_t *x_s, int64_t M, int64_t N,
                int64_t K, float s_w, float *y_f32, uint16_t *y_bf16, void *stream) {
     return product(w_packed, true, x_q, x_s, nullptr, -1, M, N, K, s_w, y_f32, y_bf16, stream);
+}
+
+int w2a8_mx4_plan(int64_t M, int64_t N, int64_t K, int ternary, int outputs, int cus, int *kernel,
+                  int *rows, int *cols, int *groups, int *pass) {
+    if (!kernel || !rows || !cols || !groups || !pass) return W2A8_ERR_NULL;
+    if (!rows_ok(M, K) || !matrix_ok(N, K)) return W2A8_ERR_SHAPE;
+    if (cus < 1 || outputs < 1 || outputs > 3) return W2A8_ERR_VALUE;
+    // (The plans ask whether there are MX4 scales and which outputs, not where.)
+    alignas(16) static uint8_t some[16];
+    Mx4Launch a = {};
+    a.KT = int(mx4_tiles(K));
+    a.KU = int(mx4_quads(K));
+    a.ws = ternary ? nullptr : some;
+    a.y_f32 = outputs & 1 ? reinterpret_cast<float *>(some) : nullptr;
+    a.y_bf16 = outputs & 2 ? reinterpret_cast<uint16_t *>(some) : nullptr;
+    a.M = int(M);
+    a.N = int(N);
+    a.K = int(K);
+    if (M <= stream_rows(a, cus)) {
+        *kernel = 1;
+        *rows = M == 1 ? 1 : M <= 16 ? 16 : 32;
+        *cols = ternary ? kTileRows : kMxRows;
+        *groups = mx4_stream_waves(a.M, int(ceil_div(N, *cols)), a.KU, cus);
+        *pass = 0;
+        return W2A8_OK;
+    }
+    const Mx4TilePlan p = mx4_tile_plan(a, cus);
+    *kernel = 2;
+    *rows = p.BM;
+    *cols = p.BN;
+    *groups = p.KS;
+    *pass = p.pass;
+    return W2A8_OK;
 }
 
 int w4mx4_linear_gemv(const void *w_packed, const void *x, int x_type, int64_t N, int64_t K,

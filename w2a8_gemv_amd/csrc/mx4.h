@@ -155,7 +155,16 @@ hipError_t launch_quant_pack_mx4(const void *W, int type, int64_t N, int K, uint
 // Weights streamed through LDS by single waves (mx4_stream.hip), M <= 32.
 constexpr int kMx4StreamRows = 32;
 hipError_t launch_mx4_stream(const Mx4Launch &a, int cus, hipStream_t stream);
-// Activations through LDS (mx4_gemm.hip), any M.
+// Waves of a workgroup of it.
+int mx4_stream_waves(int M, int strips, int KU, int cus);
+// Activations through LDS (mx4_gemm.hip), any M: the tile it takes (rows by
+// columns over groups of waves that split k, and whether results pass the
+// caches), and the launch.
+struct Mx4TilePlan {
+    int BM, BN, KS;
+    bool pass;
+};
+Mx4TilePlan mx4_tile_plan(const Mx4Launch &a, int cus);
 hipError_t launch_mx4_gemm(const Mx4Launch &a, int cus, hipStream_t stream);
 // Its 256 x 256 form for MX4 weights (mx4_gemm_wide.hip), any M.  pass:
 // results pass the caches.

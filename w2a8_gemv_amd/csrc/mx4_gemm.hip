@@ -472,17 +472,27 @@ bool results_pass(const Mx4Launch &a) {
 }
 
 template <size_t N>
-hipError_t run_plan(const Plan (&plans)[N], const Mx4Launch &a, int cus, hipStream_t stream) {
+const Plan &best_plan(const Plan (&plans)[N], const Mx4Launch &a, int cus) {
     const Plan *best = plans;
     for (const Plan &p : plans)
         if (plan_us(p, a, cus) < plan_us(*best, a, cus)) best = &p;
-    return best->launch(a, results_pass(a), stream);
+    return *best;
 }
+const Plan &best_plan(const Mx4Launch &a, int cus) {
+    return a.ws ? best_plan(kMx4Plans, a, cus) : best_plan(kTernaryPlans, a, cus);
+}
+bool plan_passes(const Plan &p, const Mx4Launch &a) { return p.KS > 1 || results_pass(a); }
 
 }  // namespace
 
+Mx4TilePlan mx4_tile_plan(const Mx4Launch &a, int cus) {
+    const Plan &p = best_plan(a, cus);
+    return {p.BM, p.BN, p.KS, plan_passes(p, a)};
+}
+
 hipError_t launch_mx4_gemm(const Mx4Launch &a, int cus, hipStream_t stream) {
-    return a.ws ? run_plan(kMx4Plans, a, cus, stream) : run_plan(kTernaryPlans, a, cus, stream);
+    const Plan &p = best_plan(a, cus);
+    return p.launch(a, plan_passes(p, a), stream);
 }
 
 }  // namespace w2a8

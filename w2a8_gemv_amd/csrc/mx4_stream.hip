@@ -303,31 +303,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void mx4_stream_kernel(Mx4Launch a)
     }
 }
 
-// Waves of a workgroup.  A CU holds as many waves as its LDS holds pairs of
-// stages (16, 8 or 5 by M).  With a strip or less for every CU the waves of a
-// strip are all there is to keep loads on their way; beyond, few waves to a
-// strip (shorter sums, and a wave that streams on), but no more than let all
-// strips start at once.  Measured (MI355X, us, cold weights): M = 1, 5120 x
-// 27648 MX4, 320 strips: 3 waves 16.7, 8 waves 17.9; 55296 x 5120 28.4 against
-// 30.9; ternary, 160 strips: 8 waves 10.2, 4 waves 11.7.  M = 16, 55296 x 5120
-// ternary: 1 wave 16.7, 2 waves 19.6, 5 waves 27 or more; 13824 x 2560 MX4: 2
-// waves 6.6, 5 waves 7.8; 8192 x 27648 ternary, 256 strips: 5 waves 15.8, 2
-// waves 18.5.  M = 17, 256 strips: 8192 x 13824 ternary: 3 waves 9.8, 2 waves
-// 11.7, 1 wave 17.4; 290 strips, 9280 x 5120: 2 waves 7.4, 1 wave 8.6, 3 waves
-// 9.4; 563 strips, 9000 x 2560 MX4: 1 wave 6.2, 2 waves 7.6.
-int stream_waves(int M, int strips, int KU, int cus) {
-    const bool many = strips > cus;
-    const int nw = M == 1    ? (many ? 3 : kMaxWaves)
-                   : M <= 16 ? (strips >= 4 * cus ? 1 : many ? 2 : 5)
-                             : (strips > 2 * cus ? 1 : many ? 2 : 3);
-    return std::min(nw, KU);
-}
-
 template <int KIND, int SRC>
 hipError_t stream_launch(Mx4Launch a, int cus, hipStream_t stream) {
     using S = Stream<KIND, SRC>;
     a.strips = int(ceil_div(a.N, 16 * S::RB));
-    const int nw = stream_waves(a.M, a.strips, a.KU, cus);
+    const int nw = mx4_stream_waves(a.M, a.strips, a.KU, cus);
     a.stages = int(std::min<int64_t>(kDepth, ceil_div(a.KU, nw)));
     const int64_t gx = std::min<int64_t>(a.strips, int64_t(1) << 20);
     const dim3 grid(unsigned(gx), unsigned(ceil_div(a.strips, gx)));
@@ -352,6 +332,26 @@ hipError_t stream_fused(const Mx4Launch &a, int type, int cus, hipStream_t strea
 }
 
 }  // namespace
+
+// Waves of a workgroup.  A CU holds as many waves as its LDS holds pairs of
+// stages (16, 8 or 5 by M).  With a strip or less for every CU the waves of a
+// strip are all there is to keep loads on their way; beyond, few waves to a
+// strip (shorter sums, and a wave that streams on), but no more than let all
+// strips start at once.  Measured (MI355X, us, cold weights): M = 1, 5120 x
+// 27648 MX4, 320 strips: 3 waves 16.7, 8 waves 17.9; 55296 x 5120 28.4 against
+// 30.9; ternary, 160 strips: 8 waves 10.2, 4 waves 11.7.  M = 16, 55296 x 5120
+// ternary: 1 wave 16.7, 2 waves 19.6, 5 waves 27 or more; 13824 x 2560 MX4: 2
+// waves 6.6, 5 waves 7.8; 8192 x 27648 ternary, 256 strips: 5 waves 15.8, 2
+// waves 18.5.  M = 17, 256 strips: 8192 x 13824 ternary: 3 waves 9.8, 2 waves
+// 11.7, 1 wave 17.4; 290 strips, 9280 x 5120: 2 waves 7.4, 1 wave 8.6, 3 waves
+// 9.4; 563 strips, 9000 x 2560 MX4: 1 wave 6.2, 2 waves 7.6.
+int mx4_stream_waves(int M, int strips, int KU, int cus) {
+    const bool many = strips > cus;
+    const int nw = M == 1    ? (many ? 3 : kMaxWaves)
+                   : M <= 16 ? (strips >= 4 * cus ? 1 : many ? 2 : 5)
+                             : (strips > 2 * cus ? 1 : many ? 2 : 3);
+    return std::min(nw, KU);
+}
 
 hipError_t launch_mx4_stream(const Mx4Launch &a, int cus, hipStream_t stream) {
     return a.ws ? stream_rows<kMx4Weights>(a, cus, stream) : stream_rows<kTernary>(a, cus, stream);
