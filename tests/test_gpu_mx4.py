@@ -546,3 +546,49 @@ def test_rows_of_another_k_are_refused(kind):
     values = w2a8.dequant_act_mx4(q, sc, K)
     assert torch.equal(w2a8.dequant_act_mx4(torch.cat([q, q]).view(-1), flat, K, M), values)
     assert torch.equal(w2a8.dequant_act_mx4(q, flat, K), values)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M", [1, 20, 150])
+def test_single_products_at_the_ends_of_fp32(M, kind):
+    """One product of other than 0 to each output: products of 4-bit values
+    (multiples of 1/4, at most six bits) are exact from the smallest subnormal
+    up to fp32's largest value; from 2^128 on they are infinities of their
+    sign.  (A value below 2^128 of six bits is below fp32's largest.)"""
+    N, K = 40, 160
+    rng = np.random.default_rng(M)
+    c = np.zeros((M, K), np.uint8)
+    c[np.arange(M), 7 * np.arange(M) % K] = rng.integers(0, 16, M)
+    scale_pairs = (((254, 250), (254, 128), (252, 127), (190, 191), (27, 80), (0, 107)) if kind == "w4"
+                   else ((254, 127), (253, 127), (251, 127), (0, 127), (1, 127)))
+    for sx, sw in scale_pairs:
+        s = np.full((M, 5), sx, np.uint8)
+        if kind == "w4":
+            wc = rng.integers(0, 16, (N, K)).astype(np.uint8)
+            ws = np.full((N, 5), sw, np.uint8)
+            wp, w = to_dev(mx4.packed_layout(wc, ws)), mx4.values(wc, ws)
+        else:
+            wp, w = weights(kind, N, K, 9)
+        want = mx4.values(c, s) @ w.T
+        assert ((np.abs(want) >= 2.0 ** 128) | (np.abs(want) <= np.finfo(np.float32).max)).all()
+        with np.errstate(over="ignore"):
+            want = torch.from_numpy(want.astype(np.float32)).to(dev())
+        yf, yb = gemm(kind, wp, *on_device(c, s), M, N, K)
+        assert torch.equal(yf, want), (sx, sw)
+        assert torch.equal(yb, want.to(torch.bfloat16)), (sx, sw)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("M", [1, 20, 150])
+def test_sums_past_fp32_are_infinities_of_their_sign(M, kind):
+    """Products of one sign, each below fp32's largest value, the sum above it."""
+    N, K = 40, 1000
+    sign = np.arange(M)[:, None] % 2
+    c = np.broadcast_to(2 + 8 * sign, (M, K)).astype(np.uint8)           # 1 and -1
+    s = np.full((M, -(-K // 32)), 254, np.uint8)                        # 2^127
+    wc, ws = np.full((N, K), 2, np.uint8), np.full((N, -(-K // 32)), 127, np.uint8)
+    wp = (to_dev(mx4.packed_layout(wc, ws)) if kind == "w4"
+          else packed_on_device(np.ones((N, K), np.int8)))
+    yf, yb = gemm(kind, wp, *on_device(c, s), M, N, K)
+    want = torch.where(torch.from_numpy(sign == 1), -float("inf"), float("inf")).to(dev()).expand(M, N)
+    assert torch.equal(yf, want) and torch.equal(yb.float(), want)
