@@ -2,6 +2,9 @@
 the host packers and size queries against it, and the refusals of every entry
 point (rejected before any HIP call: the stand-in pointers are never read)."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -9,6 +12,7 @@ import torch
 
 import mx4_sizes
 import w2a8_gemv_amd as w2a8
+from conftest import ROOT
 from oracle import mx4
 
 NULL, SHAPE, ALIGN, VALUE, BUFSIZE = 1, 2, 3, 4, 5
@@ -292,3 +296,19 @@ def test_test_sizes_reach_every_form_of_the_stream(kind):
         p = w2a8.mx4_plan(*size, mx4_sizes.CUS, kind == "w2")
         assert p == (1, rows, 32 if kind == "w2" else 16, waves, 0), size
         assert -(-size[2] // 512) >= 3 * waves, size
+
+
+# ---------------------------------------------------------------------------
+# sources
+# ---------------------------------------------------------------------------
+@pytest.mark.skipif(shutil.which("hipcc") is None, reason="needs hipcc")
+def test_kernels_claim_no_alignment_that_rows_lack():
+    """Rows of results start wherever N puts them: no 16-byte access may be
+    made through a pointer whose type claims 16-byte alignment."""
+    csrc = os.path.join(ROOT, "w2a8_gemv_amd", "csrc")
+    srcs = [os.path.join(csrc, f) for f in sorted(os.listdir(csrc)) if "mx4" in f and f.endswith(".hip")]
+    assert len(srcs) == 5
+    res = subprocess.run(["hipcc", "--offload-arch=gfx950", "-std=c++17", "-fsyntax-only",
+                          "-Werror=align-mismatch", "-I", os.path.join(ROOT, "include"), "-I", csrc, *srcs],
+                         capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stderr[-2000:]

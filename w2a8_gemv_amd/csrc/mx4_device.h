@@ -115,9 +115,17 @@ __device__ __forceinline__ int mx4_out_at(int row, int chunk) {
     return SWIZZLE ? row * COLS + 4 * (chunk ^ (row & 7)) : row * (COLS + 4) + 4 * chunk;
 }
 
-// 16 bytes of a result row; PASS: past the caches.
-template <bool PASS, class V>
-__device__ __forceinline__ void mx4_store16(V *y, V v) {
+// 16 bytes of a result row; PASS: past the caches.  (Two functions: a template
+// argument would drop the pointer's alignment, that of one element.)
+template <bool PASS>
+__device__ __forceinline__ void mx4_store16(v4f_any *y, v4f v) {
+    if constexpr (PASS)
+        __builtin_nontemporal_store(v, y);
+    else
+        *y = v;
+}
+template <bool PASS>
+__device__ __forceinline__ void mx4_store16(v4u_any *y, v4u v) {
     if constexpr (PASS)
         __builtin_nontemporal_store(v, y);
     else
@@ -130,7 +138,7 @@ __device__ __forceinline__ void mx4_store_bf16(const Mx4Launch &a, int m, int n,
     if (m >= a.M || n >= a.N) return;
     uint16_t *y = a.y_bf16 + int64_t(m) * a.N + n;
     if (n + 7 < a.N) {
-        mx4_store16<PASS>(reinterpret_cast<v4u_any *>(y), v4u_any(w));
+        mx4_store16<PASS>(reinterpret_cast<v4u_any *>(y), w);
         return;
     }
     for (int e = 0; n + e < a.N; ++e) {
@@ -155,7 +163,7 @@ __device__ __forceinline__ void mx4_store_rows(const Mx4Launch &a, const uint8_t
             if (mb + row >= a.M || n >= a.N) continue;
             float *y = a.y_f32 + int64_t(mb + row) * a.N + n;
             if (n + 3 < a.N)
-                mx4_store16<PASS>(reinterpret_cast<v4f_any *>(y), v4f_any(v));
+                mx4_store16<PASS>(reinterpret_cast<v4f_any *>(y), v);
             else
                 for (int e = 0; n + e < a.N; ++e) y[e] = e == 0 ? v[0] : e == 1 ? v[1] : v[2];
         }
