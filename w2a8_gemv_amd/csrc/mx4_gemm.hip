@@ -397,7 +397,7 @@ hipError_t gemm_launch(const Mx4Launch &a, bool pass, hipStream_t stream) {
     const int64_t gx = std::min<int64_t>(blocks, int64_t(1) << 20);
     const dim3 grid(unsigned(gx), unsigned(ceil_div(blocks, gx)));
     void *args[] = {const_cast<Mx4Launch *>(&a), &gr};
-    // (Grids of split k are small: their results always pass.)
+    // (Where k is split, results always pass: plan_passes.)
     const void *kernel = reinterpret_cast<const void *>(&mx4_gemm_kernel<KIND, WM, WN, MB, KS, true>);
     if constexpr (KS == 1) {
         if (!pass)
@@ -481,6 +481,11 @@ const Plan &best_plan(const Plan (&plans)[N], const Mx4Launch &a, int cus) {
 const Plan &best_plan(const Mx4Launch &a, int cus) {
     return a.ws ? best_plan(kMx4Plans, a, cus) : best_plan(kTernaryPlans, a, cus);
 }
+// Tiles that split k serve large outputs too, tall ones of few columns; their
+// results pass by any sizes.  Measured (MI355X, us, passing and staying, 64 x 128
+// over two where results_pass says stay): fp32, MX4: 2217 x 3636 x 919 19.0 and
+// 19.6, 72177 x 104 x 1096 23.8 and 24.9; ternary 16.4 and 16.3, 20.4 and 21.5;
+// bf16, 38044 x 344 x 985: MX4 23.0 and 25.0, ternary 20.0 and 20.0.
 bool plan_passes(const Plan &p, const Mx4Launch &a) { return p.KS > 1 || results_pass(a); }
 
 }  // namespace
