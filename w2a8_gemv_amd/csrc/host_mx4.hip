@@ -45,7 +45,14 @@ Place place(int64_t n, int64_t b, int64_t NS, int64_t KT, int64_t KU) {
 // 36.7 and 33.0, 46.0 and 34.4; ternary, M = 16, 17 and 32: 16.7 and 19.9, 21.7
 // and 20.2, 27.1 and 20.5; 27648 columns, MX4, 320 strips, M = 16, 24 and 32:
 // 25.4 and 32.3, 32.0 and 29.9, 35.8 and 31.2, 256 strips: 17.1 and 30.8, 19.5
-// and 27.5, 20.9 and 29.4; ternary, 320 strips, M = 32: 34.7 and 31.1.
+// and 27.5, 20.9 and 29.4; ternary, 320 strips, M = 32: 34.7 and 31.1.  With
+// three and five strips to a compute unit and k = 27648, MX4, the two are close:
+// M = 24: 43.6 and 47.6, 80.1 and 79.3, M = 32: 48.8 and 50.7, 87.9 and 84.6.
+// The limits are coarse where a matrix is larger still.  On the stream's side
+// of them, but faster in tiles: 40000 columns, MX4, M = 32: k = 13824 86.5 and
+// 72.1, 27648 165 and 134.  In tiles, but faster in the stream: 40960 x 2560,
+// MX4, M = 8 and 16: 13.4 and 16.1, 14.1 and 17.0; ternary, M = 17: 10.9 and
+// 12.7.
 int stream_rows(const Mx4Launch &a, int cus) {
     const bool ternary = !a.ws;
     if (a.N >= 160 * int64_t(cus)) return ternary ? 16 : 4;

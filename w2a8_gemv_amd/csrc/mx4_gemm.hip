@@ -406,14 +406,20 @@ hipError_t gemm_launch(const Mx4Launch &a, bool pass, hipStream_t stream) {
     return hipLaunchKernel(kernel, grid, dim3(T::THREADS), args, 0, stream);
 }
 
-// What a launch takes in us, from its tiles and the device alone: workgroups
-// run Q to a compute unit; a compute unit's full turns and its last one, of m
-// workgroups, each cost E a workgroup (filling, writing results) and per k-tile
-// the larger of L (a lone workgroup's latency) and B a workgroup (what the
-// compute unit gets through).  The numbers are fitted to all tile shapes at
-// 150 sizes (M 33 to 4096, N 512 to 55296, K 512 to 27648, cold weights); the
-// choice by them is 0.9% (MX4) and 0.4% (ternary) behind the best tile on
-// average.  Both sides, us: MX4 512 x 2560 x 6912: 64 x 128 split over two
+// An estimate of what a launch takes in us, from its tiles and the device
+// alone: a compute unit takes its workgroups in turns of Q and a last one of m;
+// each turn costs E a workgroup (filling, writing results) and per k-tile the
+// larger of L (a lone workgroup's latency) and B a workgroup (what the compute
+// unit gets through).  All five numbers are fitted (least squares of the
+// logarithm) to each tile's times at 150 sizes (M 33 to 4096, N 512 to 55296,
+// K 512 to 27648, cold weights, bf16 results), Q as well: it is no occupancy.
+// By LDS a compute unit holds one workgroup of 256 x 256, of ternary 16 x 64
+// and of 32 x 128, two of ternary 64 x 128, three of MX4 16 x 64, fewer than
+// their Q; where L is 0 that changes nothing, at ternary 64 x 128 the estimate
+// of a third workgroup is 6% too low, at MX4 16 x 64 that of a fourth 1%.  The
+// bytes of results are in it only as far as they go with the tiles.  The choice
+// by it is 0.9% (MX4) and 0.4% (ternary) behind the best tile on average, 13%
+// at most.  Both sides, us: MX4 512 x 2560 x 6912: 64 x 128 split over two
 // groups 14.0, 64 x 256 19.4, 128 x 256 26.1; 512 x 13824 x 2560: 128 x 256
 // 18.7, 64 x 256 23.3, 32 x 256 34.3; 64 x 5120 x 27648: 32 x 64 over four
 // groups 37.2, 64 x 256 104.  Ternary 512 x 2560 x 6912: 64 x 128 over two

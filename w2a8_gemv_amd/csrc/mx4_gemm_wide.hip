@@ -4,11 +4,14 @@
 //
 // The other tiles (mx4_gemm.hip) load a weight byte once for every 128 rows
 // or fewer; 8192 x 13824 x 5120 takes them 315 us (128 x 256), and this kernel
-// 292 us, 2048 x 5120 x 27648 217 and 161 us.  What bounds it is power first
-// (the same product of zeros takes 227 us): twice the k adds 2560 k in 121 us,
-// 6.0 PFLOP/s of the 7.35 that the instruction alone sustains on random
-// operands.  A tile's start and results, 7 us, are hidden by nothing: one
-// workgroup fills the compute unit.  Keeping workgroups and starting the next
+// 292 us, 2048 x 5120 x 27648 217 and 161 us.  Where the 292 us go: the loop
+// gets through k at 4.9 to 5.1 PFLOP/s (2560 more of k take 113 us, 5120 more
+// 235 us), which is 230 us for this k, where the instruction alone takes 160
+// (7.2 to 7.4 PFLOP/s on rounded normal values; 9.8 on zeros, where the clock
+// stays up).  So some 70 us are the loop's stalls and the idle quarter of the
+// last of seven turns of tiles, and some 60 their starts and results, hidden by
+// nothing: one workgroup fills the compute unit.  Power costs 65 us of the whole: the same product of
+// zeros takes 227.  Keeping workgroups and starting the next
 // tile's loads ahead of the results was tried (the registers of both do not
 // fit, 350 us), as were results straight from the registers (fp32 324 against
 // 313 us) and all of a wave's results through LDS at once (no change).

@@ -336,8 +336,10 @@ hipError_t stream_fused(const Mx4Launch &a, int type, int cus, hipStream_t strea
 // Waves of a workgroup.  A CU holds as many waves as its LDS holds pairs of
 // stages (16, 8 or 5 by M).  With a strip or less for every CU the waves of a
 // strip are all there is to keep loads on their way; beyond, few waves to a
-// strip (shorter sums, and a wave that streams on), but no more than let all
-// strips start at once.  Measured (MI355X, us, cold weights): M = 1, 5120 x
+// strip (shorter sums, and a wave that streams on).  For short batches that
+// lets all strips of most matrices start at once; at M = 1 the strips of the
+// largest start in turns (55296 rows: 3456 strips of three waves, 2.5 turns).
+// Measured (MI355X, us, cold weights): M = 1, 5120 x
 // 27648 MX4, 320 strips: 3 waves 16.7, 8 waves 17.9; 55296 x 5120 28.4 against
 // 30.9; ternary, 160 strips: 8 waves 10.2, 4 waves 11.7.  M = 16, 55296 x 5120
 // ternary: 1 wave 16.7, 2 waves 19.6, 5 waves 27 or more; 13824 x 2560 MX4: 2

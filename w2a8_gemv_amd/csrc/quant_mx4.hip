@@ -83,7 +83,10 @@ __device__ __forceinline__ void place_item(const Rows &t, int64_t *row, int *ite
 }
 
 // PACK: the row is row m of the weights and goes to MX16x128 (rows N ..
-// 16*NS - 1 are padding), otherwise to MX4R.
+// 16*NS - 1 are padding), otherwise to MX4R.  A row's 16 bytes of a block lie
+// 256 bytes apart there, and its scale bytes 256: 13824 x 5120 takes 68 us in
+// bf16 and 101 in fp32, where the same rows to MX4R take 39 and 68 (5125 GB/s,
+// a large copy's rate: 35 and 63).  It is done once for a matrix.
 template <int TYPE, bool PACK>
 __global__ __launch_bounds__(256) void quant_mx4_kernel(const void *x, Rows t, uint8_t *xq,
                                                         uint8_t *xs) {
