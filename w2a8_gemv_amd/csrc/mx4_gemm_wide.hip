@@ -10,11 +10,11 @@
 // (7.2 to 7.4 PFLOP/s on rounded normal values; 9.8 on zeros, where the clock
 // stays up).  So some 70 us are the loop's stalls and the idle quarter of the
 // last of seven turns of tiles, and some 60 their starts and results, hidden by
-// nothing: one workgroup fills the compute unit.  Power costs 65 us of the whole: the same product of
-// zeros takes 227.  Keeping workgroups and starting the next
-// tile's loads ahead of the results was tried (the registers of both do not
-// fit, 350 us), as were results straight from the registers (fp32 324 against
-// 313 us) and all of a wave's results through LDS at once (no change).
+// nothing: one workgroup fills the compute unit.  Power costs 65 us of the
+// whole: the same product of zeros takes 227.  Keeping workgroups and starting
+// the next tile's loads ahead of the results was tried (the registers of both
+// do not fit, 350 us), as were results straight from the registers (fp32 324
+// against 313 us) and all of a wave's results through LDS at once (no change).
 //
 //  * Both operands go through LDS (each byte is loaded once per workgroup; a
 //    wave's 128 x 128 needs 16 KiB of LDS reads per 64 instructions, half of
