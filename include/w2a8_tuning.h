@@ -118,7 +118,7 @@ int w2a8_linear_plan(int64_t N, int64_t K, int cus, int int4, int *kernel, int *
 
 /* What w4mx4_gemm (ternary = 0) or w2mx4_gemm (ternary = 1; w2a8_mx4.h) runs
  * for (M, N, K) into fp32 (outputs = 1), bf16 (2) or both (3) on a device with
- * `cus` compute units.  *kernel: 1 the weight stream (*rows 1, 16 or 32
+ * `cus` (1..65536) compute units.  *kernel: 1 the weight stream (*rows 1, 16 or 32
  * activation rows of the kernel's form, *cols weight rows of a strip, *groups
  * waves that share a strip's k), 2 output tiles (*rows x *cols results of a
  * workgroup, *groups wave groups that split k; 256 x 256 is a kernel of its

@@ -254,7 +254,7 @@ def test_plan_query_refuses():
         assert L.w2a8_mx4_plan(*ok, *out[:i], None, *out[i + 1:]) == NULL
     for i, bad in ((0, 0), (1, 0), (2, 0), (0, (1 << 20) + 1), (1, (1 << 30) + 1), (2, 1048449)):
         assert L.w2a8_mx4_plan(*ok[:i], bad, *ok[i + 1:], *out) == SHAPE
-    for i, bad in ((4, 0), (4, 4), (5, 0)):
+    for i, bad in ((4, 0), (4, 4), (5, 0), (5, 65537), (5, (1 << 31) - 1)):
         assert L.w2a8_mx4_plan(*ok[:i], bad, *ok[i + 1:], *out) == VALUE
     with pytest.raises(w2a8.W2A8Error):
         w2a8.mx4_plan(40, 100, 200, 256, f32=False)

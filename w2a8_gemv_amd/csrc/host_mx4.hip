@@ -234,7 +234,7 @@ int w2a8_mx4_plan(int64_t M, int64_t N, int64_t K, int ternary, int outputs, int
                   int *rows, int *cols, int *groups, int *pass) {
     if (!kernel || !rows || !cols || !groups || !pass) return W2A8_ERR_NULL;
     if (!rows_ok(M, K) || !matrix_ok(N, K)) return W2A8_ERR_SHAPE;
-    if (cus < 1 || outputs < 1 || outputs > 3) return W2A8_ERR_VALUE;
+    if (cus < 1 || cus > 65536 || outputs < 1 || outputs > 3) return W2A8_ERR_VALUE;
     // (The plans ask whether there are MX4 scales and which outputs, not where.)
     alignas(16) static uint8_t some[16];
     Mx4Launch a = {};
