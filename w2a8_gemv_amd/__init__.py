@@ -30,7 +30,8 @@ __all__ = [
     "mx4_act_bytes", "mx4_scale_bytes", "mx4_packed_bytes", "pack_mx4", "unpack_mx4",
     "quant_act_mx4", "dequant_act_mx4", "quant_pack_mx4", "w4mx4_gemm", "w2mx4_gemm",
     "w4mx4_linear_gemv", "w2mx4_linear_gemv", "gemm_w4mx4", "gemm_w2mx4", "linear_w4mx4",
-    "linear_w2mx4",
+    "linear_w2mx4", "rmsnorm_quant_int8", "w4a8_packed_bytes", "pack_w4a8", "unpack_w4a8",
+    "w4a8_gemm", "gemm_w4a8", "linear_w4a8", "w2a8_moe_workspace_bytes", "w2a8_moe", "moe",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw2a8.so")
@@ -110,6 +111,18 @@ def lib():
                            ("w2mx4_gemm", [P, P, P, I64, I64, I64, F32, P, P, P]),
                            ("w4mx4_linear_gemv", [P, P, I32, I64, I64, P, P, P]),
                            ("w2mx4_linear_gemv", [P, P, I32, I64, I64, F32, P, P, P])):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = I32
+        L.w4a8_packed_bytes.argtypes = [I64, I64, I64, I32]
+        L.w4a8_packed_bytes.restype = I64
+        L.w2a8_moe_workspace_bytes.argtypes = [I64] * 5
+        L.w2a8_moe_workspace_bytes.restype = I64
+        for name, args in (("rmsnorm_quant_int8", [P, P, P, I32, I64, I64, F32, P, P, P, P]),
+                           ("pack_w4a8", [P, P, P, I64, I64, I64, P, I64]),
+                           ("unpack_w4a8", [P, I64, I64, I64, I64, P, P, P]),
+                           ("w4a8_gemm", [P, P, P, I64, I64, I64, I64, I32, I32, P, P, P]),
+                           ("w2a8_moe", [P, P, P, I32, P, P, P, P, P, P, I64, I64, I64, I64, I64,
+                                         I32, I32, P, P, P, I64, P])):
             getattr(L, name).argtypes = args
             getattr(L, name).restype = I32
         L.w2a8_tune_gemv.argtypes = [I32, I32, I32, I32, I32]
@@ -908,6 +921,216 @@ def linear_w4mx4(x, w_packed, N, K, out_dtype=torch.float32, stream=None, fused=
 def linear_w2mx4(x, w_packed, s_w, N, K, out_dtype=torch.float32, stream=None, fused=True):
     """Linear layer with packed ternary weights and MX4 activations (as linear_w4mx4)."""
     return _mx4_linear(x, w_packed, float(s_w), N, K, out_dtype, stream, fused)
+
+
+# ---------------------------------------------------------------------------
+# Around the ternary layers: norm into int8 rows, 4-bit weights with group
+# scales, mixture of ternary experts (see include/w2a8_block.h)
+# ---------------------------------------------------------------------------
+def rmsnorm_quant_int8(x: torch.Tensor, weight=None, residual=None, eps: float = 1e-5, x_q=None,
+                       s_a=None, h=None, stream=None):
+    """Root-mean-square norm of x (+ residual), fp32, bf16 or fp16 [M, K] (or [K]: one row;
+    device), times weight [K], into int8 rows: (x_q int8 [M, K], s_a fp32 [M], h).
+
+    h is x + residual in their type, which the next block adds to (x itself without a
+    residual); h=residual or h=x writes it in place.  x_q * s_a is the normalised row."""
+    code, dev = _mx4_type(x, "x"), _mx4_gpu(x, "x")
+    M, K = _mx4_rows(x, "x")
+    pw = None if weight is None else _mx4_ptr(weight, "weight", dev, x.dtype, K, K)
+    pr = ph = None
+    if residual is not None:
+        pr = _mx4_ptr(residual, "residual", dev, x.dtype, M * K, M * K)
+        if h is None:
+            h = _mx4_empty(x, x.shape, x.dtype, stream)
+        ph = _mx4_ptr(h, "h", dev, x.dtype, M * K, M * K)
+    elif h is not None:
+        raise ValueError("h is given without a residual")
+    else:
+        h = x
+    if x_q is None:
+        x_q = _mx4_empty(x, (M, K), torch.int8, stream)
+        pq = x_q.data_ptr()
+    else:
+        pq = _mx4_ptr(x_q, "x_q", dev, torch.int8, M * K, M * K)
+    if s_a is None:
+        s_a = _mx4_empty(x, (M,), torch.float32, stream)
+        ps = s_a.data_ptr()
+    else:
+        ps = _mx4_ptr(s_a, "s_a", dev, torch.float32, M, M)
+    st = lib().rmsnorm_quant_int8(x.data_ptr(), pr, pw, code, M, K, eps, ph, pq, ps,
+                                  _mx4_stream(stream, dev))
+    if st:
+        raise W2A8Error(st, "rmsnorm_quant_int8")
+    return x_q, s_a, h
+
+
+@functools.lru_cache(maxsize=4096)
+def w4a8_packed_bytes(N: int, K: int, group: int, zeros: bool = False) -> int:
+    """Bytes of packed 4-bit weights with group scales (W4T16x128)."""
+    v = int(lib().w4a8_packed_bytes(N, K, group, int(bool(zeros))))
+    if v < 0:
+        raise W2A8Error(2, "w4a8_packed_bytes")
+    return v
+
+
+def _w4_scale_type(dtype):
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise TypeError(f"scales must be float16 or bfloat16, got {dtype}")
+    return _MX4_TYPES[dtype]
+
+
+def pack_w4a8(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int, group: int,
+              zeros=None) -> torch.Tensor:
+    """Interchange form (CPU): codes uint8 [N, ceil(K/2)], two values a byte, the lower k in
+    the lower half, scales fp16 or bf16 [N, ceil(K/group)] and zeros uint8 of that shape, or
+    None (the zero point is 8) -> packed uint8 [w4a8_packed_bytes] (CPU)."""
+    out = torch.empty(w4a8_packed_bytes(N, K, group, zeros is not None), dtype=torch.uint8)
+    groups = -(-K // group)
+    _need(codes, "codes", torch.uint8, "cpu", (N, -(-K // 2)))
+    if not isinstance(scales, torch.Tensor):
+        raise TypeError("scales must be a torch.Tensor")
+    _w4_scale_type(scales.dtype)
+    _need(scales, "scales", scales.dtype, "cpu", (N, groups))
+    if zeros is not None:
+        _need(zeros, "zeros", torch.uint8, "cpu", (N, groups))
+    _check(lib().pack_w4a8(_ptr(codes), _ptr(scales), _ptr(zeros), N, K, group, _ptr(out),
+                           out.numel()), "pack_w4a8")
+    return out
+
+
+def unpack_w4a8(packed: torch.Tensor, N: int, K: int, group: int, scale_dtype=torch.float16,
+                zeros: bool = False):
+    """Packed 4-bit weights (CPU) -> (codes, scales, zeros or None) in the interchange form."""
+    _need(packed, "packed", torch.uint8, "cpu")
+    w4a8_packed_bytes(N, K, group, zeros)
+    _w4_scale_type(scale_dtype)
+    groups = -(-K // group)
+    codes = torch.empty((N, -(-K // 2)), dtype=torch.uint8)
+    scales = torch.empty((N, groups), dtype=scale_dtype)
+    z = torch.empty((N, groups), dtype=torch.uint8) if zeros else None
+    _check(lib().unpack_w4a8(_ptr(packed), packed.numel(), N, K, group, _ptr(codes), _ptr(scales),
+                             _ptr(z)), "unpack_w4a8")
+    return codes, scales, z
+
+
+def _w4_gemm(w_packed, x, s_a, M, N, K, group, scale_dtype, zeros, yf, yb, dev, stream):
+    pw = _mx4_ptr(w_packed, "w_packed", dev, torch.uint8, w4a8_packed_bytes(N, K, group, zeros))
+    px = _mx4_ptr(x, "x", dev, torch.int8, M * K, M * K)
+    ps = _mx4_ptr(s_a, "s_a", dev, torch.float32, M, M)
+    st = lib().w4a8_gemm(pw, px, ps, M, N, K, group, _w4_scale_type(scale_dtype), int(bool(zeros)),
+                         yf, yb, _mx4_stream(stream, dev))
+    if st:
+        raise W2A8Error(st, "w4a8_gemm")
+
+
+def w4a8_gemm(w_packed, x, s_a, M, N, K, group, scale_dtype=torch.float16, zeros=False, y_f32=None,
+              y_bf16=None, stream=None):
+    """Raw C-ABI call: int8 rows times 4-bit weights with group scales (outputs must be
+    given); returns nothing."""
+    dev = _mx4_gpu(x, "x")
+    yf, yb = _mx4_outputs(y_f32, y_bf16, dev, M * N)
+    _w4_gemm(w_packed, x, s_a, M, N, K, group, scale_dtype, zeros, yf, yb, dev, stream)
+
+
+def gemm_w4a8(w_packed, x_q, s_a, N, K, group, scale_dtype=torch.float16, zeros=False,
+              out_dtype=torch.float32, stream=None):
+    """int8 rows x_q [M, K] (or [K]: one row) of scales s_a [M] times 4-bit weights with group
+    scales -> fp32 or bf16 [M, N], M <= 64.  scale_dtype and zeros: of the packed weights."""
+    dev = _mx4_gpu(x_q, "x_q")
+    M, k = _mx4_rows(x_q, "x_q")
+    if k != K:
+        raise ValueError(f"x_q must have rows of {K} values, got {k}")
+    y, yf, yb = _mx4_new(x_q, out_dtype, (M, N), stream)
+    _w4_gemm(w_packed, x_q, s_a, M, N, K, group, scale_dtype, zeros, yf, yb, dev, stream)
+    return y
+
+
+def linear_w4a8(x_bf16, w_packed, N, K, group, scale_dtype=torch.float16, zeros=False,
+                out_dtype=torch.float32, stream=None):
+    """Linear layer with 4-bit weights: bf16 rows [M, K] (or [K]) -> fp32 or bf16 [M, N];
+    quant_act_int8, then w4a8_gemm."""
+    _mx4_gpu(x_bf16, "x_bf16")
+    M, k = _mx4_rows(x_bf16, "x_bf16")
+    if k != K:
+        raise ValueError(f"x_bf16 must have rows of {K} values, got {k}")
+    x_q, s_a = (_mx4_empty(x_bf16, (M, K), torch.int8, stream),
+                _mx4_empty(x_bf16, (M,), torch.float32, stream))
+    quant_act_int8(x_bf16, x_q, s_a, stream=stream)
+    return gemm_w4a8(w_packed, x_q, s_a, N, K, group, scale_dtype, zeros, out_dtype, stream)
+
+
+_ACTIVATIONS = {"silu": 0, "relu2": 1}
+
+
+@functools.lru_cache(maxsize=4096)
+def _moe_sizes(M, H, I, E, top_k):
+    """Bytes of the workspace and of an expert's w_gate (or w_up) and w_down."""
+    ws = int(lib().w2a8_moe_workspace_bytes(M, H, I, E, top_k))
+    if ws < 0:
+        raise W2A8Error(2, "w2a8_moe")
+    return ws, packed_bytes(I, H), packed_bytes(H, I)
+
+
+def w2a8_moe_workspace_bytes(M: int, H: int, I: int, E: int, top_k: int) -> int:
+    """Workspace bytes of w2a8_moe (not to be cleared)."""
+    return _moe_sizes(M, H, I, E, top_k)[0]
+
+
+def _moe(x, s_a, logits, w_gate, w_up, w_down, s_gate, s_up, s_down, M, H, I, E, top_k, activation,
+         renormalize, yf, yb, pws, ws_bytes, dev, stream):
+    code = _mx4_type(logits, "logits")
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be 'silu' or 'relu2', got {activation!r}")
+    _, b1, b2 = _moe_sizes(M, H, I, E, top_k)
+    u8, f32 = torch.uint8, torch.float32
+    st = lib().w2a8_moe(
+        _mx4_ptr(x, "x", dev, torch.int8, M * H, M * H), _mx4_ptr(s_a, "s_a", dev, f32, M, M),
+        _mx4_ptr(logits, "logits", dev, logits.dtype, M * E, M * E), code,
+        _mx4_ptr(w_gate, "w_gate", dev, u8, E * b1, E * b1), _mx4_ptr(w_up, "w_up", dev, u8, E * b1, E * b1),
+        _mx4_ptr(w_down, "w_down", dev, u8, E * b2, E * b2), _mx4_ptr(s_gate, "s_gate", dev, f32, E, E),
+        _mx4_ptr(s_up, "s_up", dev, f32, E, E), _mx4_ptr(s_down, "s_down", dev, f32, E, E),
+        M, H, I, E, top_k, act, int(bool(renormalize)), yf, yb, pws, ws_bytes, _mx4_stream(stream, dev))
+    if st:
+        raise W2A8Error(st, "w2a8_moe")
+
+
+def w2a8_moe(x, s_a, logits, w_gate, w_up, w_down, s_gate, s_up, s_down, M, H, I, E, top_k,
+             activation="silu", renormalize=True, y_f32=None, y_bf16=None, workspace=None,
+             stream=None):
+    """Raw C-ABI call (outputs must be given; workspace: uint8, at least
+    w2a8_moe_workspace_bytes, made here if not given); returns nothing."""
+    dev = _mx4_gpu(x, "x")
+    yf, yb = _mx4_outputs(y_f32, y_bf16, dev, M * H)
+    need = _moe_sizes(M, H, I, E, top_k)[0]
+    if workspace is None:
+        workspace = _mx4_empty(x, (need,), torch.uint8, stream)
+    _moe(x, s_a, logits, w_gate, w_up, w_down, s_gate, s_up, s_down, M, H, I, E, top_k, activation,
+         renormalize, yf, yb, _mx4_ptr(workspace, "workspace", dev, torch.uint8, need),
+         workspace.numel(), dev, stream)
+
+
+def moe(x_q, s_a, logits, w_gate, w_up, w_down, s_gate, s_up, s_down, H, I, top_k,
+        activation="silu", renormalize=True, out_dtype=torch.float32, stream=None):
+    """Mixture of ternary experts: int8 rows x_q [M, H] (or [H]: one row) of scales s_a [M] and
+    router logits [M, E] (fp32, bf16 or fp16) -> fp32 or bf16 [M, H], M <= 64.
+
+    w_gate, w_up: uint8 [E, packed_bytes(I, H)], w_down: uint8 [E, packed_bytes(H, I)], an
+    expert a row (pack_ternary); s_gate, s_up, s_down: fp32 [E].  activation: "silu" or
+    "relu2" (squared ReLU).  renormalize: the top_k experts' weights add up to one."""
+    dev = _mx4_gpu(x_q, "x_q")
+    M, k = _mx4_rows(x_q, "x_q")
+    if k != H:
+        raise ValueError(f"x_q must have rows of {H} values, got {k}")
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    E = _mx4_rows(logits, "logits")[1]
+    need = _moe_sizes(M, H, I, E, top_k)[0]
+    y, yf, yb = _mx4_new(x_q, out_dtype, (M, H), stream)
+    ws = _mx4_empty(x_q, (need,), torch.uint8, stream)
+    _moe(x_q, s_a, logits, w_gate, w_up, w_down, s_gate, s_up, s_down, M, H, I, E, top_k, activation,
+         renormalize, yf, yb, ws.data_ptr(), need, dev, stream)
+    return y
 
 
 # ---------------------------------------------------------------------------

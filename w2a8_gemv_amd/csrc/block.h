@@ -1,0 +1,84 @@
+// Launchers and shared pieces of the operators of w2a8_block.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device.h"
+#include "mx4.h"
+#include "w2a8_block.h"
+
+namespace w2a8 {
+
+// Vectors at any alignment: rows of K bytes start wherever K puts them, and
+// global loads and stores of any width need no alignment on gfx950.
+typedef v4u v4u_b __attribute__((aligned(1)));
+typedef v2u v2u_b __attribute__((aligned(1)));
+typedef v4f v4f_b __attribute__((aligned(4)));
+
+// BYTES (8 or 16) consecutive int8 of a row from k on; those past K are 0.
+template <int BYTES>
+__device__ __forceinline__ void load_int8_tail(const int8_t *row, int k, int K, uint32_t *w) {
+    uint64_t v[2] = {0, 0};
+#pragma unroll 1
+    for (int b = 0; b < BYTES; ++b)
+        if (k + b < K) {
+            const uint64_t byte = uint64_t(uint8_t(row[k + b])) << (8 * (b & 7));
+            if (b < 8)
+                v[0] |= byte;
+            else
+                v[1] |= byte;
+        }
+#pragma unroll
+    for (int i = 0; i < BYTES / 4; ++i) w[i] = uint32_t(v[i >> 1] >> (32 * (i & 1)));
+}
+
+struct NormLaunch {
+    const void *x, *residual, *weight;
+    void *h;
+    int8_t *xq;
+    float *sa;
+    float eps;
+    int M, K;
+};
+hipError_t launch_rmsnorm_quant(const NormLaunch &a, int type, hipStream_t stream);
+
+// Products with 4-bit weights (W4T16x128).
+constexpr int kW4Rows = 16;
+constexpr int kW4TileBytes = 1024;
+inline int64_t w4_tiles(int64_t K) { return ceil_div(K, kTileK); }
+inline int64_t w4_group_quads(int64_t K, int64_t group) { return ceil_div(ceil_div(K, group), 4); }
+struct W4Launch {
+    const uint8_t *w;          // codes
+    const uint16_t *scales;
+    const uint8_t *zeros;      // or null
+    const int8_t *x;
+    const float *sa;
+    float *y_f32;
+    uint16_t *y_bf16;
+    int M, N, K, KT, GQ;
+    int group, bf16_scales, strips;
+};
+hipError_t launch_w4a8(const W4Launch &a, int cus, hipStream_t stream);
+
+// Mixture of experts: offsets into the workspace, all multiples of 256.
+struct MoeSpace {
+    int64_t slot, pair, amax, hidden, part, total;
+};
+MoeSpace moe_space(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k);
+struct MoeLaunch {
+    const int8_t *x;
+    const float *sa;
+    const void *logits;
+    const uint8_t *w_gate, *w_up, *w_down;
+    const float *s_gate, *s_up, *s_down;
+    float *y_f32;
+    uint16_t *y_bf16;
+    uint8_t *ws;
+    MoeSpace sp;
+    int64_t wb1, wb2;          // bytes of an expert's w_gate or w_up, w_down
+    int M, H, I, E, top_k, act, renormalize, logit_type;
+};
+hipError_t launch_moe(const MoeLaunch &a, int cus, hipStream_t stream);
+
+}  // namespace w2a8

@@ -3,24 +3,15 @@
 // before any HIP call.
 #include <cstring>
 
+#include "host_checks.h"
 #include "mx4.h"
 #include "w2a8_tuning.h"
 
 namespace w2a8 {
 namespace {
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool rows_ok(int64_t M, int64_t K) { return M >= 1 && M <= kMaxM && K >= 1 && K <= W2A8_MAX_K; }
 bool matrix_ok(int64_t N, int64_t K) { return N >= 1 && N <= kMaxN && K >= 1 && K <= W2A8_MAX_K; }
-bool type_ok(int t) { return t == W2A8_F32 || t == W2A8_BF16 || t == W2A8_F16; }
-
-// Do two buffers share bytes?  A kernel reads what others of its workgroups
-// have written by then, so outputs have to be apart from all other buffers.
-bool meet(const void *a, int64_t na, const void *b, int64_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + uint64_t(nb) && y < x + uint64_t(na);
-}
-int64_t type_bytes(int type) { return type == W2A8_F32 ? 4 : 2; }
 
 // Byte and half of value i (0..31) of a block's 16 code bytes.
 int code_byte(int i) { return (i / 16) * 8 + (i % 16 / 4 % 2) * 4 + i % 4; }

@@ -1,0 +1,284 @@
+// Root-mean-square norm with the residual's addition, into int8 rows (gfx950).
+//
+//   h = x + residual;  v = h * weight;  a = max |v|;
+//   q = rint(v * 127 / a);  s = a / 127 / sqrt(mean(h^2) + eps)
+//
+// The mean cancels from the codes (v / rms over max |v| / rms), so they need
+// one maximum and no sum, and come out the same in any order of reduction.
+// The sum of squares is in fp64: squares of fp32 values are exact there, and
+// none passes its range.
+//
+// Bound by memory: a row is read once, held in registers as v (fp32), reduced
+// over the workgroup, rounded and stored.  Rows past 32768 values are walked
+// twice, the second time from h.
+#include "block.h"
+
+namespace w2a8 {
+namespace {
+
+constexpr int kNormRowsMaxK = 32768;   // 4 chunks of 8 values for each of 1024 lanes
+
+__device__ __forceinline__ float half_value(uint32_t bits) {
+    return float(__builtin_bit_cast(_Float16, uint16_t(bits)));
+}
+__device__ __forceinline__ uint32_t half_bits(float v) {
+    return uint32_t(__builtin_bit_cast(uint16_t, _Float16(v)));
+}
+
+// Values i..i+7 of a float row (at any alignment of its elements).
+template <int TYPE>
+__device__ __forceinline__ void load8(const void *p, int64_t i, float (&v)[8]) {
+    if constexpr (TYPE == W2A8_F32) {
+        const float *f = static_cast<const float *>(p) + i;
+        const v4f a = *reinterpret_cast<const v4f_b *>(f), b = *reinterpret_cast<const v4f_b *>(f + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = a[j];
+            v[4 + j] = b[j];
+        }
+    } else {
+        const v4u a = *reinterpret_cast<const v4u_any *>(static_cast<const uint16_t *>(p) + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = TYPE == W2A8_BF16 ? lo_bf16(a[j]) : half_value(a[j] & 0xFFFFu);
+            v[2 * j + 1] = TYPE == W2A8_BF16 ? hi_bf16(a[j]) : half_value(a[j] >> 16);
+        }
+    }
+}
+
+// Rounds v to TYPE, stores it as values i..i+7, and leaves the rounded values.
+template <int TYPE>
+__device__ __forceinline__ void store8(void *p, int64_t i, float (&v)[8]) {
+    if constexpr (TYPE == W2A8_F32) {
+        float *f = static_cast<float *>(p) + i;
+        *reinterpret_cast<v4f_b *>(f) = v4f{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<v4f_b *>(f + 4) = v4f{v[4], v[5], v[6], v[7]};
+    } else {
+        v4u w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = TYPE == W2A8_BF16 ? bf16_pair(v[2 * j], v[2 * j + 1])
+                                     : half_bits(v[2 * j]) | half_bits(v[2 * j + 1]) << 16;
+            v[2 * j] = TYPE == W2A8_BF16 ? lo_bf16(w[j]) : half_value(w[j] & 0xFFFFu);
+            v[2 * j + 1] = TYPE == W2A8_BF16 ? hi_bf16(w[j]) : half_value(w[j] >> 16);
+        }
+        *reinterpret_cast<v4u_any *>(static_cast<uint16_t *>(p) + i) = w;
+    }
+}
+
+template <int TYPE>
+__device__ __forceinline__ float store1(void *p, int64_t i, float v) {
+    if constexpr (TYPE == W2A8_F32) {
+        static_cast<float *>(p)[i] = v;
+        return v;
+    } else {
+        const uint32_t b = TYPE == W2A8_BF16 ? bf16_bits(v) : half_bits(v);
+        static_cast<uint16_t *>(p)[i] = uint16_t(b);
+        return TYPE == W2A8_BF16 ? lo_bf16(b) : half_value(b);
+    }
+}
+
+// Chunk c (8 values) of row m: h, stored, and v; values past K are 0.
+template <int TYPE>
+__device__ __forceinline__ void norm_chunk(const NormLaunch &a, int64_t row, int c, float (&v)[8],
+                                           double &sum) {
+    const int k = 8 * c;
+    if (k + 8 <= a.K) {
+        load8<TYPE>(a.x, row + k, v);
+        if (a.residual) {
+            float r[8];
+            load8<TYPE>(a.residual, row + k, r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += r[j];
+            store8<TYPE>(a.h, row + k, v);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += double(v[j]) * double(v[j]);
+        if (a.weight) {
+            float w[8];
+            load8<TYPE>(a.weight, k, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= w[j];
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        v[j] = 0.0f;
+        if (k + j >= a.K) continue;
+        float f = mx4_load1<TYPE>(a.x, row + k + j);
+        if (a.residual)
+            f = store1<TYPE>(a.h, row + k + j, f + mx4_load1<TYPE>(a.residual, row + k + j));
+        sum += double(f) * double(f);
+        v[j] = a.weight ? f * mx4_load1<TYPE>(a.weight, k + j) : f;
+    }
+}
+
+__device__ __forceinline__ void store_codes(const NormLaunch &a, int64_t row, int c,
+                                            const float (&v)[8], float inv) {
+    uint32_t o[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        o[i] = q8(v[4 * i], inv) | (q8(v[4 * i + 1], inv) << 8) | (q8(v[4 * i + 2], inv) << 16) |
+               (q8(v[4 * i + 3], inv) << 24);
+    int8_t *out = a.xq + row + 8 * c;
+    if (8 * c + 8 <= a.K) {
+        *reinterpret_cast<v2u_b *>(out) = v2u{o[0], o[1]};
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+        if (8 * c + j < a.K) out[j] = int8_t(o[j >> 2] >> (8 * (j & 3)));
+}
+
+template <int CTRL>
+__device__ __forceinline__ double add_moved(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(uint32_t(b)), CTRL, 0xF, 0xF, false));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(uint32_t(b >> 32)), CTRL, 0xF, 0xF, false));
+    return v + __builtin_bit_cast(double, (uint64_t(hi) << 32) | lo);
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(b)), lane));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(b >> 32)), lane));
+    return __builtin_bit_cast(double, (uint64_t(hi) << 32) | lo);
+}
+// Sum over the 64 lanes of a wave, wave-uniform (the moves of wave_max_nonneg).
+__device__ __forceinline__ double wave_sum64(double v) {
+    v = add_moved<0xB1>(v);
+    v = add_moved<0x4E>(v);
+    v = add_moved<0x124>(v);
+    v = add_moved<0x128>(v);
+    return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+
+// Maximum and sum over a workgroup of up to 16 waves.  amax is taken as bits:
+// a NaN is above infinity and infinity above all numbers.
+struct NormSums {
+    double sum[16];
+    float amax[16];
+};
+__device__ __forceinline__ void block_norm(NormSums &s, float &amax, double &sum) {
+    amax = wave_max_nonneg(amax);
+    sum = wave_sum64(sum);
+    const int nw = int(blockDim.x) >> 6;
+    if (nw == 1) return;
+    const int wv = int(threadIdx.x) >> 6;
+    if ((threadIdx.x & 63) == 0) {
+        s.amax[wv] = amax;
+        s.sum[wv] = sum;
+    }
+    __syncthreads();
+    int b = 0;
+    sum = 0.0;
+    for (int i = 0; i < nw; ++i) {
+        b = max(b, __float_as_int(s.amax[i]));
+        sum += s.sum[i];
+    }
+    amax = __int_as_float(b);
+}
+__device__ __forceinline__ float abs_max(float amax, float v) {
+    return __int_as_float(max(__float_as_int(amax), __float_as_int(v) & 0x7FFFFFFF));
+}
+
+// The factor of the codes, and the row's scale by one lane.
+__device__ __forceinline__ float norm_scale(const NormLaunch &a, int m, float amax, double sum) {
+    const bool fine = amax < __builtin_inff() && sum < __builtin_inf();
+    if (threadIdx.x == 0) {
+        const double rms = sqrt(sum / double(a.K) + double(a.eps));
+        a.sa[m] = !fine ? __builtin_nanf("") : amax == 0.0f ? 0.0f : float(double(amax) / 127.0 / rms);
+    }
+    return fine && amax != 0.0f ? fminf(127.0f / amax, __FLT_MAX__) : 0.0f;
+}
+
+// One workgroup per row, CPL chunks of 8 values per lane.
+template <int TYPE, int CPL>
+__global__ __launch_bounds__(1024) void norm_rows_kernel(NormLaunch a) {
+    __shared__ NormSums red;
+    const int tid = int(threadIdx.x), bd = int(blockDim.x), m = int(blockIdx.x);
+    const int nc = (a.K + 7) >> 3;
+    const int64_t row = int64_t(m) * a.K;
+    float v[CPL][8], amax = 0.0f;
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+        if (tid + i * bd < nc) norm_chunk<TYPE>(a, row, tid + i * bd, v[i], sum);
+    }
+#pragma unroll
+    for (int i = 0; i < CPL; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = abs_max(amax, v[i][j]);
+    block_norm(red, amax, sum);
+    const float inv = norm_scale(a, m, amax, sum);
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+        if (inv == 0.0f) {
+            // (a NaN times 0 is no code 0)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+        }
+        if (tid + i * bd < nc) store_codes(a, row, tid + i * bd, v[i], inv);
+    }
+}
+
+// Rows of any length: the second walk reads h, which this lane wrote (x
+// where there is no residual).
+template <int TYPE>
+__global__ __launch_bounds__(1024) void norm_long_kernel(NormLaunch a) {
+    __shared__ NormSums red;
+    const int tid = int(threadIdx.x), bd = int(blockDim.x), m = int(blockIdx.x);
+    const int nc = (a.K + 7) >> 3;
+    const int64_t row = int64_t(m) * a.K;
+    float amax = 0.0f, v[8];
+    double sum = 0.0;
+    for (int c = tid; c < nc; c += bd) {
+        norm_chunk<TYPE>(a, row, c, v, sum);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = abs_max(amax, v[j]);
+    }
+    block_norm(red, amax, sum);
+    const float inv = norm_scale(a, m, amax, sum);
+    NormLaunch again = a;
+    if (a.residual) again.x = a.h;
+    again.residual = nullptr;
+    for (int c = tid; c < nc; c += bd) {
+        norm_chunk<TYPE>(again, row, c, v, sum);
+        if (inv == 0.0f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        }
+        store_codes(a, row, c, v, inv);
+    }
+}
+
+template <int TYPE>
+hipError_t norm_type(const NormLaunch &a, hipStream_t stream) {
+    const int slots = (a.K + 7) / 8;
+    const void *fn = reinterpret_cast<const void *>(&norm_long_kernel<TYPE>);
+    int threads = 1024;
+    if (a.K <= kNormRowsMaxK) {
+        static const void *const fns[4] = {reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 1>),
+                                           reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 2>),
+                                           reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 3>),
+                                           reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 4>)};
+        const int cpl = (slots + 1023) / 1024;
+        fn = fns[cpl - 1];
+        threads = ((slots + cpl - 1) / cpl + 63) / 64 * 64;
+    }
+    NormLaunch l = a;
+    void *args[] = {&l};
+    return hipLaunchKernel(fn, dim3(unsigned(a.M)), dim3(unsigned(threads)), args, 0, stream);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm_quant(const NormLaunch &a, int type, hipStream_t stream) {
+    return type == W2A8_F32    ? norm_type<W2A8_F32>(a, stream)
+           : type == W2A8_BF16 ? norm_type<W2A8_BF16>(a, stream)
+                               : norm_type<W2A8_F16>(a, stream);
+}
+
+}  // namespace w2a8
