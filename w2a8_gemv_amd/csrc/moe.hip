@@ -1,47 +1,54 @@
-// Mixture of ternary experts for a few tokens (gfx950): the layer of w2a8_moe
-// in four launches.
+// Mixture of ternary experts for a few tokens (gfx950): the layer of w2a8_moe.
 //
-//   route     every token's top_k experts and their weights, and every
-//             expert's tokens: pairs (token, expert) in the order of experts
-//   gate, up  hidden[pair] = act(g) * u, and its largest magnitude
-//   down      hidden quantized to int8 by it, part[pair] = p * (w_down . q) ...
-//   combine   y[token] = the sum of its pairs' parts, in order of rank
+// One token at a time, two launches (few tokens, which share few experts):
+//   up_one    routes inside every workgroup; hidden = act(g) * u of one expert
+//   down_one  hidden to int8 in every workgroup, w_down of all the token's
+//             experts, and their weighted sum
+// Token rows together, five launches (more tokens):
+//   route     every token's experts and weights, every expert's tokens: pairs
+//             (token, expert) in the order of experts; rows padded to tiles
+//   up        hidden[pair]          quant  hidden to int8
+//   down      part[pair]            combine  y[token], pairs in order of rank
 //
-// The weights of an expert are read once for 16 of its tokens: a workgroup
-// takes a strip of 32 weight rows of one expert, its waves the strip's tiles
-// in turn.  The matrix instruction (16x16x64, int8) takes activation rows as
-// its first operand and weight rows as its second; lane (r, c) reads 8 bytes
-// of the T32x128 slots of k-parts c and 4 + c: two words, of weight rows 2r
-// and 2r + 1.  Sums are integers, so waves add up in any order; the pair's
-// maximum is an atomic maximum, which has no order either.
+// All sums of products are integers, so how they are split and joined does
+// not show.  Weights are in the T32x128 layout, one matrix an expert.
 #include "block.h"
 
 namespace w2a8 {
 namespace {
 
-constexpr int kMoeRows = 16;       // tokens of a pass
-constexpr int kMoeWaves = 8;
+constexpr int kMoeRows = 16;       // tokens of a pass of the matrix kernels
 constexpr int kRouteThreads = 1024;
+constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr int kRouteTokens = W2A8_MOE_MAX_M / kRouteWaves;   // of a wave
 constexpr int kMaxPairs = W2A8_MOE_MAX_M * W2A8_MOE_MAX_TOP_K;
 constexpr int kPerLane = W2A8_MOE_MAX_E / 64;
 
-// What the route leaves behind, at the start of the workspace.
-struct Slots {
-    int count;                          // experts that have tokens
-    int bad[W2A8_MOE_MAX_M];            // tokens whose logits are no numbers
-    int expert[W2A8_MOE_MAX_E], begin[W2A8_MOE_MAX_E], tokens[W2A8_MOE_MAX_E];
+// What the route leaves behind.
+struct Slot {
+    int expert, begin;                  // -1: none; the first of its pairs
+    uint32_t mask[2];                   // its tokens
 };
-// Pairs: the token and weight of each, and each token's pairs by rank.
 struct Pairs {
-    int token[kMaxPairs];
-    float weight[kMaxPairs];
-    int of[kMaxPairs];                  // [token][rank]: pair or -1
+    int count;
+    int of[kMaxPairs];                  // [token][rank]: pair, -1 none, -2 a broken token
+    float weight[kMaxPairs];            // of a pair
+};
+struct Picked {                         // one token at a time: [token][rank]
+    int expert;                         // -1: none, -2: a broken token
+    float weight;
 };
 
+// ---------------------------------------------------------------------------
+// Routing
+// ---------------------------------------------------------------------------
 // Order of floats as unsigned integers; 0 stands for an expert that cannot be taken.
 __device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t b = __float_as_uint(v);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
     v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xF, 0xF, false)));
@@ -56,156 +63,109 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
     for (int o = 1; o < 64; o *= 2) v += __shfl_xor(v, o);
     return v;
 }
-
 __device__ __forceinline__ float logit(const MoeLaunch &a, int64_t i) {
     return a.logit_type == W2A8_F32    ? mx4_load1<W2A8_F32>(a.logits, i)
            : a.logit_type == W2A8_BF16 ? mx4_load1<W2A8_BF16>(a.logits, i)
                                        : mx4_load1<W2A8_F16>(a.logits, i);
 }
 
-__global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeLaunch a) {
-    __shared__ uint32_t mask[W2A8_MOE_MAX_E][2];      // tokens of an expert
-    __shared__ short taken[kMaxPairs];                // [token][rank]
-    __shared__ int ends[2][W2A8_MOE_MAX_E], begins[W2A8_MOE_MAX_E];
-    const int tid = int(threadIdx.x), lane = tid & 63, wv = tid >> 6;
-    Slots *slots = reinterpret_cast<Slots *>(a.ws + a.sp.slot);
-    Pairs *pairs = reinterpret_cast<Pairs *>(a.ws + a.sp.pair);
-    uint32_t *amax = reinterpret_cast<uint32_t *>(a.ws + a.sp.amax);
-    if (tid < W2A8_MOE_MAX_E) mask[tid][0] = mask[tid][1] = 0;
-    for (int i = tid; i < a.M * a.top_k; i += kRouteThreads) amax[i] = 0;
-    __syncthreads();
+// A token's logits over the lanes of a wave: expert lane + 64 i.
+struct Router {
+    float l[kPerLane];
+    uint32_t key[kPerLane];
+    bool bad;
 
-    float weight[W2A8_MOE_MAX_M / (kRouteThreads / 64)];     // of rank `lane`, of this wave's tokens
-#pragma unroll
-    for (int q = 0; q < W2A8_MOE_MAX_M / (kRouteThreads / 64); ++q) {
-        const int m = wv + q * (kRouteThreads / 64);
-        weight[q] = 0.0f;
-        if (m >= a.M) continue;
-        float l[kPerLane];
-        uint32_t key[kPerLane];
-        bool bad = false;
+    __device__ __forceinline__ void load(const MoeLaunch &a, int m, int lane) {
+        bool b = false;
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i) {
             const int e = lane + 64 * i;
             l[i] = e < a.E ? logit(a, int64_t(m) * a.E + e) : -__builtin_inff();
-            bad |= !(l[i] < __builtin_inff());
+        }
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+            b |= !(l[i] < __builtin_inff());
             key[i] = l[i] == -__builtin_inff() ? 0u : order_key(l[i] + 0.0f);   // (-0 ties with 0)
         }
-        bad = __any(bad);
-        float top = 0.0f, sum = 0.0f, all = 0.0f;
+        bad = __any(b);
+    }
+    // The next expert by rank (-1: none is left) and its logit.
+    __device__ __forceinline__ int next(int lane, float *value) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < kPerLane; ++i) best = max(best, key[i]);
+        best = wave_max_u32(best);
+        if (best == 0 || bad) return -1;
+        int e = -1;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+            const uint64_t hit = __ballot(key[i] == best);
+            if (e < 0 && hit) e = 64 * i + __builtin_ctzll(hit);
+        }
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+            if (lane + 64 * i == e) key[i] = 0;
+        *value = key_value(best);
+        return e;
+    }
+    // All ranks: lane j is left with rank j's expert and weight.
+    __device__ __forceinline__ void all(const MoeLaunch &a, int lane, int *expert, float *weight) {
+        float top = 0.0f, sum = 0.0f, whole = 0.0f;
+        *expert = bad ? -2 : -1;
+        *weight = 0.0f;
         for (int j = 0; j < a.top_k; ++j) {
-            uint32_t best = 0;
+            float v;
+            const int e = next(lane, &v);
+            if (e < 0) break;
+            if (j == 0) {
+                top = v;
 #pragma unroll
-            for (int i = 0; i < kPerLane; ++i) best = max(best, key[i]);
-            best = wave_max_u32(best);
-            if (bad) best = 0;
-            int e = -1;
-#pragma unroll
-            for (int i = 0; i < kPerLane; ++i) {
-                const uint64_t hit = __ballot(best != 0 && key[i] == best);
-                if (e < 0 && hit) e = 64 * i + __builtin_ctzll(hit);
+                for (int i = 0; i < kPerLane; ++i) whole += expf(l[i] - top);
+                if (!a.renormalize) whole = wave_sum_f32(whole);
             }
-            float p = 0.0f;
-            if (e >= 0) {
-#pragma unroll
-                for (int i = 0; i < kPerLane; ++i)
-                    if (lane + 64 * i == e) key[i] = 0;
-                const float v = __uint_as_float(best & 0x80000000u ? best & 0x7FFFFFFFu : ~best);
-                if (j == 0) {
-                    top = v;
-#pragma unroll
-                    for (int i = 0; i < kPerLane; ++i) all += expf(l[i] - top);
-                    all = wave_sum_f32(all);
-                }
-                p = expf(v - top);
-                sum += p;
-                if (lane == 0) {
-                    taken[m * a.top_k + j] = short(e);
-                    atomicOr(&mask[e][m >> 5], 1u << (m & 31));
-                }
-            } else if (lane == 0) {
-                taken[m * a.top_k + j] = -1;
+            const float p = expf(v - top);
+            sum += p;
+            if (lane == j) {
+                *expert = e;
+                *weight = p;
             }
-            if (lane == j) weight[q] = p;
         }
-        weight[q] /= a.renormalize ? sum : all;
-        if (lane == 0) slots->bad[m] = bad;
+        if (*expert >= 0) *weight /= a.renormalize ? sum : whole;
     }
-    __syncthreads();
-
-    // Places of the experts' pairs and slots: sums of (pairs, experts) over
-    // the experts before, in one word each.
-    const int n = tid < W2A8_MOE_MAX_E ? __popc(mask[tid][0]) + __popc(mask[tid][1]) : 0;
-    int v = n + (n ? 1 << 16 : 0);
-    if (tid < W2A8_MOE_MAX_E) ends[0][tid] = v;
-    __syncthreads();
-    int from = 0;
-    for (int o = 1; o < W2A8_MOE_MAX_E; o *= 2) {
-        if (tid < W2A8_MOE_MAX_E) ends[from ^ 1][tid] = ends[from][tid] + (tid >= o ? ends[from][tid - o] : 0);
-        from ^= 1;
-        __syncthreads();
-    }
-    if (tid < W2A8_MOE_MAX_E) {
-        const int before = ends[from][tid] - v;
-        begins[tid] = before & 0xFFFF;
-        if (n) {
-            slots->expert[before >> 16] = tid;
-            slots->begin[before >> 16] = before & 0xFFFF;
-            slots->tokens[before >> 16] = n;
-        }
-        if (tid == W2A8_MOE_MAX_E - 1) slots->count = ends[from][tid] >> 16;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < W2A8_MOE_MAX_M / (kRouteThreads / 64); ++q) {
-        const int m = wv + q * (kRouteThreads / 64);
-        if (m >= a.M || lane >= a.top_k) continue;
-        const int e = taken[m * a.top_k + lane];
-        int at = -1;
-        if (e >= 0) {
-            const uint32_t lo = mask[e][0], hi = mask[e][1];
-            at = begins[e] + (m < 32 ? __popc(lo & ((1u << m) - 1u))
-                                     : __popc(lo) + __popc(hi & ((1u << (m - 32)) - 1u)));
-            pairs->token[at] = m;
-            pairs->weight[at] = weight[q];
-        }
-        pairs->of[m * a.top_k + lane] = at;
-    }
-}
-
-// The weight words of a tile that a lane brings: rows 2r, 2r + 1 of k-parts c
-// and 4 + c.
-struct Words {
-    v2u h[2];
 };
-__device__ __forceinline__ Words load_words(const uint8_t *tile, int r, int c) {
-    Words w;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        w.h[h] = __builtin_nontemporal_load(
-            reinterpret_cast<const v2u *>(tile + 16 * (8 * (r >> 1) + c + 4 * h) + 8 * (r & 1)));
-    return w;
-}
-__device__ __forceinline__ void add_tile(const Words &w, const v4i (&x)[2], v4i (&acc)[2]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[h], expand_word(w.h[h][j]), acc[j], 0, 0, 0);
-}
 
-// Sums of the waves' results (COUNT words a lane) in wave 0 .. nw - 1: wave w
-// is left with words i % nw == w, the others' are stale.
-template <int COUNT>
-__device__ __forceinline__ void add_waves(int *red, int lane, int wv, int nw, int (&v)[COUNT]) {
-    __syncthreads();
+// ---------------------------------------------------------------------------
+// One token at a time
+// ---------------------------------------------------------------------------
+// Lane l of a wave reads 16 bytes of a step of eight tiles: tile l / 8, k-part
+// l % 8, four weight rows (a slice of 128 bytes a tile).  Codes c = w + 1
+// against activations by dot products, less the activations' sum; masks leave
+// c, 4c and 16c, divided out at the end.
+struct Dots {
+    int a1[4], a4[4], a16[4];
+
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i) red[(wv * COUNT + i) * 64 + lane] = v[i];
-    __syncthreads();
-    if (wv != 0) return;
+        for (int q = 0; q < 4; ++q) a1[q] = a4[q] = a16[q] = 0;
+    }
+    __device__ __forceinline__ void add(v4u w, v4u x) {
 #pragma unroll
-    for (int i = 0; i < COUNT; ++i)
-        for (int w = 1; w < nw; ++w) v[i] += red[(w * COUNT + i) * 64 + lane];
+        for (int q = 0; q < 4; ++q) {
+            a1[q] = dot4(w[q] & 0x03030303u, x[0], a1[q]);
+            a4[q] = dot4(w[q] & 0x0C0C0C0Cu, x[1], a4[q]);
+            a16[q] = dot4(w[q] & 0x30303030u, x[2], a16[q]);
+            a16[q] = dot4((w[q] >> 2) & 0x30303030u, x[3], a16[q]);
+        }
+    }
+    // Row q's sum over the wave (the same in all lanes), less the activations'.
+    __device__ __forceinline__ int row(int q, int sx) const {
+        return wave_sum(a1[q] + (a4[q] >> 2) + (a16[q] >> 4)) - sx;
+    }
+};
+__device__ __forceinline__ int add16(v4u x, int s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = dot4(x[i], 0x01010101u, s);
+    return s;
 }
 
 __device__ __forceinline__ float activate(int act, float g, float u) {
@@ -214,166 +174,562 @@ __device__ __forceinline__ float activate(int act, float g, float u) {
     return (p * p) * u;
 }
 
-__global__ __launch_bounds__(64 * kMoeWaves) void moe_up_kernel(MoeLaunch a) {
-    extern __shared__ __attribute__((aligned(16))) int red[];
-    const Slots *slots = reinterpret_cast<const Slots *>(a.ws + a.sp.slot);
-    const int slot = int(blockIdx.y), s = int(blockIdx.x);
-    if (slot >= slots->count) return;
-    const Pairs *pairs = reinterpret_cast<const Pairs *>(a.ws + a.sp.pair);
-    uint32_t *amax = reinterpret_cast<uint32_t *>(a.ws + a.sp.amax);
-    float *hidden = reinterpret_cast<float *>(a.ws + a.sp.hidden);
-    const int e = slots->expert[slot], begin = slots->begin[slot], tokens = slots->tokens[slot];
-    const int lane = int(threadIdx.x) & 63, r = lane & 15, c = lane >> 4;
-    const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), nw = int(blockDim.x) >> 6;
-    const int KT = (a.H + kTileK - 1) / kTileK, whole = a.H / kTileK;
-    const int64_t off = int64_t(e) * a.wb1 + int64_t(s) * KT * kTileBytes;
-    const uint8_t *wg = a.w_gate + off, *wu = a.w_up + off;
-    const float sg = a.s_gate[e], su = a.s_up[e];
+// Workgroup (strip, rank, token) of eight waves, one slice of four rows each.
+// A wave's loads are its own, so nothing is shared but the strip's largest
+// hidden value.  Every wave routes by itself: up to `rank` + 1 maxima.
+constexpr int kOneDepth = 3;
 
-    for (int m0 = 0; m0 < tokens; m0 += kMoeRows) {
-        const int8_t *xr = a.x + int64_t(pairs->token[begin + min(m0 + r, tokens - 1)]) * a.H;
-        v4i acc[2][2];
+__global__ __launch_bounds__(512) void moe_up_one_kernel(MoeLaunch a) {
+    __shared__ uint32_t most[8];
+    const int s = int(blockIdx.x), rank = int(blockIdx.y), m = int(blockIdx.z);
+    const int lane = int(threadIdx.x) & 63;
+    const int sl = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    Router route;
+    route.load(a, m, lane);
+    const Router start = route;
+    int e = -1;
+    float v;
+    for (int j = 0; j <= rank; ++j) e = route.next(lane, &v);
+    const int pair = m * a.top_k + rank;
+    float *tops = reinterpret_cast<float *>(a.ws + a.sp.tops);
+    const int strips = int(gridDim.x);
+
+    if (e >= 0) {
+        const float sa = a.sa[m], sg = a.s_gate[e], su = a.s_up[e];
+        const int u = lane >> 3, kg = lane & 7;
+        const int KT = (a.H + kTileK - 1) / kTileK, nst = (KT + 7) / 8;
+        const int64_t off = int64_t(e) * a.wb1 + int64_t(s) * KT * kTileBytes + 16 * (8 * sl + kg);
+        const uint8_t *wg = a.w_gate + off, *wu = a.w_up + off;
+        const int8_t *x = a.x + int64_t(m) * a.H;
+        v4u g[kOneDepth], p[kOneDepth], xv[kOneDepth];
+        auto load = [&](int i, int d) __attribute__((always_inline)) {
+            const int t = 8 * i + u, at = min(t, KT - 1) * kTileBytes;
+            g[d] = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(wg + at));
+            p[d] = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(wu + at));
+            const int k = t * kTileK + 16 * kg;
+            xv[d] = v4u{0u, 0u, 0u, 0u};
+            if (k + 16 <= a.H) {
+                xv[d] = *reinterpret_cast<const v4u_b *>(x + k);
+            } else if (k < a.H) {
+                uint32_t w[4];
+                load_int8_tail<16>(x, k, a.H, w);
+                xv[d] = v4u{w[0], w[1], w[2], w[3]};
+            }
+        };
+        Dots dg, du;
+        dg.clear();
+        du.clear();
+        int sx = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = v4i{0, 0, 0, 0};
-#pragma unroll 2
-        for (int t = wv; t < whole; t += nw) {
-            const Words g = load_words(wg + int64_t(t) * kTileBytes, r, c);
-            const Words u = load_words(wu + int64_t(t) * kTileBytes, r, c);
-            v4i x[2];
+        for (int d = 0; d < kOneDepth; ++d)
+            if (d < nst) load(d, d);
+        for (int i = 0; i < nst; i += kOneDepth) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                x[h] = __builtin_bit_cast(v4i, *reinterpret_cast<const v4u_b *>(xr + t * kTileK + 64 * h + 16 * c));
-            add_tile(g, x, acc[0]);
-            add_tile(u, x, acc[1]);
+            for (int d = 0; d < kOneDepth; ++d) {
+                if (i + d < nst) {
+                    sx = add16(xv[d], sx);
+                    dg.add(g[d], xv[d]);
+                    du.add(p[d], xv[d]);
+                }
+                if (i + d + kOneDepth < nst) load(i + d + kOneDepth, d);
+            }
         }
-        if (whole < KT && wv == whole % nw) {
-            uint32_t w[2][4];
+        sx = wave_sum(sx);
+        int ig = 0, iu = 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) load_int8_tail<16>(xr, whole * kTileK + 64 * h + 16 * c, a.H, w[h]);
-            const v4i x[2] = {v4i{int(w[0][0]), int(w[0][1]), int(w[0][2]), int(w[0][3])},
-                              v4i{int(w[1][0]), int(w[1][1]), int(w[1][2]), int(w[1][3])}};
-            add_tile(load_words(wg + int64_t(whole) * kTileBytes, r, c), x, acc[0]);
-            add_tile(load_words(wu + int64_t(whole) * kTileBytes, r, c), x, acc[1]);
+        for (int q = 0; q < 4; ++q) {
+            const int rg = dg.row(q, sx), ru = du.row(q, sx);
+            ig = lane == q ? rg : ig;
+            iu = lane == q ? ru : iu;
         }
-        int v[16];
+        const float h = activate(a.act, (float(ig) * sa) * sg, (float(iu) * sa) * su);
+        const int row = s * kTileRows + 4 * sl + lane;
+        const bool mine = lane < 4 && row < a.I;
+        if (mine) reinterpret_cast<float *>(a.ws + a.sp.hidden)[int64_t(pair) * a.I + row] = h;
+        const uint32_t top = wave_max_u32(mine ? __float_as_uint(h) & 0x7FFFFFFFu : 0u);
+        if (lane == 0) most[sl] = top;
+    }
+    // What the second launch needs of the route: once a token.
+    if (s == 0 && rank == 0 && sl == 0) {
+        Router again = start;
+        int expert;
+        float weight;
+        again.all(a, lane, &expert, &weight);
+        Picked *out = reinterpret_cast<Picked *>(a.ws + a.sp.picked) + m * a.top_k;
+        if (lane < a.top_k) out[lane] = Picked{expert, weight};
+    }
+    if (e < 0) return;      // (the same for all waves)
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint32_t t = most[0];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = acc[i >> 3][(i >> 2) & 1][i & 3];
-        if (nw > 1) add_waves(red, lane, wv, nw, v);
-        if (wv != 0) continue;
-        // Lane (r, c): weight rows 2r + j, pairs 4c + i.
+        for (int i = 1; i < 8; ++i) t = max(t, most[i]);
+        tops[int64_t(pair) * strips + s] = __uint_as_float(t);
+    }
+}
+
+// Four fp32 of a row to codes, values past the row 0.
+__device__ __forceinline__ v4f load4(const float *h, int k, int K) {
+    v4f f = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (k + 4 <= K) return *reinterpret_cast<const v4f_b *>(h + k);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (k + i < K) f[i] = h[k + i];
+    return f;
+}
+__device__ __forceinline__ uint32_t codes4(v4f f, float inv) {
+    return q8(f[0], inv) | (q8(f[1], inv) << 8) | (q8(f[2], inv) << 16) | (q8(f[3], inv) << 24);
+}
+// The factor of the codes and the scale of a row of largest magnitude `top`
+// (a row that is not finite has no codes: NaN).
+__device__ __forceinline__ float code_factor(float top) {
+    return top == 0.0f || !(top < __builtin_inff()) ? 0.0f : fminf(127.0f / top, __FLT_MAX__);
+}
+__device__ __forceinline__ float code_scale(float top) {
+    return top < __builtin_inff() ? top / 127.0f : __builtin_nanf("");
+}
+
+// Workgroup (16 rows of y, token) of eight waves: wave w takes slice w % 4 of
+// the rows and half w / 4 of the steps of all the token's experts.
+constexpr int kDownDepth = 4;
+constexpr int kDownAhead = 4;      // groups of four hidden values that a lane loads ahead
+
+__global__ __launch_bounds__(512) void moe_down_one_kernel(MoeLaunch a) {
+    extern __shared__ __attribute__((aligned(16))) int8_t q[];     // [rank][tiles * 128]
+    __shared__ float factor[W2A8_MOE_MAX_TOP_K], scale[W2A8_MOE_MAX_TOP_K];
+    __shared__ int sums[2][W2A8_MOE_MAX_TOP_K][16];
+    const int m = int(blockIdx.y), tid = int(threadIdx.x), lane = tid & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), part = wv >> 2;
+    const int KT = (a.I + kTileK - 1) / kTileK, nst = (KT + 7) / 8, stride = KT * kTileK;
+    const Picked *picked = reinterpret_cast<const Picked *>(a.ws + a.sp.picked) + m * a.top_k;
+    const float *hidden = reinterpret_cast<const float *>(a.ws + a.sp.hidden) + int64_t(m) * a.top_k * a.I;
+    const int strips = (a.I + kTileRows - 1) / kTileRows;
+    const float *tops = reinterpret_cast<const float *>(a.ws + a.sp.tops) + int64_t(m) * a.top_k * strips;
+    Picked mine = {-1, 0.0f};
+    if (lane < a.top_k) mine = picked[lane];
+
+    // Hidden values, four at a time over all ranks: the first ones now.
+    const int per = stride / 4, groups = a.top_k * per;
+    v4f ahead[kDownAhead];
+#pragma unroll
+    for (int i = 0; i < kDownAhead; ++i) {
+        const int g = tid + 512 * i, j = g / per;
+        if (g < groups) ahead[i] = load4(hidden + int64_t(j) * a.I, 4 * (g - j * per), a.I);
+    }
+    if (tid < 2 * W2A8_MOE_MAX_TOP_K * 16) (&sums[0][0][0])[tid] = 0;
+
+    // This wave's steps, and the first of its weights.
+    const int ranks = __popcll(__ballot(mine.expert >= 0));
+    const int total = ranks * nst, u0 = total * part / 2, u1 = total * (part + 1) / 2;
+    const int u = lane >> 3, kg = lane & 7;
+    const int s = int(blockIdx.x) >> 1, sl = 4 * (int(blockIdx.x) & 1) + (wv & 3);
+    const uint8_t *wd = a.w_down + int64_t(s) * KT * kTileBytes + 16 * (8 * sl + kg);
+    v4u w[kDownDepth];
+    auto load = [&](int n, int d) __attribute__((always_inline)) {
+        const int j = n / nst, t = min(8 * (n - j * nst) + u, KT - 1);
+        const int e = __builtin_amdgcn_readlane(mine.expert, j);
+        w[d] = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(wd + int64_t(e) * a.wb2 + t * kTileBytes));
+    };
+#pragma unroll
+    for (int d = 0; d < kDownDepth; ++d)
+        if (u0 + d < u1) load(u0 + d, d);
+
+    // Each rank's largest hidden value, from the strips'.
+    for (int j = wv; j < ranks; j += 8) {
+        uint32_t t = 0;
+        for (int i = lane; i < strips; i += 64) t = max(t, __float_as_uint(tops[int64_t(j) * strips + i]));
+        const float top = __uint_as_float(wave_max_u32(t));
+        if (lane == 0) {
+            factor[j] = code_factor(top);
+            scale[j] = code_scale(top);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kDownAhead; ++i) {
+        const int g = tid + 512 * i, j = g / per;
+        if (g < groups && j < ranks) *reinterpret_cast<uint32_t *>(q + 4 * g) = codes4(ahead[i], factor[j]);
+    }
+    for (int g = tid + 512 * kDownAhead; g < groups; g += 512) {
+        const int j = g / per;
+        if (j < ranks)
+            *reinterpret_cast<uint32_t *>(q + 4 * g) =
+                codes4(load4(hidden + int64_t(j) * a.I, 4 * (g - j * per), a.I), factor[j]);
+    }
+    __syncthreads();
+
+    Dots acc;
+    acc.clear();
+    int sx = 0, j = u0 / nst, st = u0 - j * nst;
+    auto flush = [&]() __attribute__((always_inline)) {
+        const int x = wave_sum(sx);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int m = m0 + 4 * c + i;
-            const int at = begin + m;
-            const float sa = m < tokens ? a.sa[pairs->token[at]] : 0.0f;
-            uint32_t most = 0;
+            const int r = acc.row(i, x);
+            if (lane == i) sums[part][j][4 * (wv & 3) + i] = r;
+        }
+        acc.clear();
+        sx = 0;
+    };
+    for (int n = u0; n < u1; n += kDownDepth) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int row = s * kTileRows + 2 * r + j;
-                const float g = (float(v[4 * j + i]) * sa) * sg, u = (float(v[8 + 4 * j + i]) * sa) * su;
-                const float h = activate(a.act, g, u);
-                if (m < tokens && row < a.I) {
-                    hidden[int64_t(at) * a.I + row] = h;
-                    most = max(most, __float_as_uint(h) & 0x7FFFFFFFu);
+        for (int d = 0; d < kDownDepth; ++d) {
+            if (n + d < u1) {
+                const int t = 8 * st + u;
+                v4u x = {0u, 0u, 0u, 0u};
+                if (t < KT) x = *reinterpret_cast<const v4u *>(q + j * stride + t * kTileK + 16 * kg);
+                sx = add16(x, sx);
+                acc.add(w[d], x);
+                if (++st == nst || n + d + 1 == u1) {
+                    flush();
+                    st = 0;
+                    ++j;
                 }
             }
-            // The largest of the strip's 32 rows: one atomic a pair.
-            for (int o = 1; o < 16; o *= 2) most = max(most, uint32_t(__shfl_xor(int(most), o)));
-            if (r == 0 && m < tokens) atomicMax(&amax[at], most);
+            if (n + d + kDownDepth < u1) load(n + d + kDownDepth, d);
+        }
+    }
+    __syncthreads();
+    if (tid >= 64) return;
+    const int row = 16 * int(blockIdx.x) + lane;
+    float y = __builtin_amdgcn_readfirstlane(mine.expert) == -2 ? __builtin_nanf("") : 0.0f;
+    for (int j = 0; j < ranks; ++j) {
+        const float p = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine.weight), j));
+        const float sd = a.s_down[__builtin_amdgcn_readlane(mine.expert, j)];
+        if (lane < 16) y += p * ((float(sums[0][j][lane] + sums[1][j][lane]) * scale[j]) * sd);
+    }
+    if (lane >= 16 || row >= a.H) return;
+    const int64_t at = int64_t(m) * a.H + row;
+    if (a.y_f32) a.y_f32[at] = y;
+    if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(y));
+}
+
+// ---------------------------------------------------------------------------
+// Token rows together
+// ---------------------------------------------------------------------------
+// Block 0 routes; block 1 + m pads row m with zeros to whole tiles, where the
+// matrix kernel reads it without asking for its end.
+__global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeLaunch a, int slots) {
+    __shared__ uint32_t mask[W2A8_MOE_MAX_E][2];      // tokens of an expert
+    __shared__ int ends[2][W2A8_MOE_MAX_E], begins[W2A8_MOE_MAX_E];
+    const int tid = int(threadIdx.x), lane = tid & 63, wv = tid >> 6;
+    if (blockIdx.x > 0) {
+        const int m = int(blockIdx.x) - 1, Hp = (a.H + kTileK - 1) / kTileK * kTileK;
+        const int8_t *row = a.x + int64_t(m) * a.H;
+        uint8_t *out = a.ws + a.sp.rows + int64_t(m) * Hp;
+        for (int k = 16 * tid; k < Hp; k += 16 * kRouteThreads) {
+            v4u v;
+            if (k + 16 <= a.H) {
+                v = *reinterpret_cast<const v4u_b *>(row + k);
+            } else {
+                uint32_t w[4];
+                load_int8_tail<16>(row, k, a.H, w);
+                v = v4u{w[0], w[1], w[2], w[3]};
+            }
+            *reinterpret_cast<v4u *>(out + k) = v;
+        }
+        return;
+    }
+    Slot *slot = reinterpret_cast<Slot *>(a.ws + a.sp.slot);
+    Pairs *pairs = reinterpret_cast<Pairs *>(a.ws + a.sp.pair);
+    if (tid < W2A8_MOE_MAX_E) mask[tid][0] = mask[tid][1] = 0;
+    __syncthreads();
+    int expert[kRouteTokens];           // of rank `lane`, of this wave's tokens
+    float weight[kRouteTokens];
+#pragma unroll
+    for (int i = 0; i < kRouteTokens; ++i) {
+        const int m = wv + i * kRouteWaves;
+        expert[i] = -1;
+        if (m >= a.M) continue;
+        Router r;
+        r.load(a, m, lane);
+        r.all(a, lane, &expert[i], &weight[i]);
+        if (lane < a.top_k && expert[i] >= 0) atomicOr(&mask[expert[i]][m >> 5], 1u << (m & 31));
+    }
+    __syncthreads();
+    // Places of the experts' pairs and slots: sums of (pairs, experts) over
+    // the experts before, in one word.
+    const int n = tid < W2A8_MOE_MAX_E ? __popc(mask[tid][0]) + __popc(mask[tid][1]) : 0;
+    const int both = n + (n ? 1 << 16 : 0);
+    if (tid < W2A8_MOE_MAX_E) ends[0][tid] = both;
+    __syncthreads();
+    int from = 0;
+    for (int o = 1; o < W2A8_MOE_MAX_E; o *= 2) {
+        if (tid < W2A8_MOE_MAX_E) ends[from ^ 1][tid] = ends[from][tid] + (tid >= o ? ends[from][tid - o] : 0);
+        from ^= 1;
+        __syncthreads();
+    }
+    const int used = ends[from][W2A8_MOE_MAX_E - 1];
+    if (tid < W2A8_MOE_MAX_E) {
+        const int before = ends[from][tid] - both;
+        begins[tid] = before & 0xFFFF;
+        if (n) slot[before >> 16] = Slot{tid, before & 0xFFFF, {mask[tid][0], mask[tid][1]}};
+        if (tid >= used >> 16 && tid < slots) slot[tid] = Slot{-1, 0, {0, 0}};
+        if (tid == 0) pairs->count = used & 0xFFFF;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRouteTokens; ++i) {
+        const int m = wv + i * kRouteWaves, e = expert[i];
+        if (m >= a.M || lane >= a.top_k) continue;
+        int at = e;
+        if (e >= 0) {
+            const uint32_t lo = mask[e][0], hi = mask[e][1];
+            at = begins[e] + (m < 32 ? __popc(lo & ((1u << m) - 1u))
+                                     : __popc(lo) + __popc(hi & ((1u << (m - 32)) - 1u)));
+            pairs->weight[at] = weight[i];
+        }
+        pairs->of[m * a.top_k + lane] = at;
+    }
+}
+
+// The matrix instruction (16x16x64, int8) takes activation rows as its first
+// operand and weight rows as its second: lane (r, c) brings row r and the 16
+// bytes of k-part c of both, and holds results of weight row r and activation
+// rows 4c .. 4c + 3.  A T32x128 slot holds four rows, so lane r stands for rows
+// 2r and 2r + 1 of the strip, the two words of 8 bytes of a slot, and reads
+// those of k-parts c and 4 + c: one tile in four instructions.
+struct Words {
+    v2u h[2];
+};
+__device__ __forceinline__ Words load_words(const uint8_t *w) {
+    Words d;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) d.h[h] = __builtin_nontemporal_load(reinterpret_cast<const v2u *>(w + 64 * h));
+    return d;
+}
+__device__ __forceinline__ int words_at(int r, int c) { return 16 * (8 * (r >> 1) + c) + 8 * (r & 1); }
+__device__ __forceinline__ void add_tile(const Words &w, const v4u (&x)[2], v4i (&acc)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, x[h]), expand_word(w.h[h][j]),
+                                                           acc[j], 0, 0, 0);
+}
+
+// Sums over tiles wv, wv + nw, ... of a strip of MATS matrices, against row x
+// (padded to whole tiles), D tiles of a wave on their way.
+template <int MATS, int D>
+__device__ __forceinline__ void strip_sums(const uint8_t *const (&w)[MATS], const int8_t *x, int KT, int wv, int nw,
+                                           v4i (&acc)[MATS][2]) {
+    Words d[D][MATS];
+    v4u xv[D][2];
+    const int n = wv < KT ? (KT - wv + nw - 1) / nw : 0;
+    auto load = [&](int i, int j) __attribute__((always_inline)) {
+        const int t = wv + i * nw;
+#pragma unroll
+        for (int k = 0; k < MATS; ++k) d[j][k] = load_words(w[k] + int64_t(t) * kTileBytes);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) xv[j][h] = *reinterpret_cast<const v4u *>(x + t * kTileK + 64 * h);
+    };
+#pragma unroll
+    for (int k = 0; k < MATS; ++k) acc[k][0] = acc[k][1] = v4i{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < D; ++j)
+        if (j < n) load(j, j);
+    for (int i = 0; i < n; i += D) {
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+            if (i + j < n)
+#pragma unroll
+                for (int k = 0; k < MATS; ++k) add_tile(d[j][k], xv[j], acc[k]);
+            if (i + j + D < n) load(i + j + D, j);
         }
     }
 }
 
-__global__ __launch_bounds__(64 * kMoeWaves) void moe_down_kernel(MoeLaunch a, int chunk, int rows) {
-    extern __shared__ __attribute__((aligned(16))) int8_t lds[];
-    const Slots *slots = reinterpret_cast<const Slots *>(a.ws + a.sp.slot);
-    const int slot = int(blockIdx.y), s = int(blockIdx.x);
-    if (slot >= slots->count) return;
-    const Pairs *pairs = reinterpret_cast<const Pairs *>(a.ws + a.sp.pair);
-    const uint32_t *amax = reinterpret_cast<const uint32_t *>(a.ws + a.sp.amax);
-    const float *hidden = reinterpret_cast<const float *>(a.ws + a.sp.hidden);
-    float *part = reinterpret_cast<float *>(a.ws + a.sp.part);
-    const int e = slots->expert[slot], begin = slots->begin[slot], tokens = slots->tokens[slot];
-    const int tid = int(threadIdx.x), lane = tid & 63, r = lane & 15, c = lane >> 4;
-    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), nw = int(blockDim.x) >> 6;
-    const int KT = (a.I + kTileK - 1) / kTileK;
-    const uint8_t *wd = a.w_down + int64_t(e) * a.wb2 + int64_t(s) * KT * kTileBytes;
-    const float sd = a.s_down[e];
-    const int stride = chunk + 16;        // rows of LDS start in banks of their own
-    int *red = reinterpret_cast<int *>(lds);
+// Sums of the waves' words; wave w is left with the words of rows 4c + i, i %
+// nw == w (v[COUNT / 4 blocks][4]), the others' are its own.
+template <int BLOCKS>
+__device__ __forceinline__ void join_waves(int *red, int lane, int wv, int nw, v4i (&v)[BLOCKS]) {
+    if (nw == 1) return;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < BLOCKS; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[((wv * BLOCKS + k) * 4 + i) * 64 + lane] = v[k][i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i % nw != wv) continue;
+#pragma unroll
+        for (int k = 0; k < BLOCKS; ++k) {
+            int s = 0;
+            for (int w = 0; w < nw; ++w) s += red[((w * BLOCKS + k) * 4 + i) * 64 + lane];
+            v[k][i] = s;
+        }
+    }
+}
+
+// The place of the n-th set bit of a 64-bit mask, for n = first + (lane's r);
+// the last one for n past the last.
+__device__ __forceinline__ int token_of(uint64_t mask, int first, int r) {
+    for (int i = 0; i < first; ++i) mask &= mask - 1;
+    int at = 0;
+    for (int i = 0; i < kMoeRows && mask; ++i) {
+        const int b = __builtin_ctzll(mask);
+        if (i <= r) at = b;
+        mask &= mask - 1;
+    }
+    return at;
+}
+
+typedef v2f v2f_a __attribute__((aligned(4)));
+
+__global__ __launch_bounds__(512) void moe_up_kernel(MoeLaunch a) {
+    extern __shared__ __attribute__((aligned(16))) int red[];
+    const Slot slot = reinterpret_cast<const Slot *>(a.ws + a.sp.slot)[blockIdx.y];
+    if (slot.expert < 0) return;
+    const int s = int(blockIdx.x);
+    float *hidden = reinterpret_cast<float *>(a.ws + a.sp.hidden);
+    const uint64_t mask = (uint64_t(slot.mask[1]) << 32) | slot.mask[0];
+    const int tokens = __popcll(mask);
+    const int lane = int(threadIdx.x) & 63, r = lane & 15, c = lane >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), nw = int(blockDim.x) >> 6;
+    const int KT = (a.H + kTileK - 1) / kTileK;
+    const int64_t off = int64_t(slot.expert) * a.wb1 + int64_t(s) * KT * kTileBytes + words_at(r, c);
+    const uint8_t *const w[2] = {a.w_gate + off, a.w_up + off};
+    const int8_t *rows = reinterpret_cast<const int8_t *>(a.ws + a.sp.rows) + 16 * c;
+    const float sg = a.s_gate[slot.expert], su = a.s_up[slot.expert];
 
     for (int m0 = 0; m0 < tokens; m0 += kMoeRows) {
-        const int mt = min(tokens - m0, rows);
-        v4i acc[2] = {v4i{0, 0, 0, 0}, v4i{0, 0, 0, 0}};
-        for (int k0 = 0; k0 < a.I; k0 += chunk) {
-            const int kn = min(chunk, KT * kTileK - k0);
-            __syncthreads();
-            // int8 rows of the chunk, four values a lane; zeros past I.
-            for (int j = 0; j < mt; ++j) {
-                const int at = begin + m0 + j;
-                const float most = __uint_as_float(amax[at]);
-                const float inv = most == 0.0f ? 0.0f : fminf(127.0f / most, __FLT_MAX__);
-                const float *h = hidden + int64_t(at) * a.I + k0;
-                for (int k = 4 * tid; k < kn; k += 4 * int(blockDim.x)) {
-                    v4f f = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if (k0 + k + 4 <= a.I)
-                        f = *reinterpret_cast<const v4f_b *>(h + k);
-                    else
-#pragma unroll
-                        for (int i = 0; i < 3; ++i)
-                            if (k0 + k + i < a.I) f[i] = h[k + i];
-                    *reinterpret_cast<uint32_t *>(lds + j * stride + k) =
-                        q8(f[0], inv) | (q8(f[1], inv) << 8) | (q8(f[2], inv) << 16) | (q8(f[3], inv) << 24);
-                }
-            }
-            __syncthreads();
-            const int8_t *xr = lds + min(r, mt - 1) * stride;
-#pragma unroll 2
-            for (int t = wv; t < kn / kTileK; t += nw) {
-                const Words w = load_words(wd + int64_t(k0 / kTileK + t) * kTileBytes, r, c);
-                v4i x[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) x[h] = *reinterpret_cast<const v4i *>(xr + t * kTileK + 64 * h + 16 * c);
-                add_tile(w, x, acc);
-            }
-        }
-        int v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = acc[i >> 2][i & 3];
-        if (nw > 1) add_waves(red, lane, wv, nw, v);
-        if (wv != 0) continue;
+        const int token = token_of(mask, m0, r);
+        const float mine = a.sa[token];            // of row r
+        v4i acc[2][2];
+        strip_sums<2, 3>(w, rows + int64_t(token) * KT * kTileK, KT, wv, nw, acc);
+        v4i v[4] = {acc[0][0], acc[0][1], acc[1][0], acc[1][1]};
+        join_waves(red, lane, wv, nw, v);
+        // Lane (r, c): weight rows 2r + j, pairs m0 + 4c + i.
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int m = m0 + 4 * c + i;
-            if (m >= tokens) continue;
-            const int at = begin + m;
-            const float most = __uint_as_float(amax[at]);
-            // (A hidden row that is not finite has no codes.)
-            const float sh = most < __builtin_inff() ? most / 127.0f : __builtin_nanf("");
-            const float p = pairs->weight[at];
+            if (i % nw != wv) continue;
+            const float sa = __shfl(mine, 4 * c + i);
+            const int m = m0 + 4 * c + i, row = s * kTileRows + 2 * r;
+            float h[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int row = s * kTileRows + 2 * r + j;
-                if (row < a.H) part[int64_t(at) * a.H + row] = p * ((float(v[4 * j + i]) * sh) * sd);
-            }
+            for (int j = 0; j < 2; ++j)
+                h[j] = activate(a.act, (float(v[j][i]) * sa) * sg, (float(v[2 + j][i]) * sa) * su);
+            float *out = hidden + int64_t(slot.begin + m) * a.I + row;
+            if (m >= tokens || row >= a.I) continue;
+            if (row + 1 < a.I)
+                *reinterpret_cast<v2f_a *>(out) = v2f{h[0], h[1]};
+            else
+                out[0] = h[0];
+        }
+    }
+}
+
+// One workgroup per pair: its hidden row to int8, padded with zeros to whole
+// tiles; the first values stay in registers between the two walks.
+constexpr int kQuantThreads = 512, kQuantKept = 4;
+
+__global__ __launch_bounds__(kQuantThreads) void moe_quant_kernel(MoeLaunch a) {
+    __shared__ uint32_t most[kQuantThreads / 64];
+    const int pair = int(blockIdx.x), tid = int(threadIdx.x);
+    const float *h = reinterpret_cast<const float *>(a.ws + a.sp.hidden) + int64_t(pair) * a.I;
+    const int Ip = (a.I + kTileK - 1) / kTileK * kTileK;
+    v4f kept[kQuantKept];
+    uint32_t top = 0;
+    if (pair >= reinterpret_cast<const Pairs *>(a.ws + a.sp.pair)->count) return;
+    auto largest = [&](v4f f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    };
+#pragma unroll
+    for (int i = 0; i < kQuantKept; ++i) kept[i] = load4(h, 4 * (tid + kQuantThreads * i), a.I);
+#pragma unroll
+    for (int i = 0; i < kQuantKept; ++i) largest(kept[i]);
+    for (int k = 4 * (tid + kQuantThreads * kQuantKept); k < a.I; k += 4 * kQuantThreads) largest(load4(h, k, a.I));
+    top = wave_max_u32(top);
+    if ((tid & 63) == 0) most[tid >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kQuantThreads / 64; ++i) top = max(top, most[i]);
+    const float factor = code_factor(__uint_as_float(top));
+    uint32_t *out = reinterpret_cast<uint32_t *>(a.ws + a.sp.codes + int64_t(pair) * Ip);
+#pragma unroll
+    for (int i = 0; i < kQuantKept; ++i)
+        if (4 * (tid + kQuantThreads * i) < Ip) out[tid + kQuantThreads * i] = codes4(kept[i], factor);
+    for (int g = tid + kQuantThreads * kQuantKept; 4 * g < Ip; g += kQuantThreads)
+        out[g] = codes4(load4(h, 4 * g, a.I), factor);
+    if (tid == 0) reinterpret_cast<float *>(a.ws + a.sp.scales)[pair] = code_scale(__uint_as_float(top));
+}
+
+__global__ __launch_bounds__(512) void moe_down_kernel(MoeLaunch a) {
+    extern __shared__ __attribute__((aligned(16))) int red[];
+    const Slot slot = reinterpret_cast<const Slot *>(a.ws + a.sp.slot)[blockIdx.y];
+    if (slot.expert < 0) return;
+    const int s = int(blockIdx.x);
+    const Pairs *pairs = reinterpret_cast<const Pairs *>(a.ws + a.sp.pair);
+    const float *scales = reinterpret_cast<const float *>(a.ws + a.sp.scales);
+    float *part = reinterpret_cast<float *>(a.ws + a.sp.part);
+    const int tokens = __popc(slot.mask[0]) + __popc(slot.mask[1]);
+    const int lane = int(threadIdx.x) & 63, r = lane & 15, c = lane >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), nw = int(blockDim.x) >> 6;
+    const int KT = (a.I + kTileK - 1) / kTileK;
+    const uint8_t *const w[1] = {a.w_down + int64_t(slot.expert) * a.wb2 + int64_t(s) * KT * kTileBytes + words_at(r, c)};
+    const int8_t *codes = reinterpret_cast<const int8_t *>(a.ws + a.sp.codes) + 16 * c;
+    const float sd = a.s_down[slot.expert];
+
+    for (int m0 = 0; m0 < tokens; m0 += kMoeRows) {
+        const int at = slot.begin + min(m0 + r, tokens - 1);
+        const float mine = scales[at], weight = pairs->weight[at];      // of row r
+        v4i acc[1][2];
+        strip_sums<1, 4>(w, codes + int64_t(at) * KT * kTileK, KT, wv, nw, acc);
+        join_waves(red, lane, wv, nw, acc[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i % nw != wv) continue;
+            const float sh = __shfl(mine, 4 * c + i), p = __shfl(weight, 4 * c + i);
+            const int m = m0 + 4 * c + i, row = s * kTileRows + 2 * r;
+            float *out = part + int64_t(slot.begin + m) * a.H + row;
+            const v2f y = {p * ((float(acc[0][0][i]) * sh) * sd), p * ((float(acc[0][1][i]) * sh) * sd)};
+            if (m >= tokens || row >= a.H) continue;
+            if (row + 1 < a.H)
+                *reinterpret_cast<v2f_a *>(out) = y;
+            else
+                out[0] = y[0];
         }
     }
 }
 
 __global__ __launch_bounds__(256) void moe_combine_kernel(MoeLaunch a) {
     const int n = int(blockIdx.x) * 256 + int(threadIdx.x), m = int(blockIdx.y);
-    if (n >= a.H) return;
-    const Slots *slots = reinterpret_cast<const Slots *>(a.ws + a.sp.slot);
-    const Pairs *pairs = reinterpret_cast<const Pairs *>(a.ws + a.sp.pair);
+    const int *of = reinterpret_cast<const Pairs *>(a.ws + a.sp.pair)->of + m * a.top_k;
     const float *part = reinterpret_cast<const float *>(a.ws + a.sp.part);
-    float y = slots->bad[m] ? __builtin_nanf("") : 0.0f;
+    if (n >= a.H) return;
+    float y = of[0] == -2 ? __builtin_nanf("") : 0.0f;
+#pragma unroll 4
     for (int j = 0; j < a.top_k; ++j) {
-        const int at = pairs->of[m * a.top_k + j];
-        if (at >= 0) y += part[int64_t(at) * a.H + n];
+        const int at = of[j];
+        const float p = part[int64_t(max(at, 0)) * a.H + n];
+        y += at >= 0 ? p : 0.0f;
     }
     const int64_t at = int64_t(m) * a.H + n;
     if (a.y_f32) a.y_f32[at] = y;
     if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(y));
+}
+
+hipError_t launch(const void *fn, dim3 grid, int threads, size_t lds, void **args, hipStream_t stream) {
+    return hipLaunchKernel(fn, grid, dim3(unsigned(threads)), args, lds, stream);
+}
+
+// Most LDS of the hidden rows of a token (the kernel has some of its own).
+constexpr int64_t kOneLds = 49152;
+#ifndef ONE_M
+#define ONE_M 1
+#endif
+bool one_at_a_time(const MoeLaunch &a) {
+    return a.M <= ONE_M && a.top_k * round_up(a.I, kTileK) <= kOneLds;
+}
+
+// Waves of a workgroup of the matrix kernels: some 16 on a compute unit.
+int moe_waves(int64_t groups, int64_t KT, int cus) {
+#ifdef MOE_NW
+    return MOE_NW;
+#endif
+    return int(std::max<int64_t>(1, std::min<int64_t>({8, KT, 16 * int64_t(cus) / groups})));
 }
 
 }  // namespace
@@ -381,40 +737,50 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeLaunch a) {
 MoeSpace moe_space(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k) {
     MoeSpace s;
     const int64_t pairs = M * top_k;
-    s.slot = 0;
-    s.pair = s.slot + round_up(sizeof(Slots), 256);
-    s.amax = s.pair + round_up(sizeof(Pairs), 256);
-    s.hidden = s.amax + round_up(4 * pairs, 256);
-    s.part = s.hidden + round_up(4 * pairs * I, 256);
-    s.total = s.part + round_up(4 * pairs * H, 256);
+    int64_t at = 0;
+    const auto take = [&](int64_t bytes) {
+        const int64_t from = at;
+        at += round_up(bytes, 256);
+        return from;
+    };
+    s.picked = take(pairs * sizeof(Picked));
+    s.tops = take(4 * pairs * ceil_div(I, kTileRows));
+    s.slot = take(W2A8_MOE_MAX_E * sizeof(Slot));
+    s.pair = take(sizeof(Pairs));
+    s.scales = take(4 * pairs);
+    s.rows = take(M * round_up(H, kTileK));
+    s.codes = take(pairs * round_up(I, kTileK));
+    s.hidden = take(4 * pairs * I);
+    s.part = take(4 * pairs * H);
+    s.total = at;
     return s;
 }
 
 hipError_t launch_moe(const MoeLaunch &la, int cus, hipStream_t stream) {
     MoeLaunch a = la;
-    void *args[] = {&a};
-    const unsigned slots = unsigned(std::min(a.E, a.M * a.top_k));
-    hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&moe_route_kernel), dim3(1),
-                                   dim3(kRouteThreads), args, 0, stream);
-    if (e != hipSuccess) return e;
-    const int nw1 = int(std::min<int64_t>(kMoeWaves, ceil_div(a.H, kTileK)));
-    e = hipLaunchKernel(reinterpret_cast<const void *>(&moe_up_kernel),
-                        dim3(unsigned(ceil_div(a.I, kTileRows)), slots), dim3(unsigned(64 * nw1)), args,
-                        size_t(nw1) * 4096, stream);
-    if (e != hipSuccess) return e;
-    const int64_t KT = ceil_div(a.I, kTileK);
-    const int nw2 = int(std::min<int64_t>(kMoeWaves, KT));
-    // Rows of a pass and the part of I that they have in LDS: 64 KiB at most.
-    int rows = std::min(a.M, kMoeRows);
-    int chunk = int(std::min<int64_t>(KT, (65536 / rows - 16) / kTileK) * kTileK);
-    const size_t bytes = std::max(size_t(rows) * (chunk + 16), size_t(nw2) * 2048);
-    void *args2[] = {&a, &chunk, &rows};
-    e = hipLaunchKernel(reinterpret_cast<const void *>(&moe_down_kernel),
-                        dim3(unsigned(ceil_div(a.H, kTileRows)), slots), dim3(unsigned(64 * nw2)), args2,
-                        bytes, stream);
-    if (e != hipSuccess) return e;
-    return hipLaunchKernel(reinterpret_cast<const void *>(&moe_combine_kernel),
-                           dim3(unsigned(ceil_div(a.H, 256)), unsigned(a.M)), dim3(256), args, 0, stream);
+    const auto fn = [](auto *k) { return reinterpret_cast<const void *>(k); };
+    const int64_t up = ceil_div(a.I, kTileRows), down = ceil_div(a.H, kTileRows);
+    int slots = std::min(a.E, a.M * a.top_k);
+    void *args[] = {&a, &slots};
+    hipError_t e;
+    if (one_at_a_time(a)) {
+        e = launch(fn(&moe_up_one_kernel), dim3(unsigned(up), unsigned(a.top_k), unsigned(a.M)), 512, 0, args, stream);
+        if (e != hipSuccess) return e;
+        return launch(fn(&moe_down_one_kernel), dim3(unsigned(ceil_div(a.H, 16)), unsigned(a.M)), 512,
+                      size_t(a.top_k * round_up(a.I, kTileK)), args, stream);
+    }
+    const int64_t KT1 = ceil_div(a.H, kTileK), KT2 = ceil_div(a.I, kTileK);
+    const int nw1 = moe_waves(up * slots, KT1, cus), nw2 = moe_waves(down * slots, KT2, cus);
+    if ((e = launch(fn(&moe_route_kernel), dim3(unsigned(1 + a.M)), kRouteThreads, 0, args, stream)) != hipSuccess) return e;
+    if ((e = launch(fn(&moe_up_kernel), dim3(unsigned(up), unsigned(slots)), 64 * nw1, size_t(nw1) * 4096, args, stream)) !=
+        hipSuccess)
+        return e;
+    if ((e = launch(fn(&moe_quant_kernel), dim3(unsigned(a.M * a.top_k)), kQuantThreads, 0, args, stream)) != hipSuccess)
+        return e;
+    if ((e = launch(fn(&moe_down_kernel), dim3(unsigned(down), unsigned(slots)), 64 * nw2, size_t(nw2) * 2048, args,
+                    stream)) != hipSuccess)
+        return e;
+    return launch(fn(&moe_combine_kernel), dim3(unsigned(ceil_div(a.H, 256)), unsigned(a.M)), 256, 0, args, stream);
 }
 
 }  // namespace w2a8
