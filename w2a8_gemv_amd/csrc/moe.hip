@@ -18,6 +18,7 @@ namespace w2a8 {
 namespace {
 
 constexpr int kMoeRows = 16;       // tokens of a pass of the matrix kernels
+constexpr int kMoeWaves = 4;       // waves of a workgroup of them
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / 64;
 constexpr int kRouteTokens = W2A8_MOE_MAX_M / kRouteWaves;   // of a wave
@@ -31,10 +32,9 @@ struct Slot {
 };
 struct Pairs {
     int count;
-    int of[kMaxPairs];                  // [token][rank]: pair, -1 none, -2 a broken token
-    float weight[kMaxPairs];            // of a pair
+    int of[kMaxPairs];                  // [token][rank]: pair, -1 none
 };
-struct Picked {                         // one token at a time: [token][rank]
+struct Picked {                         // [token][rank]
     int expert;                         // -1: none, -2: a broken token
     float weight;
 };
@@ -76,12 +76,15 @@ struct Router {
     bool bad;
 
     __device__ __forceinline__ void load(const MoeLaunch &a, int m, int lane) {
-        bool b = false;
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i) {
             const int e = lane + 64 * i;
-            l[i] = e < a.E ? logit(a, int64_t(m) * a.E + e) : -__builtin_inff();
+            l[i] = -__builtin_inff();
+            if (e < a.E) l[i] = logit(a, int64_t(m) * a.E + e);
         }
+    }
+    __device__ __forceinline__ void keys() {
+        bool b = false;
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i) {
             b |= !(l[i] < __builtin_inff());
@@ -90,22 +93,32 @@ struct Router {
         bad = __any(b);
     }
     // The next expert by rank (-1: none is left) and its logit.
-    __device__ __forceinline__ int next(int lane, float *value) {
+    __device__ __forceinline__ int next(int E, int lane, float *value) {
         uint32_t best = key[0];
+        if (E > 64) {
 #pragma unroll
-        for (int i = 1; i < kPerLane; ++i) best = max(best, key[i]);
+            for (int i = 1; i < kPerLane; ++i) best = max(best, key[i]);
+        }
         best = wave_max_u32(best);
         if (best == 0 || bad) return -1;
-        int e = -1;
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-            const uint64_t hit = __ballot(key[i] == best);
-            if (e < 0 && hit) e = 64 * i + __builtin_ctzll(hit);
-        }
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i)
-            if (lane + 64 * i == e) key[i] = 0;
         *value = key_value(best);
+        // The first 64 experts that hold it, and the first lane of them.
+        uint64_t hit = __ballot(key[0] == best);
+        int e = __builtin_ctzll(hit);
+        if (E > 64) {
+#pragma unroll
+            for (int i = 1; i < kPerLane; ++i) {
+                const uint64_t more = __ballot(key[i] == best);
+                if (!hit) {
+                    e = 64 * i + __builtin_ctzll(more);
+                    hit = more;
+                }
+            }
+#pragma unroll
+            for (int i = 1; i < kPerLane; ++i)
+                if (lane + 64 * i == e) key[i] = 0;
+        }
+        if (lane == e) key[0] = 0;
         return e;
     }
     // All ranks: lane j is left with rank j's expert and weight.
@@ -115,7 +128,7 @@ struct Router {
         *weight = 0.0f;
         for (int j = 0; j < a.top_k; ++j) {
             float v;
-            const int e = next(lane, &v);
+            const int e = next(a.E, lane, &v);
             if (e < 0) break;
             if (j == 0) {
                 top = v;
@@ -157,11 +170,25 @@ struct Dots {
             a16[q] = dot4((w[q] >> 2) & 0x30303030u, x[3], a16[q]);
         }
     }
-    // Row q's sum over the wave (the same in all lanes), less the activations'.
-    __device__ __forceinline__ int row(int q, int sx) const {
-        return wave_sum(a1[q] + (a4[q] >> 2) + (a16[q] >> 4)) - sx;
+    // Row q's sum over the 8 k-parts of a tile.
+    __device__ __forceinline__ int row(int q) const { return sum8(a1[q] + (a4[q] >> 2) + (a16[q] >> 4)); }
+    // The same less the activations' (sx, a lane's), row kg, and of `other` row kg - 4.
+    __device__ __forceinline__ int rows(int sx, int kg, const Dots &other) const {
+        int v = row(0);
+#pragma unroll
+        for (int q = 1; q < 8; ++q) {
+            const int n = q < 4 ? row(q) : other.row(q - 4);
+            v = kg == q ? n : v;
+        }
+        return v - sum8(sx);
     }
 };
+// Sum over the eight tiles of a step: lanes of the same k-part.
+__device__ __forceinline__ int sum_over_tiles(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x128, 0xF, 0xF, false);   // row_ror:8
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
 __device__ __forceinline__ int add16(v4u x, int s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) s = dot4(x[i], 0x01010101u, s);
@@ -174,7 +201,8 @@ __device__ __forceinline__ float activate(int act, float g, float u) {
     return (p * p) * u;
 }
 
-// Workgroup (strip, rank, token) of eight waves, one slice of four rows each.
+// Workgroup (strip, rank, token) of eight waves, one slice of four rows each (the
+// strip past the last only routes).
 // A wave's loads are its own, so nothing is shared but the strip's largest
 // hidden value.  Every wave routes by itself: up to `rank` + 1 maxima.
 constexpr int kOneDepth = 3;
@@ -186,15 +214,25 @@ __global__ __launch_bounds__(512) void moe_up_one_kernel(MoeLaunch a) {
     const int sl = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     Router route;
     route.load(a, m, lane);
-    const Router start = route;
+    route.keys();
+    const int strips = int(gridDim.x) - 1;
+    if (s == strips) {
+        // What the second launch needs of the route, once a token.
+        if (rank > 0 || sl > 0) return;
+        int expert;
+        float weight;
+        route.all(a, lane, &expert, &weight);
+        Picked *out = reinterpret_cast<Picked *>(a.ws + a.sp.picked) + m * a.top_k;
+        if (lane < a.top_k) out[lane] = Picked{expert, weight};
+        return;
+    }
     int e = -1;
     float v;
-    for (int j = 0; j <= rank; ++j) e = route.next(lane, &v);
+    for (int j = 0; j <= rank; ++j) e = route.next(a.E, lane, &v);
+    if (e < 0) return;      // (the same for all waves)
     const int pair = m * a.top_k + rank;
     float *tops = reinterpret_cast<float *>(a.ws + a.sp.tops);
-    const int strips = int(gridDim.x);
-
-    if (e >= 0) {
+    {
         const float sa = a.sa[m], sg = a.s_gate[e], su = a.s_up[e];
         const int u = lane >> 3, kg = lane & 7;
         const int KT = (a.H + kTileK - 1) / kTileK, nst = (KT + 7) / 8;
@@ -234,31 +272,17 @@ __global__ __launch_bounds__(512) void moe_up_one_kernel(MoeLaunch a) {
                 if (i + d + kOneDepth < nst) load(i + d + kOneDepth, d);
             }
         }
-        sx = wave_sum(sx);
-        int ig = 0, iu = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int rg = dg.row(q, sx), ru = du.row(q, sx);
-            ig = lane == q ? rg : ig;
-            iu = lane == q ? ru : iu;
-        }
-        const float h = activate(a.act, (float(ig) * sa) * sg, (float(iu) * sa) * su);
+        // Lane kg of eight takes row kg % 4 of the gate's or the up weights' sums;
+        // lanes 0 .. 3 then have the wave's.
+        const int v = sum_over_tiles(dg.rows(sx, kg, du));
+        const int up = __builtin_amdgcn_ds_swizzle(v, 0x101F);      // lane ^ 4
+        const float h = activate(a.act, (float(v) * sa) * sg, (float(up) * sa) * su);
         const int row = s * kTileRows + 4 * sl + lane;
         const bool mine = lane < 4 && row < a.I;
         if (mine) reinterpret_cast<float *>(a.ws + a.sp.hidden)[int64_t(pair) * a.I + row] = h;
         const uint32_t top = wave_max_u32(mine ? __float_as_uint(h) & 0x7FFFFFFFu : 0u);
         if (lane == 0) most[sl] = top;
     }
-    // What the second launch needs of the route: once a token.
-    if (s == 0 && rank == 0 && sl == 0) {
-        Router again = start;
-        int expert;
-        float weight;
-        again.all(a, lane, &expert, &weight);
-        Picked *out = reinterpret_cast<Picked *>(a.ws + a.sp.picked) + m * a.top_k;
-        if (lane < a.top_k) out[lane] = Picked{expert, weight};
-    }
-    if (e < 0) return;      // (the same for all waves)
     __syncthreads();
     if (threadIdx.x == 0) {
         uint32_t t = most[0];
@@ -289,17 +313,27 @@ __device__ __forceinline__ float code_scale(float top) {
     return top < __builtin_inff() ? top / 127.0f : __builtin_nanf("");
 }
 
-// Workgroup (16 rows of y, token) of eight waves: wave w takes slice w % 4 of
-// the rows and half w / 4 of the steps of all the token's experts.
-constexpr int kDownDepth = 4;
-constexpr int kDownAhead = 4;      // groups of four hidden values that a lane loads ahead
+#ifndef DSL
+#define DSL 4
+#define DD 4
+#define DTH 1024
+#endif
+// Workgroup (8 rows of y, token) of eight waves: wave w takes slice w % 2 of
+// the rows and quarter w / 2 of the steps of all the token's experts.
+constexpr int kDownDepth = DD;
+constexpr int kDownSlices = DSL, kDownThreads = DTH, kDownWaves = DTH / 64,
+              kDownParts = kDownWaves / kDownSlices, kDownRows = 4 * kDownSlices;
+#ifndef DA
+#define DA 4
+#endif
+constexpr int kDownAhead = DA;      // groups of four hidden values that a lane loads ahead
 
-__global__ __launch_bounds__(512) void moe_down_one_kernel(MoeLaunch a) {
+__global__ __launch_bounds__(kDownThreads) void moe_down_one_kernel(MoeLaunch a) {
     extern __shared__ __attribute__((aligned(16))) int8_t q[];     // [rank][tiles * 128]
     __shared__ float factor[W2A8_MOE_MAX_TOP_K], scale[W2A8_MOE_MAX_TOP_K];
-    __shared__ int sums[2][W2A8_MOE_MAX_TOP_K][16];
+    __shared__ int sums[W2A8_MOE_MAX_TOP_K][kDownRows];
     const int m = int(blockIdx.y), tid = int(threadIdx.x), lane = tid & 63;
-    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), part = wv >> 2;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), part = wv / kDownSlices, slice = wv % kDownSlices;
     const int KT = (a.I + kTileK - 1) / kTileK, nst = (KT + 7) / 8, stride = KT * kTileK;
     const Picked *picked = reinterpret_cast<const Picked *>(a.ws + a.sp.picked) + m * a.top_k;
     const float *hidden = reinterpret_cast<const float *>(a.ws + a.sp.hidden) + int64_t(m) * a.top_k * a.I;
@@ -313,16 +347,23 @@ __global__ __launch_bounds__(512) void moe_down_one_kernel(MoeLaunch a) {
     v4f ahead[kDownAhead];
 #pragma unroll
     for (int i = 0; i < kDownAhead; ++i) {
-        const int g = tid + 512 * i, j = g / per;
+        const int g = tid + kDownThreads * i, j = g / per;
         if (g < groups) ahead[i] = load4(hidden + int64_t(j) * a.I, 4 * (g - j * per), a.I);
     }
-    if (tid < 2 * W2A8_MOE_MAX_TOP_K * 16) (&sums[0][0][0])[tid] = 0;
+    // Each rank's largest hidden value, from the strips' (two ranks at most a wave).
+    uint32_t most[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (wv + kDownWaves * i < a.top_k)
+            for (int n = lane; n < strips; n += 64)
+                most[i] = max(most[i], __float_as_uint(tops[int64_t(wv + kDownWaves * i) * strips + n]));
+    if (tid < W2A8_MOE_MAX_TOP_K * kDownRows) (&sums[0][0])[tid] = 0;
 
     // This wave's steps, and the first of its weights.
     const int ranks = __popcll(__ballot(mine.expert >= 0));
-    const int total = ranks * nst, u0 = total * part / 2, u1 = total * (part + 1) / 2;
+    const int total = ranks * nst, u0 = total * part / kDownParts, u1 = total * (part + 1) / kDownParts;
     const int u = lane >> 3, kg = lane & 7;
-    const int s = int(blockIdx.x) >> 1, sl = 4 * (int(blockIdx.x) & 1) + (wv & 3);
+    const int s = int(blockIdx.x) / (8 / kDownSlices), sl = kDownSlices * (int(blockIdx.x) % (8 / kDownSlices)) + slice;
     const uint8_t *wd = a.w_down + int64_t(s) * KT * kTileBytes + 16 * (8 * sl + kg);
     v4u w[kDownDepth];
     auto load = [&](int n, int d) __attribute__((always_inline)) {
@@ -334,12 +375,12 @@ __global__ __launch_bounds__(512) void moe_down_one_kernel(MoeLaunch a) {
     for (int d = 0; d < kDownDepth; ++d)
         if (u0 + d < u1) load(u0 + d, d);
 
-    // Each rank's largest hidden value, from the strips'.
-    for (int j = wv; j < ranks; j += 8) {
-        uint32_t t = 0;
-        for (int i = lane; i < strips; i += 64) t = max(t, __float_as_uint(tops[int64_t(j) * strips + i]));
-        const float top = __uint_as_float(wave_max_u32(t));
-        if (lane == 0) {
+    const float sd = mine.expert >= 0 ? a.s_down[mine.expert] : 0.0f;     // of rank `lane`
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int j = wv + kDownWaves * i;
+        const float top = __uint_as_float(wave_max_u32(most[i]));
+        if (j < ranks && lane == 0) {
             factor[j] = code_factor(top);
             scale[j] = code_scale(top);
         }
@@ -347,10 +388,10 @@ __global__ __launch_bounds__(512) void moe_down_one_kernel(MoeLaunch a) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kDownAhead; ++i) {
-        const int g = tid + 512 * i, j = g / per;
+        const int g = tid + kDownThreads * i, j = g / per;
         if (g < groups && j < ranks) *reinterpret_cast<uint32_t *>(q + 4 * g) = codes4(ahead[i], factor[j]);
     }
-    for (int g = tid + 512 * kDownAhead; g < groups; g += 512) {
+    for (int g = tid + kDownThreads * kDownAhead; g < groups; g += kDownThreads) {
         const int j = g / per;
         if (j < ranks)
             *reinterpret_cast<uint32_t *>(q + 4 * g) =
@@ -362,12 +403,12 @@ __global__ __launch_bounds__(512) void moe_down_one_kernel(MoeLaunch a) {
     acc.clear();
     int sx = 0, j = u0 / nst, st = u0 - j * nst;
     auto flush = [&]() __attribute__((always_inline)) {
-        const int x = wave_sum(sx);
+        const int x = sum8(sx);
+        int r[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = acc.row(i, x);
-            if (lane == i) sums[part][j][4 * (wv & 3) + i] = r;
-        }
+        for (int i = 0; i < 4; ++i) r[i] = acc.row(i) - x;
+        const int mine = kg == 0 ? r[0] : kg == 1 ? r[1] : kg == 2 ? r[2] : r[3];
+        if (kg < 4) atomicAdd(&sums[j][4 * slice + kg], mine);
         acc.clear();
         sx = 0;
     };
@@ -391,14 +432,14 @@ __global__ __launch_bounds__(512) void moe_down_one_kernel(MoeLaunch a) {
     }
     __syncthreads();
     if (tid >= 64) return;
-    const int row = 16 * int(blockIdx.x) + lane;
+    const int row = kDownRows * int(blockIdx.x) + lane;
     float y = __builtin_amdgcn_readfirstlane(mine.expert) == -2 ? __builtin_nanf("") : 0.0f;
     for (int j = 0; j < ranks; ++j) {
         const float p = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine.weight), j));
-        const float sd = a.s_down[__builtin_amdgcn_readlane(mine.expert, j)];
-        if (lane < 16) y += p * ((float(sums[0][j][lane] + sums[1][j][lane]) * scale[j]) * sd);
+        const float d = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sd), j));
+        if (lane < kDownRows) y += p * ((float(sums[j][lane]) * scale[j]) * d);
     }
-    if (lane >= 16 || row >= a.H) return;
+    if (lane >= kDownRows || row >= a.H) return;
     const int64_t at = int64_t(m) * a.H + row;
     if (a.y_f32) a.y_f32[at] = y;
     if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(y));
@@ -407,16 +448,38 @@ __global__ __launch_bounds__(512) void moe_down_one_kernel(MoeLaunch a) {
 // ---------------------------------------------------------------------------
 // Token rows together
 // ---------------------------------------------------------------------------
-// Block 0 routes; block 1 + m pads row m with zeros to whole tiles, where the
-// matrix kernel reads it without asking for its end.
+// Sum over a workgroup.
+__device__ __forceinline__ int block_sum(int *red, int v) {
+    v = wave_sum(v);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0;
+    for (int i = 0; i < int(blockDim.x) >> 6; ++i) v += red[i];
+    return v;
+}
+
+// Block 1 + m: the experts of token m and their weights, and its row, padded
+// with zeros to whole tiles (where the matrix kernel reads it without asking
+// for its end), and the row's sum.  Block 0: the experts' tokens.
 __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeLaunch a, int slots) {
     __shared__ uint32_t mask[W2A8_MOE_MAX_E][2];      // tokens of an expert
-    __shared__ int ends[2][W2A8_MOE_MAX_E], begins[W2A8_MOE_MAX_E];
+    __shared__ int begins[W2A8_MOE_MAX_E], red[kRouteWaves];
     const int tid = int(threadIdx.x), lane = tid & 63, wv = tid >> 6;
     if (blockIdx.x > 0) {
         const int m = int(blockIdx.x) - 1, Hp = (a.H + kTileK - 1) / kTileK * kTileK;
         const int8_t *row = a.x + int64_t(m) * a.H;
         uint8_t *out = a.ws + a.sp.rows + int64_t(m) * Hp;
+        if (wv == kRouteWaves - 1) {      // (the wave that has least of the row)
+            Router r;
+            r.load(a, m, lane);
+            r.keys();
+            int expert;
+            float weight;
+            r.all(a, lane, &expert, &weight);
+            Picked *to = reinterpret_cast<Picked *>(a.ws + a.sp.picked) + m * a.top_k;
+            if (lane < a.top_k) to[lane] = Picked{expert, weight};
+        }
+        int sum = 0;
         for (int k = 16 * tid; k < Hp; k += 16 * kRouteThreads) {
             v4u v;
             if (k + 16 <= a.H) {
@@ -427,57 +490,75 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeLaunch a, i
                 v = v4u{w[0], w[1], w[2], w[3]};
             }
             *reinterpret_cast<v4u *>(out + k) = v;
+            sum = add16(v, sum);
         }
+        sum = block_sum(red, sum);
+        if (tid == 0) reinterpret_cast<int *>(a.ws + a.sp.row_sums)[m] = sum;
         return;
     }
     Slot *slot = reinterpret_cast<Slot *>(a.ws + a.sp.slot);
     Pairs *pairs = reinterpret_cast<Pairs *>(a.ws + a.sp.pair);
+    Router r[kRouteTokens];
+#pragma unroll
+    for (int i = 0; i < kRouteTokens; ++i)
+        if (wv + i * kRouteWaves < a.M) r[i].load(a, wv + i * kRouteWaves, lane);
     if (tid < W2A8_MOE_MAX_E) mask[tid][0] = mask[tid][1] = 0;
     __syncthreads();
     int expert[kRouteTokens];           // of rank `lane`, of this wave's tokens
-    float weight[kRouteTokens];
 #pragma unroll
     for (int i = 0; i < kRouteTokens; ++i) {
         const int m = wv + i * kRouteWaves;
         expert[i] = -1;
         if (m >= a.M) continue;
-        Router r;
-        r.load(a, m, lane);
-        r.all(a, lane, &expert[i], &weight[i]);
-        if (lane < a.top_k && expert[i] >= 0) atomicOr(&mask[expert[i]][m >> 5], 1u << (m & 31));
+        r[i].keys();
+        for (int j = 0; j < a.top_k; ++j) {
+            float v;
+            const int e = r[i].next(a.E, lane, &v);
+            if (e < 0) break;
+            if (lane == j) expert[i] = e;
+        }
+        if (expert[i] >= 0) atomicOr(&mask[expert[i]][m >> 5], 1u << (m & 31));
     }
     __syncthreads();
     // Places of the experts' pairs and slots: sums of (pairs, experts) over
-    // the experts before, in one word.
-    const int n = tid < W2A8_MOE_MAX_E ? __popc(mask[tid][0]) + __popc(mask[tid][1]) : 0;
-    const int both = n + (n ? 1 << 16 : 0);
-    if (tid < W2A8_MOE_MAX_E) ends[0][tid] = both;
-    __syncthreads();
-    int from = 0;
-    for (int o = 1; o < W2A8_MOE_MAX_E; o *= 2) {
-        if (tid < W2A8_MOE_MAX_E) ends[from ^ 1][tid] = ends[from][tid] + (tid >= o ? ends[from][tid - o] : 0);
-        from ^= 1;
-        __syncthreads();
-    }
-    const int used = ends[from][W2A8_MOE_MAX_E - 1];
-    if (tid < W2A8_MOE_MAX_E) {
-        const int before = ends[from][tid] - both;
-        begins[tid] = before & 0xFFFF;
-        if (n) slot[before >> 16] = Slot{tid, before & 0xFFFF, {mask[tid][0], mask[tid][1]}};
-        if (tid >= used >> 16 && tid < slots) slot[tid] = Slot{-1, 0, {0, 0}};
-        if (tid == 0) pairs->count = used & 0xFFFF;
+    // the experts before, in one word.  One wave, four experts a lane.
+    if (wv == 0) {
+        int n[kPerLane], before = 0;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+            const int e = kPerLane * lane + i;
+            n[i] = __popc(mask[e][0]) + __popc(mask[e][1]);
+            before += n[i] + (n[i] ? 1 << 16 : 0);
+        }
+        const int mine = before;
+        for (int o = 1; o < 64; o *= 2) {
+            const int up = __shfl_up(before, o);
+            before += lane >= o ? up : 0;
+        }
+        const int used = __shfl(before, 63);
+        before -= mine;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+            const int e = kPerLane * lane + i;
+            begins[e] = before & 0xFFFF;
+            if (n[i]) {
+                slot[before >> 16] = Slot{e, before & 0xFFFF, {mask[e][0], mask[e][1]}};
+                before += n[i] + (1 << 16);
+            }
+            if (e >= used >> 16 && e < slots) slot[e] = Slot{-1, 0, {0, 0}};
+        }
+        if (lane == 0) pairs->count = used & 0xFFFF;
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kRouteTokens; ++i) {
         const int m = wv + i * kRouteWaves, e = expert[i];
         if (m >= a.M || lane >= a.top_k) continue;
-        int at = e;
+        int at = -1;
         if (e >= 0) {
             const uint32_t lo = mask[e][0], hi = mask[e][1];
             at = begins[e] + (m < 32 ? __popc(lo & ((1u << m) - 1u))
                                      : __popc(lo) + __popc(hi & ((1u << (m - 32)) - 1u)));
-            pairs->weight[at] = weight[i];
         }
         pairs->of[m * a.top_k + lane] = at;
     }
@@ -488,7 +569,8 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeLaunch a, i
 // bytes of k-part c of both, and holds results of weight row r and activation
 // rows 4c .. 4c + 3.  A T32x128 slot holds four rows, so lane r stands for rows
 // 2r and 2r + 1 of the strip, the two words of 8 bytes of a slot, and reads
-// those of k-parts c and 4 + c: one tile in four instructions.
+// those of k-parts c and 4 + c: one tile in four instructions.  It multiplies the
+// codes w + 1 as they are; the sums are less the row's sum at the end.
 struct Words {
     v2u h[2];
 };
@@ -499,12 +581,17 @@ __device__ __forceinline__ Words load_words(const uint8_t *w) {
     return d;
 }
 __device__ __forceinline__ int words_at(int r, int c) { return 16 * (8 * (r >> 1) + c) + 8 * (r & 1); }
+// The 16 codes w + 1 of a word as bytes, in the order of k.
+__device__ __forceinline__ v4i code_bytes(uint32_t w) {
+    return v4i{int(w & 0x03030303u), int((w >> 2) & 0x03030303u), int((w >> 4) & 0x03030303u),
+               int((w >> 6) & 0x03030303u)};
+}
 __device__ __forceinline__ void add_tile(const Words &w, const v4u (&x)[2], v4i (&acc)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, x[h]), expand_word(w.h[h][j]),
+            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, x[h]), code_bytes(w.h[h][j]),
                                                            acc[j], 0, 0, 0);
 }
 
@@ -577,45 +664,61 @@ __device__ __forceinline__ int token_of(uint64_t mask, int first, int r) {
 
 typedef v2f v2f_a __attribute__((aligned(4)));
 
+// STRIPS strips of a slot's expert to a workgroup (those past the last are
+// read as the last, and not stored): its rows are read once for all of them.
+template <int STRIPS, int D>
 __global__ __launch_bounds__(512) void moe_up_kernel(MoeLaunch a) {
     extern __shared__ __attribute__((aligned(16))) int red[];
     const Slot slot = reinterpret_cast<const Slot *>(a.ws + a.sp.slot)[blockIdx.y];
     if (slot.expert < 0) return;
-    const int s = int(blockIdx.x);
+    const int s0 = STRIPS * int(blockIdx.x);
     float *hidden = reinterpret_cast<float *>(a.ws + a.sp.hidden);
     const uint64_t mask = (uint64_t(slot.mask[1]) << 32) | slot.mask[0];
     const int tokens = __popcll(mask);
     const int lane = int(threadIdx.x) & 63, r = lane & 15, c = lane >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), nw = int(blockDim.x) >> 6;
-    const int KT = (a.H + kTileK - 1) / kTileK;
-    const int64_t off = int64_t(slot.expert) * a.wb1 + int64_t(s) * KT * kTileBytes + words_at(r, c);
-    const uint8_t *const w[2] = {a.w_gate + off, a.w_up + off};
+    const int KT = (a.H + kTileK - 1) / kTileK, last = (a.I - 1) / kTileRows;
+    const uint8_t *w[2 * STRIPS];
+#pragma unroll
+    for (int k = 0; k < STRIPS; ++k) {
+        const int64_t off = int64_t(slot.expert) * a.wb1 + int64_t(min(s0 + k, last)) * KT * kTileBytes + words_at(r, c);
+        w[2 * k] = a.w_gate + off;
+        w[2 * k + 1] = a.w_up + off;
+    }
     const int8_t *rows = reinterpret_cast<const int8_t *>(a.ws + a.sp.rows) + 16 * c;
+    const int *row_sums = reinterpret_cast<const int *>(a.ws + a.sp.row_sums);
     const float sg = a.s_gate[slot.expert], su = a.s_up[slot.expert];
 
     for (int m0 = 0; m0 < tokens; m0 += kMoeRows) {
         const int token = token_of(mask, m0, r);
         const float mine = a.sa[token];            // of row r
-        v4i acc[2][2];
-        strip_sums<2, 3>(w, rows + int64_t(token) * KT * kTileK, KT, wv, nw, acc);
-        v4i v[4] = {acc[0][0], acc[0][1], acc[1][0], acc[1][1]};
+        const int sum = row_sums[token];
+        v4i acc[2 * STRIPS][2];
+        strip_sums<2 * STRIPS, D>(w, rows + int64_t(token) * KT * kTileK, KT, wv, nw, acc);
+        v4i v[4 * STRIPS];
+#pragma unroll
+        for (int k = 0; k < 4 * STRIPS; ++k) v[k] = acc[k >> 1][k & 1];
         join_waves(red, lane, wv, nw, v);
         // Lane (r, c): weight rows 2r + j, pairs m0 + 4c + i.
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i % nw != wv) continue;
             const float sa = __shfl(mine, 4 * c + i);
-            const int m = m0 + 4 * c + i, row = s * kTileRows + 2 * r;
-            float h[2];
+            const int sx = __shfl(sum, 4 * c + i), m = m0 + 4 * c + i;
+            if (m >= tokens) continue;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                h[j] = activate(a.act, (float(v[j][i]) * sa) * sg, (float(v[2 + j][i]) * sa) * su);
-            float *out = hidden + int64_t(slot.begin + m) * a.I + row;
-            if (m >= tokens || row >= a.I) continue;
-            if (row + 1 < a.I)
-                *reinterpret_cast<v2f_a *>(out) = v2f{h[0], h[1]};
-            else
-                out[0] = h[0];
+            for (int k = 0; k < STRIPS; ++k) {
+                const int row = (s0 + k) * kTileRows + 2 * r;
+                float h[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    h[j] = activate(a.act, (float(v[4 * k + j][i] - sx) * sa) * sg, (float(v[4 * k + 2 + j][i] - sx) * sa) * su);
+                float *out = hidden + int64_t(slot.begin + m) * a.I + row;
+                if (row + 1 < a.I)
+                    *reinterpret_cast<v2f_a *>(out) = v2f{h[0], h[1]};
+                else if (row < a.I)
+                    out[0] = h[0];
+            }
         }
     }
 }
@@ -626,6 +729,7 @@ constexpr int kQuantThreads = 512, kQuantKept = 4;
 
 __global__ __launch_bounds__(kQuantThreads) void moe_quant_kernel(MoeLaunch a) {
     __shared__ uint32_t most[kQuantThreads / 64];
+    __shared__ int red[kQuantThreads / 64];
     const int pair = int(blockIdx.x), tid = int(threadIdx.x);
     const float *h = reinterpret_cast<const float *>(a.ws + a.sp.hidden) + int64_t(pair) * a.I;
     const int Ip = (a.I + kTileK - 1) / kTileK * kTileK;
@@ -648,48 +752,68 @@ __global__ __launch_bounds__(kQuantThreads) void moe_quant_kernel(MoeLaunch a) {
     for (int i = 0; i < kQuantThreads / 64; ++i) top = max(top, most[i]);
     const float factor = code_factor(__uint_as_float(top));
     uint32_t *out = reinterpret_cast<uint32_t *>(a.ws + a.sp.codes + int64_t(pair) * Ip);
+    int sum = 0;
+    auto store = [&](int g, v4f f) __attribute__((always_inline)) {
+        const uint32_t w = codes4(f, factor);
+        out[g] = w;
+        sum = dot4(w, 0x01010101u, sum);
+    };
 #pragma unroll
     for (int i = 0; i < kQuantKept; ++i)
-        if (4 * (tid + kQuantThreads * i) < Ip) out[tid + kQuantThreads * i] = codes4(kept[i], factor);
-    for (int g = tid + kQuantThreads * kQuantKept; 4 * g < Ip; g += kQuantThreads)
-        out[g] = codes4(load4(h, 4 * g, a.I), factor);
-    if (tid == 0) reinterpret_cast<float *>(a.ws + a.sp.scales)[pair] = code_scale(__uint_as_float(top));
+        if (4 * (tid + kQuantThreads * i) < Ip) store(tid + kQuantThreads * i, kept[i]);
+    for (int g = tid + kQuantThreads * kQuantKept; 4 * g < Ip; g += kQuantThreads) store(g, load4(h, 4 * g, a.I));
+    sum = block_sum(red, sum);
+    if (tid != 0) return;
+    reinterpret_cast<float *>(a.ws + a.sp.scales)[pair] = code_scale(__uint_as_float(top));
+    reinterpret_cast<int *>(a.ws + a.sp.code_sums)[pair] = sum;
 }
 
+template <int STRIPS, int D>
 __global__ __launch_bounds__(512) void moe_down_kernel(MoeLaunch a) {
     extern __shared__ __attribute__((aligned(16))) int red[];
     const Slot slot = reinterpret_cast<const Slot *>(a.ws + a.sp.slot)[blockIdx.y];
     if (slot.expert < 0) return;
-    const int s = int(blockIdx.x);
-    const Pairs *pairs = reinterpret_cast<const Pairs *>(a.ws + a.sp.pair);
+    const int s0 = STRIPS * int(blockIdx.x);
     const float *scales = reinterpret_cast<const float *>(a.ws + a.sp.scales);
+    const int *code_sums = reinterpret_cast<const int *>(a.ws + a.sp.code_sums);
     float *part = reinterpret_cast<float *>(a.ws + a.sp.part);
     const int tokens = __popc(slot.mask[0]) + __popc(slot.mask[1]);
     const int lane = int(threadIdx.x) & 63, r = lane & 15, c = lane >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), nw = int(blockDim.x) >> 6;
-    const int KT = (a.I + kTileK - 1) / kTileK;
-    const uint8_t *const w[1] = {a.w_down + int64_t(slot.expert) * a.wb2 + int64_t(s) * KT * kTileBytes + words_at(r, c)};
+    const int KT = (a.I + kTileK - 1) / kTileK, last = (a.H - 1) / kTileRows;
+    const uint8_t *w[STRIPS];
+#pragma unroll
+    for (int k = 0; k < STRIPS; ++k)
+        w[k] = a.w_down + int64_t(slot.expert) * a.wb2 + int64_t(min(s0 + k, last)) * KT * kTileBytes + words_at(r, c);
     const int8_t *codes = reinterpret_cast<const int8_t *>(a.ws + a.sp.codes) + 16 * c;
     const float sd = a.s_down[slot.expert];
 
     for (int m0 = 0; m0 < tokens; m0 += kMoeRows) {
         const int at = slot.begin + min(m0 + r, tokens - 1);
-        const float mine = scales[at], weight = pairs->weight[at];      // of row r
-        v4i acc[1][2];
-        strip_sums<1, 4>(w, codes + int64_t(at) * KT * kTileK, KT, wv, nw, acc);
-        join_waves(red, lane, wv, nw, acc[0]);
+        const float mine = scales[at];             // of row r
+        const int sum = code_sums[at];
+        v4i acc[STRIPS][2];
+        strip_sums<STRIPS, D>(w, codes + int64_t(at) * KT * kTileK, KT, wv, nw, acc);
+        v4i v[2 * STRIPS];
+#pragma unroll
+        for (int k = 0; k < 2 * STRIPS; ++k) v[k] = acc[k >> 1][k & 1];
+        join_waves(red, lane, wv, nw, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i % nw != wv) continue;
-            const float sh = __shfl(mine, 4 * c + i), p = __shfl(weight, 4 * c + i);
-            const int m = m0 + 4 * c + i, row = s * kTileRows + 2 * r;
-            float *out = part + int64_t(slot.begin + m) * a.H + row;
-            const v2f y = {p * ((float(acc[0][0][i]) * sh) * sd), p * ((float(acc[0][1][i]) * sh) * sd)};
-            if (m >= tokens || row >= a.H) continue;
-            if (row + 1 < a.H)
-                *reinterpret_cast<v2f_a *>(out) = y;
-            else
-                out[0] = y[0];
+            const float sh = __shfl(mine, 4 * c + i);
+            const int sx = __shfl(sum, 4 * c + i), m = m0 + 4 * c + i;
+            if (m >= tokens) continue;
+#pragma unroll
+            for (int k = 0; k < STRIPS; ++k) {
+                const int row = (s0 + k) * kTileRows + 2 * r;
+                float *out = part + int64_t(slot.begin + m) * a.H + row;
+                const v2f y = {(float(v[2 * k][i] - sx) * sh) * sd, (float(v[2 * k + 1][i] - sx) * sh) * sd};
+                if (row + 1 < a.H)
+                    *reinterpret_cast<v2f_a *>(out) = y;
+                else if (row < a.H)
+                    out[0] = y[0];
+            }
         }
     }
 }
@@ -697,14 +821,15 @@ __global__ __launch_bounds__(512) void moe_down_kernel(MoeLaunch a) {
 __global__ __launch_bounds__(256) void moe_combine_kernel(MoeLaunch a) {
     const int n = int(blockIdx.x) * 256 + int(threadIdx.x), m = int(blockIdx.y);
     const int *of = reinterpret_cast<const Pairs *>(a.ws + a.sp.pair)->of + m * a.top_k;
+    const Picked *picked = reinterpret_cast<const Picked *>(a.ws + a.sp.picked) + m * a.top_k;
     const float *part = reinterpret_cast<const float *>(a.ws + a.sp.part);
     if (n >= a.H) return;
-    float y = of[0] == -2 ? __builtin_nanf("") : 0.0f;
+    float y = picked[0].expert == -2 ? __builtin_nanf("") : 0.0f;
 #pragma unroll 4
     for (int j = 0; j < a.top_k; ++j) {
         const int at = of[j];
         const float p = part[int64_t(max(at, 0)) * a.H + n];
-        y += at >= 0 ? p : 0.0f;
+        y += at >= 0 ? picked[j].weight * p : 0.0f;
     }
     const int64_t at = int64_t(m) * a.H + n;
     if (a.y_f32) a.y_f32[at] = y;
@@ -718,18 +843,10 @@ hipError_t launch(const void *fn, dim3 grid, int threads, size_t lds, void **arg
 // Most LDS of the hidden rows of a token (the kernel has some of its own).
 constexpr int64_t kOneLds = 49152;
 #ifndef ONE_M
-#define ONE_M 1
+#define ONE_M 3
 #endif
 bool one_at_a_time(const MoeLaunch &a) {
     return a.M <= ONE_M && a.top_k * round_up(a.I, kTileK) <= kOneLds;
-}
-
-// Waves of a workgroup of the matrix kernels: some 16 on a compute unit.
-int moe_waves(int64_t groups, int64_t KT, int cus) {
-#ifdef MOE_NW
-    return MOE_NW;
-#endif
-    return int(std::max<int64_t>(1, std::min<int64_t>({8, KT, 16 * int64_t(cus) / groups})));
 }
 
 }  // namespace
@@ -748,6 +865,8 @@ MoeSpace moe_space(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k) {
     s.slot = take(W2A8_MOE_MAX_E * sizeof(Slot));
     s.pair = take(sizeof(Pairs));
     s.scales = take(4 * pairs);
+    s.code_sums = take(4 * pairs);
+    s.row_sums = take(4 * M);
     s.rows = take(M * round_up(H, kTileK));
     s.codes = take(pairs * round_up(I, kTileK));
     s.hidden = take(4 * pairs * I);
@@ -764,21 +883,25 @@ hipError_t launch_moe(const MoeLaunch &la, int cus, hipStream_t stream) {
     void *args[] = {&a, &slots};
     hipError_t e;
     if (one_at_a_time(a)) {
-        e = launch(fn(&moe_up_one_kernel), dim3(unsigned(up), unsigned(a.top_k), unsigned(a.M)), 512, 0, args, stream);
+        e = launch(fn(&moe_up_one_kernel), dim3(unsigned(up + 1), unsigned(a.top_k), unsigned(a.M)), 512, 0, args,
+                   stream);
         if (e != hipSuccess) return e;
-        return launch(fn(&moe_down_one_kernel), dim3(unsigned(ceil_div(a.H, 16)), unsigned(a.M)), 512,
+        return launch(fn(&moe_down_one_kernel), dim3(unsigned(ceil_div(a.H, kDownRows)), unsigned(a.M)), kDownThreads,
                       size_t(a.top_k * round_up(a.I, kTileK)), args, stream);
     }
     const int64_t KT1 = ceil_div(a.H, kTileK), KT2 = ceil_div(a.I, kTileK);
-    const int nw1 = moe_waves(up * slots, KT1, cus), nw2 = moe_waves(down * slots, KT2, cus);
+        // Two strips to a workgroup where that leaves four workgroups to a compute unit.
+    const bool up2 = ceil_div(up, 2) * slots >= 4 * cus, down2 = ceil_div(down, 2) * slots >= 4 * cus;
+    const int nw1 = int(std::min<int64_t>(kMoeWaves, KT1)), nw2 = int(std::min<int64_t>(kMoeWaves, KT2));
+    const size_t lds1 = size_t(nw1) * (up2 ? 8192 : 4096), lds2 = size_t(nw2) * (down2 ? 4096 : 2048);
     if ((e = launch(fn(&moe_route_kernel), dim3(unsigned(1 + a.M)), kRouteThreads, 0, args, stream)) != hipSuccess) return e;
-    if ((e = launch(fn(&moe_up_kernel), dim3(unsigned(up), unsigned(slots)), 64 * nw1, size_t(nw1) * 4096, args, stream)) !=
-        hipSuccess)
+    if ((e = launch(up2 ? fn(&moe_up_kernel<2, 2>) : fn(&moe_up_kernel<1, 3>),
+                    dim3(unsigned(ceil_div(up, up2 ? 2 : 1)), unsigned(slots)), 64 * nw1, lds1, args, stream)) != hipSuccess)
         return e;
     if ((e = launch(fn(&moe_quant_kernel), dim3(unsigned(a.M * a.top_k)), kQuantThreads, 0, args, stream)) != hipSuccess)
         return e;
-    if ((e = launch(fn(&moe_down_kernel), dim3(unsigned(down), unsigned(slots)), 64 * nw2, size_t(nw2) * 2048, args,
-                    stream)) != hipSuccess)
+    if ((e = launch(down2 ? fn(&moe_down_kernel<2, 3>) : fn(&moe_down_kernel<1, 4>),
+                    dim3(unsigned(ceil_div(down, down2 ? 2 : 1)), unsigned(slots)), 64 * nw2, lds2, args, stream)) != hipSuccess)
         return e;
     return launch(fn(&moe_combine_kernel), dim3(unsigned(ceil_div(a.H, 256)), unsigned(a.M)), 256, 0, args, stream);
 }
