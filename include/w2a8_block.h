@@ -81,15 +81,21 @@ int pack_w4a8(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros
 int unpack_w4a8(const void *packed, int64_t packed_bytes, int64_t N, int64_t K, int64_t group,
                 uint8_t *codes, uint16_t *scales, uint8_t *zeros);
 
+/* Device workspace bytes of w4a8_gemm, or -1 if a size is out of range: 0 up
+ * to 16 rows, else room for the sums of up to 8 parts of k. */
+int64_t w4a8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
 /* Product of int8 rows with them, 1 <= M <= W4A8_MAX_M (W2A8_ERR_SHAPE above):
  *   y[m][n] = s_a[m] * sum_g s[n][g] * sum_{k in g} (q[n][k] - z[n][g]) * x[m][k]
  * The sum over a group is exact, that over groups is in fp32.
  * x: device, int8 [M][K]; s_a: device, fp32 [M].  scale_type: W2A8_BF16 or
  * W2A8_F16.  zeros: whether w_packed has zero points.  y_f32, y_bf16: device,
- * [M][N], at least one of them. */
+ * [M][N], at least one of them.  workspace: device, at least
+ * w4a8_workspace_bytes(M, N, K) bytes, 16-byte aligned (NULL when that is 0);
+ * needs no clearing and holds nothing between calls. */
 int w4a8_gemm(const void *w_packed, const int8_t *x, const float *s_a, int64_t M, int64_t N,
               int64_t K, int64_t group, int scale_type, int zeros, float *y_f32, uint16_t *y_bf16,
-              void *stream);
+              void *workspace, int64_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
  * Mixture of ternary experts for a few tokens.

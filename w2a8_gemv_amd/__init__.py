@@ -31,7 +31,7 @@ __all__ = [
     "quant_act_mx4", "dequant_act_mx4", "quant_pack_mx4", "w4mx4_gemm", "w2mx4_gemm",
     "w4mx4_linear_gemv", "w2mx4_linear_gemv", "gemm_w4mx4", "gemm_w2mx4", "linear_w4mx4",
     "linear_w2mx4", "rmsnorm_quant_int8", "w4a8_packed_bytes", "pack_w4a8", "unpack_w4a8",
-    "w4a8_gemm", "gemm_w4a8", "linear_w4a8", "w2a8_moe_workspace_bytes", "w2a8_moe", "moe",
+    "w4a8_workspace_bytes", "w4a8_gemm", "gemm_w4a8", "linear_w4a8", "w2a8_moe_workspace_bytes", "w2a8_moe", "moe",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw2a8.so")
@@ -115,12 +115,14 @@ def lib():
             getattr(L, name).restype = I32
         L.w4a8_packed_bytes.argtypes = [I64, I64, I64, I32]
         L.w4a8_packed_bytes.restype = I64
+        L.w4a8_workspace_bytes.argtypes = [I64, I64, I64]
+        L.w4a8_workspace_bytes.restype = I64
         L.w2a8_moe_workspace_bytes.argtypes = [I64] * 5
         L.w2a8_moe_workspace_bytes.restype = I64
         for name, args in (("rmsnorm_quant_int8", [P, P, P, I32, I64, I64, F32, P, P, P, P]),
                            ("pack_w4a8", [P, P, P, I64, I64, I64, P, I64]),
                            ("unpack_w4a8", [P, I64, I64, I64, I64, P, P, P]),
-                           ("w4a8_gemm", [P, P, P, I64, I64, I64, I64, I32, I32, P, P, P]),
+                           ("w4a8_gemm", [P, P, P, I64, I64, I64, I64, I32, I32, P, P, P, I64, P]),
                            ("w2a8_moe", [P, P, P, I32, P, P, P, P, P, P, I64, I64, I64, I64, I64,
                                          I32, I32, P, P, P, I64, P])):
             getattr(L, name).argtypes = args
@@ -1013,23 +1015,38 @@ def unpack_w4a8(packed: torch.Tensor, N: int, K: int, group: int, scale_dtype=to
     return codes, scales, z
 
 
-def _w4_gemm(w_packed, x, s_a, M, N, K, group, scale_dtype, zeros, yf, yb, dev, stream):
+@functools.lru_cache(maxsize=4096)
+def w4a8_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Workspace bytes of w4a8_gemm (not to be cleared): 0 up to 16 rows."""
+    v = int(lib().w4a8_workspace_bytes(M, N, K))
+    if v < 0:
+        raise W2A8Error(2, "w4a8_gemm")
+    return v
+
+
+def _w4_gemm(w_packed, x, s_a, M, N, K, group, scale_dtype, zeros, yf, yb, dev, workspace, stream):
     pw = _mx4_ptr(w_packed, "w_packed", dev, torch.uint8, w4a8_packed_bytes(N, K, group, zeros))
     px = _mx4_ptr(x, "x", dev, torch.int8, M * K, M * K)
     ps = _mx4_ptr(s_a, "s_a", dev, torch.float32, M, M)
-    st = lib().w4a8_gemm(pw, px, ps, M, N, K, group, _w4_scale_type(scale_dtype), int(bool(zeros)),
-                         yf, yb, _mx4_stream(stream, dev))
+    code, need, pws = _w4_scale_type(scale_dtype), w4a8_workspace_bytes(M, N, K), None
+    if need:
+        if workspace is None:
+            workspace = _mx4_empty(x, (need,), torch.uint8, stream)
+        pws = _mx4_ptr(workspace, "workspace", dev, torch.uint8, need)
+    st = lib().w4a8_gemm(pw, px, ps, M, N, K, group, code, int(bool(zeros)), yf, yb, pws, need,
+                         _mx4_stream(stream, dev))
     if st:
         raise W2A8Error(st, "w4a8_gemm")
 
 
 def w4a8_gemm(w_packed, x, s_a, M, N, K, group, scale_dtype=torch.float16, zeros=False, y_f32=None,
-              y_bf16=None, stream=None):
+              y_bf16=None, workspace=None, stream=None):
     """Raw C-ABI call: int8 rows times 4-bit weights with group scales (outputs must be
-    given); returns nothing."""
+    given; workspace: uint8, at least w4a8_workspace_bytes, made here if not given); returns
+    nothing."""
     dev = _mx4_gpu(x, "x")
     yf, yb = _mx4_outputs(y_f32, y_bf16, dev, M * N)
-    _w4_gemm(w_packed, x, s_a, M, N, K, group, scale_dtype, zeros, yf, yb, dev, stream)
+    _w4_gemm(w_packed, x, s_a, M, N, K, group, scale_dtype, zeros, yf, yb, dev, workspace, stream)
 
 
 def gemm_w4a8(w_packed, x_q, s_a, N, K, group, scale_dtype=torch.float16, zeros=False,
@@ -1041,7 +1058,7 @@ def gemm_w4a8(w_packed, x_q, s_a, N, K, group, scale_dtype=torch.float16, zeros=
     if k != K:
         raise ValueError(f"x_q must have rows of {K} values, got {k}")
     y, yf, yb = _mx4_new(x_q, out_dtype, (M, N), stream)
-    _w4_gemm(w_packed, x_q, s_a, M, N, K, group, scale_dtype, zeros, yf, yb, dev, stream)
+    _w4_gemm(w_packed, x_q, s_a, M, N, K, group, scale_dtype, zeros, yf, yb, dev, None, stream)
     return y
 
 

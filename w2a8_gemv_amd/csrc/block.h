@@ -58,7 +58,11 @@ struct W4Launch {
     uint16_t *y_bf16;
     int M, N, K, KT, GQ;
     int group, bf16_scales, strips;
+    float *ws;                 // sums of parts of k, [part][M][N]
+    int parts;
 };
+// Most parts that k is split into (and the rows from which it may be).
+constexpr int kW4Parts = 8, kW4PartRows = 17;
 hipError_t launch_w4a8(const W4Launch &a, int cus, hipStream_t stream);
 
 // Mixture of experts: offsets into the workspace, all multiples of 256.

@@ -41,6 +41,11 @@ W4Size w4_size(int64_t N, int64_t K, int64_t group, bool zeros) {
     return s;
 }
 
+// Space for the parts of k of the products that may split it.
+int64_t w4_workspace(int64_t M, int64_t N, int64_t K) {
+    return M < kW4PartRows || w4_tiles(K) < 16 ? 0 : 4 * M * N * std::min<int64_t>(kW4Parts, w4_tiles(K) / 8);
+}
+
 bool moe_ok(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k) {
     return M >= 1 && M <= W2A8_MOE_MAX_M && H >= 1 && H <= W2A8_MAX_K && I >= 1 && I <= W2A8_MAX_K &&
            E >= 1 && E <= W2A8_MOE_MAX_E && top_k >= 1 && top_k <= E && top_k <= W2A8_MOE_MAX_TOP_K;
@@ -137,18 +142,32 @@ int unpack_w4a8(const void *packed, int64_t packed_bytes, int64_t N, int64_t K, 
     return W2A8_OK;
 }
 
+int64_t w4a8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (M < 1 || M > W4A8_MAX_M || !matrix_ok(N, K)) return -1;
+    return w4_workspace(M, N, K);
+}
+
 int w4a8_gemm(const void *w_packed, const int8_t *x, const float *s_a, int64_t M, int64_t N, int64_t K,
-              int64_t group, int scale_type, int zeros, float *y_f32, uint16_t *y_bf16, void *stream) {
+              int64_t group, int scale_type, int zeros, float *y_f32, uint16_t *y_bf16, void *workspace,
+              int64_t ws_bytes, void *stream) {
     if (!w_packed || !x || !s_a || (!y_f32 && !y_bf16)) return W2A8_ERR_NULL;
     if (M < 1 || M > W4A8_MAX_M || !matrix_ok(N, K)) return W2A8_ERR_SHAPE;
     if (!group_ok(group) || (scale_type != W2A8_BF16 && scale_type != W2A8_F16)) return W2A8_ERR_VALUE;
     if (!aligned16(w_packed) || !aligned16(x) || !aligned4(s_a) || !aligned16(y_f32) || !aligned16(y_bf16))
         return W2A8_ERR_ALIGN;
+    const int64_t need = w4_workspace(M, N, K);
+    if (need > 0) {
+        if (!workspace) return W2A8_ERR_NULL;
+        if (!aligned16(workspace)) return W2A8_ERR_ALIGN;
+        if (ws_bytes < need) return W2A8_ERR_BUFSIZE;
+    }
     const W4Size z = w4_size(N, K, group, zeros != 0);
     const auto clear = [&](const void *y, int64_t ny) {
         return !meet(y, ny, w_packed, z.total) && !meet(y, ny, x, M * K) && !meet(y, ny, s_a, M * 4);
     };
-    if (!clear(y_f32, M * N * 4) || !clear(y_bf16, M * N * 2) || meet(y_f32, M * N * 4, y_bf16, M * N * 2))
+    const int64_t nf = M * N * 4, nb = M * N * 2;
+    if (!clear(y_f32, nf) || !clear(y_bf16, nb) || meet(y_f32, nf, y_bf16, nb) ||
+        (need > 0 && (!clear(workspace, need) || meet(workspace, need, y_f32, nf) || meet(workspace, need, y_bf16, nb))))
         return W2A8_ERR_VALUE;
     DeviceInfo dev;
     const int st = current_device(&dev);
@@ -169,6 +188,8 @@ int w4a8_gemm(const void *w_packed, const int8_t *x, const float *s_a, int64_t M
     a.group = int(group);
     a.bf16_scales = scale_type == W2A8_BF16;
     a.strips = int(ceil_div(N, kW4Rows));
+    a.ws = static_cast<float *>(workspace);
+    a.parts = 1;
     const hipError_t e = launch_w4a8(a, dev.cus, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? W2A8_OK : W2A8_ERR_LAUNCH;
 }

@@ -147,7 +147,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4a8_kernel(W4Launch a) {
                 }
 #pragma unroll
                 for (int e = 0; e < RES; ++e)
-                    y[b][e] = __builtin_fmaf(float(ZEROS ? acc[e] - z16 * sum[e] : acc[e]), sc, y[b][e]);
+                    y[b][e] = __builtin_fmaf(float(ZEROS ? acc[e] - __mul24(z16, sum[e]) : acc[e]), sc, y[b][e]);
             }
         }
     };
@@ -209,13 +209,224 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4a8_kernel(W4Launch a) {
     }
 }
 
+// More rows (17 to 64): activations through LDS.  A workgroup of four waves
+// takes 4 * STRIPS strips, each wave STRIPS of them, and walks a range of the
+// tiles of k together; the rows' part of a tile (MB blocks of 16 rows x 128 k)
+// is staged once for all of them.  LDS holds it as [block][chunk of 16 k][row],
+// where every operand is 16 (or, for groups of 32, 8) bytes of a lane and a
+// quarter of a wave reads 256 bytes in a row; chunks are 16 bytes apart from
+// that, so that the stores of a row's chunks fall in different banks.  Rows
+// start anywhere, so they are staged through registers, a tile ahead.
+constexpr int kChunkBytes = 272;
+
+template <int P, int MB, bool ZEROS, int STRIPS>
+__global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(W4Launch a) {
+    constexpr int STAGE = MB * 8 * kChunkBytes, PER = (MB * 128 + 255) / 256;
+    constexpr int D = 3;                     // tiles of weights on their way
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][STAGE];
+    const int tid = int(threadIdx.x), lane = tid & 63, r = lane & 15, c = lane >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int s0 = (int(blockIdx.x) * 4 + wv) * STRIPS, part = int(blockIdx.y);
+    // Tiles t0 .. t1 - 1 of k.
+    const int t0 = int(int64_t(a.KT) * part / a.parts), t1 = int(int64_t(a.KT) * (part + 1) / a.parts);
+
+    const uint8_t *wp[STRIPS], *zp[STRIPS];
+    const uint16_t *sp[STRIPS];
+#pragma unroll
+    for (int k = 0; k < STRIPS; ++k) {
+        const int64_t s = min(s0 + k, a.strips - 1);       // (past the last: not stored)
+        wp[k] = a.w + s * a.KT * kW4TileBytes + 16 * lane;
+        sp[k] = a.scales + (s * a.GQ * 16 + r) * 4;
+        zp[k] = ZEROS ? a.zeros + (s * a.GQ * 16 + r) * 4 : nullptr;
+    }
+    struct Weights {
+        v4u w;
+        uint32_t s[(P + 1) / 2], z;
+    };
+    auto load_w = [&](int t, Weights (&d)[STRIPS]) __attribute__((always_inline)) {
+        const int g = P * t, at = (g >> 2) * 64 + (g & 3);
+#pragma unroll
+        for (int k = 0; k < STRIPS; ++k) {
+            d[k].w = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(wp[k] + int64_t(t) * kW4TileBytes));
+            if constexpr (P == 1)
+                d[k].s[0] = sp[k][at];
+            else
+#pragma unroll
+                for (int i = 0; i < P / 2; ++i) d[k].s[i] = reinterpret_cast<const uint32_t *>(sp[k] + at)[i];
+            if constexpr (ZEROS)
+                d[k].z = P == 1   ? zp[k][at]
+                         : P == 2 ? *reinterpret_cast<const uint16_t *>(zp[k] + at)
+                                  : *reinterpret_cast<const uint32_t *>(zp[k] + at);
+        }
+    };
+    // This thread's chunks of the rows: row id / 8, chunk id % 8 (rows past M
+    // repeat the last one).
+    const int8_t *xp[PER];
+    int to[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int id = tid + 256 * j, row = min(id >> 3, 16 * MB - 1), q = id & 7;
+        xp[j] = a.x + int64_t(min(row, a.M - 1)) * a.K;
+        to[j] = ((row >> 4) * 8 + q) * kChunkBytes + 16 * (row & 15);
+    }
+    const int q16 = 16 * (tid & 7);
+    v4u xv[PER];
+    auto load_x = [&](int t) __attribute__((always_inline)) {
+        const int k = t * kTileK + q16;
+        if ((t + 1) * kTileK <= a.K) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) xv[j] = *reinterpret_cast<const v4u_b *>(xp[j] + k);
+        } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                uint32_t w[4];
+                load_int8_tail<16>(xp[j], k, a.K, w);
+                xv[j] = v4u{w[0], w[1], w[2], w[3]};
+            }
+        }
+    };
+    auto store_x = [&](uint8_t *stage) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (MB * 128 % 256 == 0 || tid + 256 * j < MB * 128) *reinterpret_cast<v4u *>(stage + to[j]) = xv[j];
+    };
+
+    float y[STRIPS][MB][4];
+#pragma unroll
+    for (int k = 0; k < STRIPS; ++k)
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[k][b][e] = 0.0f;
+
+    auto use = [&](const Weights (&d)[STRIPS], const uint8_t *stage) __attribute__((always_inline)) {
+        const v4i none = {0, 0, 0, 0};
+        const v4u ones = {0x01010101u, 0x01010101u, 0x01010101u, 0x01010101u};
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float sc[STRIPS];
+            int z16[STRIPS];
+#pragma unroll
+            for (int k = 0; k < STRIPS; ++k) {
+                const uint32_t sb = (d[k].s[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
+                sc[k] = (a.bf16_scales ? __uint_as_float(sb << 16) : float(__builtin_bit_cast(_Float16, uint16_t(sb)))) * 0.0625f;
+                z16[k] = ZEROS ? int(d[k].z << (24 - 8 * i)) >> 24 << 4 : 0;
+            }
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                v4i acc[STRIPS], sum = none;
+#pragma unroll
+                for (int k = 0; k < STRIPS; ++k) acc[k] = none;
+                if constexpr (P == 4) {
+                    const v2u x = *reinterpret_cast<const v2u *>(stage + (b * 8 + 2 * i + (c >> 1)) * kChunkBytes + 16 * r + 8 * (c & 1));
+#pragma unroll
+                    for (int k = 0; k < STRIPS; ++k)
+                        acc[k] = mfma32(x, v2u{low_values(d[k].w[i]), high_values(d[k].w[i])}, acc[k]);
+                    if constexpr (ZEROS) sum = mfma32(x, v2u{ones[0], ones[1]}, sum);
+                } else {
+#pragma unroll
+                    for (int j = (P == 1 ? 0 : i); j < (P == 1 ? 2 : i + 1); ++j) {
+                        const v4u x = *reinterpret_cast<const v4u *>(stage + (b * 8 + (P == 1 ? 2 * c + j : 4 * j + c)) * kChunkBytes + 16 * r);
+#pragma unroll
+                        for (int k = 0; k < STRIPS; ++k) {
+                            const uint32_t w0 = d[k].w[2 * j], w1 = d[k].w[2 * j + 1];
+                            acc[k] = mfma64(x, v4u{low_values(w0), high_values(w0), low_values(w1), high_values(w1)}, acc[k]);
+                        }
+                        if constexpr (ZEROS) sum = mfma64(x, ones, sum);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < STRIPS; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[k][b][e] = __builtin_fmaf(float(ZEROS ? acc[k][e] - __mul24(z16[k], sum[e]) : acc[k][e]), sc[k], y[k][b][e]);
+            }
+        }
+    };
+
+    Weights d[D][STRIPS];
+    load_x(t0);
+#pragma unroll
+    for (int j = 0; j < D; ++j)
+        if (t0 + j < t1) load_w(t0 + j, d[j]);
+    store_x(lds[0]);
+    if (t0 + 1 < t1) load_x(t0 + 1);
+    __syncthreads();
+    // (Two stages and D weight sets: the loop's body is 2 D tiles.)
+    for (int t = t0; t < t1; t += 2 * D) {
+#pragma unroll
+        for (int j = 0; j < 2 * D; ++j) {
+            if (t + j < t1) {
+                if (t + j + 1 < t1) store_x(lds[(j + 1) & 1]);
+                if (t + j + 2 < t1) load_x(t + j + 2);
+                use(d[j % D], lds[j & 1]);
+                if (t + j + D < t1) load_w(t + j + D, d[j % D]);
+                __syncthreads();
+            }
+        }
+    }
+
+    // Lane (r, c) of strip k and block b: weight row r, activation rows 16b + 4c + e.
+#pragma unroll
+    for (int k = 0; k < STRIPS; ++k) {
+        const int row = (s0 + k) * kW4Rows + r;
+        if (row >= a.N) continue;
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int m = 16 * b + 4 * c + e;
+                if (m >= a.M) continue;
+                const int64_t at = int64_t(m) * a.N + row;
+                if (a.parts > 1) {
+                    a.ws[part * (int64_t(a.M) * a.N) + at] = y[k][b][e];
+                    continue;
+                }
+                const float v = y[k][b][e] * a.sa[m];
+                if (a.y_f32) a.y_f32[at] = v;
+                if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
+            }
+    }
+}
+
+// The parts of k, added in order.
+__global__ __launch_bounds__(256) void w4a8_join_kernel(W4Launch a) {
+    const int n = int(blockIdx.x) * 256 + int(threadIdx.x), m = int(blockIdx.y);
+    if (n >= a.N) return;
+    const int64_t at = int64_t(m) * a.N + n, all = int64_t(a.M) * a.N;
+    float v = 0.0f;
+#pragma unroll 8
+    for (int p = 0; p < a.parts; ++p) v += a.ws[p * all + at];
+    v *= a.sa[m];
+    if (a.y_f32) a.y_f32[at] = v;
+    if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
+}
+
+#ifndef TS
+#define TS 1
+#define WGC 2
+#endif
+template <int P, bool ZEROS>
+hipError_t w4_tiles_launch(const W4Launch &la, int cus, hipStream_t stream) {
+    W4Launch a = la;
+    const int blocks = int(ceil_div(a.strips, 4 * TS));
+    a.parts = std::max(1, std::min({WGC * cus / blocks, a.KT / 8, kW4Parts}));
+    const void *fn = a.M <= 32   ? reinterpret_cast<const void *>(&w4a8_tile_kernel<P, 2, ZEROS, TS>)
+                     : a.M <= 48 ? reinterpret_cast<const void *>(&w4a8_tile_kernel<P, 3, ZEROS, TS>)
+                                 : reinterpret_cast<const void *>(&w4a8_tile_kernel<P, 4, ZEROS, TS>);
+    void *args[] = {&a};
+    const hipError_t e = hipLaunchKernel(fn, dim3(unsigned(blocks), unsigned(a.parts)), dim3(256), args, 0, stream);
+    if (e != hipSuccess || a.parts == 1) return e;
+    return hipLaunchKernel(reinterpret_cast<const void *>(&w4a8_join_kernel),
+                           dim3(unsigned(ceil_div(a.N, 256)), unsigned(a.M)), dim3(256), args, 0, stream);
+}
+
 template <int P, bool ZEROS>
 hipError_t w4_launch(const W4Launch &a, int cus, hipStream_t stream) {
-    const void *fn = a.M == 1    ? reinterpret_cast<const void *>(&w4a8_kernel<P, 1, ZEROS, true>)
-                     : a.M <= 16 ? reinterpret_cast<const void *>(&w4a8_kernel<P, 1, ZEROS, false>)
-                     : a.M <= 32 ? reinterpret_cast<const void *>(&w4a8_kernel<P, 2, ZEROS, false>)
-                                 : reinterpret_cast<const void *>(&w4a8_kernel<P, 4, ZEROS, false>);
-    const int per = a.M == 1 ? 1 : a.M <= 16 ? 4 : a.M <= 32 ? 8 : 16;
+    if (a.M > 16) return w4_tiles_launch<P, ZEROS>(a, cus, stream);
+    const void *fn = a.M == 1 ? reinterpret_cast<const void *>(&w4a8_kernel<P, 1, ZEROS, true>)
+                              : reinterpret_cast<const void *>(&w4a8_kernel<P, 1, ZEROS, false>);
+    const int per = a.M == 1 ? 1 : 4;
     const int nw = std::min(kMaxWaves, a.KT);
     W4Launch l = a;
     void *args[] = {&l};
