@@ -612,15 +612,27 @@ __device__ __forceinline__ void strip_sums(const uint8_t *const (&w)[MATS], cons
     };
 #pragma unroll
     for (int k = 0; k < MATS; ++k) acc[k][0] = acc[k][1] = v4i{0, 0, 0, 0};
+    auto use = [&](int j) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < MATS; ++k) add_tile(d[j][k], xv[j], acc[k]);
+    };
 #pragma unroll
     for (int j = 0; j < D; ++j)
         if (j < n) load(j, j);
-    for (int i = 0; i < n; i += D) {
+    // While no load can be past the end none is asked for it: a load that may
+    // be skipped makes the compiler wait for all before it.
+    int i = 0;
+    for (; i + 2 * D <= n; i += D) {
 #pragma unroll
         for (int j = 0; j < D; ++j) {
-            if (i + j < n)
+            use(j);
+            load(i + j + D, j);
+        }
+    }
+    for (; i < n; i += D) {
 #pragma unroll
-                for (int k = 0; k < MATS; ++k) add_tile(d[j][k], xv[j], acc[k]);
+        for (int j = 0; j < D; ++j) {
+            if (i + j < n) use(j);
             if (i + j + D < n) load(i + j + D, j);
         }
     }

@@ -11,10 +11,11 @@
 //
 // Two values share a byte.  In the high half, as two's complement of q - 8, a
 // value is a signed byte of 16 times itself: the high values are one AND, the
-// low ones a shift and an AND, and the 16 goes out with the scale (a power of
-// two, so exactly).  A group's sum is at most 16 * 15 * 127 * 128 < 2^22, exact
-// as int32 and as fp32.  With zero points, one more instruction with a
-// constant operand of ones gives sum x of the group for every lane.
+// low ones a shift and an AND, and the 16 goes out in the end (a power of two,
+// so exactly).  With zero points a byte is q - z itself, three to four
+// operations a word.  A group's sum is at most 16 * 8 * 127 * 128 < 2^22, exact
+// as int32 and as fp32.  What is left of the work, and the most of it, is one
+// conversion and one multiply-add for every result and group.
 //
 // A workgroup takes one strip of 16 weight rows; its waves take the strip's
 // tiles (16 x 128, 1 KiB) in turn and add their sums in LDS in wave order.
@@ -26,9 +27,29 @@ namespace {
 
 constexpr int kMaxWaves = 8;
 
-// The 8 values of a word as signed bytes of 16 times themselves.
-__device__ __forceinline__ uint32_t low_values(uint32_t w) { return (w << 4) & 0xF0F0F0F0u; }
-__device__ __forceinline__ uint32_t high_values(uint32_t w) { return w & 0xF0F0F0F0u; }
+// The low and high values of a word (bytes of q - 8, two each) as signed bytes:
+// 16 (q - 8), or with a zero point (in every byte of z) q - z.  The latter takes
+// 128 + q - z, from which no byte borrows, and the sign bit back out.
+template <bool ZEROS>
+__device__ __forceinline__ uint32_t low_values(uint32_t w, uint32_t z) {
+    if constexpr (!ZEROS) return (w << 4) & 0xF0F0F0F0u;
+    return (((w & 0x0F0F0F0Fu) ^ 0x88888888u) - z) ^ 0x80808080u;
+}
+template <bool ZEROS>
+__device__ __forceinline__ uint32_t high_values(uint32_t w, uint32_t z) {
+    if constexpr (!ZEROS) return w & 0xF0F0F0F0u;
+    return low_values<true>(w >> 4, z);
+}
+// What the sums of such bytes are multiplied by, in the end.
+template <bool ZEROS>
+constexpr float kBack = ZEROS ? 1.0f : 0.0625f;
+// Zero point byte i (z - 8) of a word, as z in every byte.
+__device__ __forceinline__ uint32_t zero_bytes(uint32_t z, int i) {
+    return __builtin_amdgcn_perm(0u, (z & 0x0F0F0F0Fu) ^ 0x08080808u, 0x01010101u * uint32_t(i));
+}
+__device__ __forceinline__ float scale_value(uint32_t bits, int bf16) {
+    return bf16 ? __uint_as_float(bits << 16) : float(__builtin_bit_cast(_Float16, uint16_t(bits)));
+}
 
 __device__ __forceinline__ v4i mfma64(v4u x, v4u w, v4i acc) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, x), __builtin_bit_cast(v4i, w),
@@ -120,34 +141,27 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4a8_kernel(W4Launch a) {
         for (int e = 0; e < RES; ++e) y[b][e] = 0.0f;
 
     auto use = [&](const T &d) __attribute__((always_inline)) {
-        const v4i none = {0, 0, 0, 0};
-        const v4u ones = {0x01010101u, 0x01010101u, 0x01010101u, 0x01010101u};
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const uint32_t sb = (d.s[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
-            const float sc = (a.bf16_scales ? __uint_as_float(sb << 16)
-                                            : float(__builtin_bit_cast(_Float16, uint16_t(sb)))) * 0.0625f;
-            const int z16 = ZEROS ? int(d.z << (24 - 8 * i)) >> 24 << 4 : 0;
+            const float sc = scale_value((d.s[i >> 1] >> (16 * (i & 1))) & 0xFFFFu, a.bf16_scales);
+            const uint32_t z = ZEROS ? zero_bytes(d.z, i) : 0u;
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
-                v4i acc = none, sum = none;
+                v4i acc = {0, 0, 0, 0};
                 const uint32_t *x = d.x[b];
                 if constexpr (P == 4) {
-                    const v2u xo = {x[2 * i], x[2 * i + 1]};
-                    acc = mfma32(xo, v2u{low_values(d.w[i]), high_values(d.w[i])}, acc);
-                    if constexpr (ZEROS) sum = mfma32(xo, v2u{ones[0], ones[1]}, sum);
+                    acc = mfma32(v2u{x[2 * i], x[2 * i + 1]}, v2u{low_values<ZEROS>(d.w[i], z), high_values<ZEROS>(d.w[i], z)}, acc);
                 } else {
 #pragma unroll
                     for (int j = (P == 1 ? 0 : i); j < (P == 1 ? 2 : i + 1); ++j) {
-                        const v4u xo = {x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
                         const uint32_t w0 = d.w[2 * j], w1 = d.w[2 * j + 1];
-                        acc = mfma64(xo, v4u{low_values(w0), high_values(w0), low_values(w1), high_values(w1)}, acc);
-                        if constexpr (ZEROS) sum = mfma64(xo, ones, sum);
+                        acc = mfma64(v4u{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]},
+                                     v4u{low_values<ZEROS>(w0, z), high_values<ZEROS>(w0, z), low_values<ZEROS>(w1, z),
+                                         high_values<ZEROS>(w1, z)}, acc);
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < RES; ++e)
-                    y[b][e] = __builtin_fmaf(float(ZEROS ? acc[e] - __mul24(z16, sum[e]) : acc[e]), sc, y[b][e]);
+                for (int e = 0; e < RES; ++e) y[b][e] = __builtin_fmaf(float(acc[e]), sc, y[b][e]);
             }
         }
     };
@@ -156,20 +170,18 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4a8_kernel(W4Launch a) {
     const int whole = a.K / kTileK;
     const int n = wv < whole ? (whole - wv + nw - 1) / nw : 0;
     T d[D];
+    auto load = [&](int i, T &t) __attribute__((always_inline)) {
+        load_w(wv + i * nw, t);
+        load_x(wv + i * nw, t);
+    };
 #pragma unroll
     for (int j = 0; j < D; ++j)
-        if (j < n) {
-            load_w(wv + j * nw, d[j]);
-            load_x(wv + j * nw, d[j]);
-        }
+        if (j < n) load(j, d[j]);
     for (int i = 0; i < n; i += D) {
 #pragma unroll
         for (int j = 0; j < D; ++j) {
             if (i + j < n) use(d[j]);
-            if (i + j + D < n) {
-                load_w(wv + (i + j + D) * nw, d[j]);
-                load_x(wv + (i + j + D) * nw, d[j]);
-            }
+            if (i + j + D < n) load(i + j + D, d[j]);
         }
     }
     if (whole < a.KT && wv == whole % nw) {
@@ -201,7 +213,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4a8_kernel(W4Launch a) {
             }
             const int m = ONE ? c : 16 * b + 4 * c + e;
             if (m >= a.M || row >= a.N) continue;
-            v *= a.sa[m];
+            v *= kBack<ZEROS> * a.sa[m];
             const int64_t at = int64_t(m) * a.N + row;
             if (a.y_f32) a.y_f32[at] = v;
             if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
@@ -217,18 +229,28 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4a8_kernel(W4Launch a) {
 // quarter of a wave reads 256 bytes in a row; chunks are 16 bytes apart from
 // that, so that the stores of a row's chunks fall in different banks.  Rows
 // start anywhere, so they are staged through registers, a tile ahead.
+#ifndef TS
+#define TS 1
+#define WGC 2
+#define TG 2
+#define TD 2
+#endif
 constexpr int kChunkBytes = 272;
 
-template <int P, int MB, bool ZEROS, int STRIPS>
-__global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(W4Launch a) {
+template <int P, int MB, bool ZEROS, int STRIPS, int GROUPS>
+__global__ __launch_bounds__(256 * GROUPS, 2) void w4a8_tile_kernel(W4Launch a) {
     constexpr int STAGE = MB * 8 * kChunkBytes, PER = (MB * 128 + 255) / 256;
-    constexpr int D = 3;                     // tiles of weights on their way
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2][STAGE];
-    const int tid = int(threadIdx.x), lane = tid & 63, r = lane & 15, c = lane >> 4;
+    constexpr int D = TD;                    // tiles of weights on their way
+    __shared__ __attribute__((aligned(16))) uint8_t stages[GROUPS][2][STAGE];
+    const int tid = int(threadIdx.x) & 255, lane = tid & 63, r = lane & 15, c = lane >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int group = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 8);
+    uint8_t(&lds)[2][STAGE] = stages[group];
     const int s0 = (int(blockIdx.x) * 4 + wv) * STRIPS, part = int(blockIdx.y);
-    // Tiles t0 .. t1 - 1 of k.
+    // The part's tiles of k from t0 on; this group's are t0 + group + i * GROUPS,
+    // i < n (steps: the most that a group has).
     const int t0 = int(int64_t(a.KT) * part / a.parts), t1 = int(int64_t(a.KT) * (part + 1) / a.parts);
+    const int steps = (t1 - t0 + GROUPS - 1) / GROUPS, n = (t1 - t0 - group + GROUPS - 1) / GROUPS;
 
     const uint8_t *wp[STRIPS], *zp[STRIPS];
     const uint16_t *sp[STRIPS];
@@ -270,8 +292,7 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(W4Launch a) {
         to[j] = ((row >> 4) * 8 + q) * kChunkBytes + 16 * (row & 15);
     }
     const int q16 = 16 * (tid & 7);
-    v4u xv[PER];
-    auto load_x = [&](int t) __attribute__((always_inline)) {
+    auto load_x = [&](int t, v4u (&xv)[PER]) __attribute__((always_inline)) {
         const int k = t * kTileK + q16;
         if ((t + 1) * kTileK <= a.K) {
 #pragma unroll
@@ -285,7 +306,7 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(W4Launch a) {
             }
         }
     };
-    auto store_x = [&](uint8_t *stage) __attribute__((always_inline)) {
+    auto store_x = [&](uint8_t *stage, const v4u (&xv)[PER]) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < PER; ++j)
             if (MB * 128 % 256 == 0 || tid + 256 * j < MB * 128) *reinterpret_cast<v4u *>(stage + to[j]) = xv[j];
@@ -300,29 +321,25 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(W4Launch a) {
             for (int e = 0; e < 4; ++e) y[k][b][e] = 0.0f;
 
     auto use = [&](const Weights (&d)[STRIPS], const uint8_t *stage) __attribute__((always_inline)) {
-        const v4i none = {0, 0, 0, 0};
-        const v4u ones = {0x01010101u, 0x01010101u, 0x01010101u, 0x01010101u};
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             float sc[STRIPS];
-            int z16[STRIPS];
+            uint32_t z[STRIPS];
 #pragma unroll
             for (int k = 0; k < STRIPS; ++k) {
-                const uint32_t sb = (d[k].s[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
-                sc[k] = (a.bf16_scales ? __uint_as_float(sb << 16) : float(__builtin_bit_cast(_Float16, uint16_t(sb)))) * 0.0625f;
-                z16[k] = ZEROS ? int(d[k].z << (24 - 8 * i)) >> 24 << 4 : 0;
+                sc[k] = scale_value((d[k].s[i >> 1] >> (16 * (i & 1))) & 0xFFFFu, a.bf16_scales);
+                z[k] = ZEROS ? zero_bytes(d[k].z, i) : 0u;
             }
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
-                v4i acc[STRIPS], sum = none;
+                v4i acc[STRIPS];
 #pragma unroll
-                for (int k = 0; k < STRIPS; ++k) acc[k] = none;
+                for (int k = 0; k < STRIPS; ++k) acc[k] = v4i{0, 0, 0, 0};
                 if constexpr (P == 4) {
                     const v2u x = *reinterpret_cast<const v2u *>(stage + (b * 8 + 2 * i + (c >> 1)) * kChunkBytes + 16 * r + 8 * (c & 1));
 #pragma unroll
                     for (int k = 0; k < STRIPS; ++k)
-                        acc[k] = mfma32(x, v2u{low_values(d[k].w[i]), high_values(d[k].w[i])}, acc[k]);
-                    if constexpr (ZEROS) sum = mfma32(x, v2u{ones[0], ones[1]}, sum);
+                        acc[k] = mfma32(x, v2u{low_values<ZEROS>(d[k].w[i], z[k]), high_values<ZEROS>(d[k].w[i], z[k])}, acc[k]);
                 } else {
 #pragma unroll
                     for (int j = (P == 1 ? 0 : i); j < (P == 1 ? 2 : i + 1); ++j) {
@@ -330,40 +347,81 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(W4Launch a) {
 #pragma unroll
                         for (int k = 0; k < STRIPS; ++k) {
                             const uint32_t w0 = d[k].w[2 * j], w1 = d[k].w[2 * j + 1];
-                            acc[k] = mfma64(x, v4u{low_values(w0), high_values(w0), low_values(w1), high_values(w1)}, acc[k]);
+                            acc[k] = mfma64(x, v4u{low_values<ZEROS>(w0, z[k]), high_values<ZEROS>(w0, z[k]),
+                                                   low_values<ZEROS>(w1, z[k]), high_values<ZEROS>(w1, z[k])}, acc[k]);
                         }
-                        if constexpr (ZEROS) sum = mfma64(x, ones, sum);
                     }
                 }
 #pragma unroll
                 for (int k = 0; k < STRIPS; ++k)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[k][b][e] = __builtin_fmaf(float(ZEROS ? acc[k][e] - __mul24(z16[k], sum[e]) : acc[k][e]), sc[k], y[k][b][e]);
+                    for (int e = 0; e < 4; ++e) y[k][b][e] = __builtin_fmaf(float(acc[k][e]), sc[k], y[k][b][e]);
             }
         }
     };
 
+    // Weights D tiles ahead; rows D + 1, the nearest of them in the other stage.
     Weights d[D][STRIPS];
-    load_x(t0);
+    v4u xv[D][PER];
+    const auto tile = [&](int i) { return t0 + group + i * GROUPS; };
+    if (n > 0) load_x(tile(0), xv[0]);
 #pragma unroll
     for (int j = 0; j < D; ++j)
-        if (t0 + j < t1) load_w(t0 + j, d[j]);
-    store_x(lds[0]);
-    if (t0 + 1 < t1) load_x(t0 + 1);
-    __syncthreads();
-    // (Two stages and D weight sets: the loop's body is 2 D tiles.)
-    for (int t = t0; t < t1; t += 2 * D) {
+        if (j < n) load_w(tile(j), d[j]);
+    if (n > 0) store_x(lds[0], xv[0]);
 #pragma unroll
-        for (int j = 0; j < 2 * D; ++j) {
-            if (t + j < t1) {
-                if (t + j + 1 < t1) store_x(lds[(j + 1) & 1]);
-                if (t + j + 2 < t1) load_x(t + j + 2);
-                use(d[j % D], lds[j & 1]);
-                if (t + j + D < t1) load_w(t + j + D, d[j % D]);
+    for (int j = 1; j <= D; ++j)
+        if (j < n) load_x(tile(j), xv[j % D]);
+    __syncthreads();
+    // While no load can be past the end none is asked for it: a load that may
+    // be skipped makes the compiler wait for all before it.
+    static_assert(D % 2 == 0, "stages and weight sets turn together");
+    int i = 0;
+    for (; i + 2 * D < (t1 - t0) / GROUPS; i += D) {
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+            store_x(lds[(j + 1) & 1], xv[(j + 1) % D]);
+            load_x(tile(i + j + 1 + D), xv[(j + 1) % D]);
+            use(d[j], lds[j & 1]);
+            load_w(tile(i + j + D), d[j]);
+            __syncthreads();
+        }
+    }
+    for (; i < steps; i += D) {
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+            if (i + j < steps) {
+                if (i + j + 1 < n) store_x(lds[(j + 1) & 1], xv[(j + 1) % D]);
+                if (i + j + 1 + D < n) load_x(tile(i + j + 1 + D), xv[(j + 1) % D]);
+                if (i + j < n) use(d[j], lds[j & 1]);
+                if (i + j + D < n) load_w(tile(i + j + D), d[j]);
                 __syncthreads();
             }
         }
+    }
+
+    // The groups' sums, added in their order by the first one.
+    if constexpr (GROUPS > 1) {
+        static_assert(STRIPS * MB * 4096 <= 2 * STAGE, "a group's sums fit its stages");
+        float *mine = reinterpret_cast<float *>(&lds[0][0]);
+#pragma unroll
+        for (int k = 0; k < STRIPS; ++k)
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (group > 0) mine[((k * MB + b) * 4 + e) * 256 + tid] = y[k][b][e];
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int g = 1; g < GROUPS; ++g)
+#pragma unroll
+            for (int k = 0; k < STRIPS; ++k)
+#pragma unroll
+                for (int b = 0; b < MB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[k][b][e] += reinterpret_cast<const float *>(&stages[g][0][0])[((k * MB + b) * 4 + e) * 256 + tid];
     }
 
     // Lane (r, c) of strip k and block b: weight row r, activation rows 16b + 4c + e.
@@ -382,7 +440,7 @@ __global__ __launch_bounds__(256, 2) void w4a8_tile_kernel(W4Launch a) {
                     a.ws[part * (int64_t(a.M) * a.N) + at] = y[k][b][e];
                     continue;
                 }
-                const float v = y[k][b][e] * a.sa[m];
+                const float v = y[k][b][e] * (kBack<ZEROS> * a.sa[m]);
                 if (a.y_f32) a.y_f32[at] = v;
                 if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
             }
@@ -397,25 +455,21 @@ __global__ __launch_bounds__(256) void w4a8_join_kernel(W4Launch a) {
     float v = 0.0f;
 #pragma unroll 8
     for (int p = 0; p < a.parts; ++p) v += a.ws[p * all + at];
-    v *= a.sa[m];
+    v *= (a.zeros ? kBack<true> : kBack<false>) * a.sa[m];
     if (a.y_f32) a.y_f32[at] = v;
     if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
 }
 
-#ifndef TS
-#define TS 1
-#define WGC 2
-#endif
 template <int P, bool ZEROS>
 hipError_t w4_tiles_launch(const W4Launch &la, int cus, hipStream_t stream) {
     W4Launch a = la;
     const int blocks = int(ceil_div(a.strips, 4 * TS));
-    a.parts = std::max(1, std::min({WGC * cus / blocks, a.KT / 8, kW4Parts}));
-    const void *fn = a.M <= 32   ? reinterpret_cast<const void *>(&w4a8_tile_kernel<P, 2, ZEROS, TS>)
-                     : a.M <= 48 ? reinterpret_cast<const void *>(&w4a8_tile_kernel<P, 3, ZEROS, TS>)
-                                 : reinterpret_cast<const void *>(&w4a8_tile_kernel<P, 4, ZEROS, TS>);
+    a.parts = 2 * blocks > cus ? 1 : std::max(1, std::min({WGC * cus / blocks, a.KT / 8, kW4Parts}));
+    const void *fn = a.M <= 32   ? reinterpret_cast<const void *>(&w4a8_tile_kernel<P, 2, ZEROS, TS, TG>)
+                     : a.M <= 48 ? reinterpret_cast<const void *>(&w4a8_tile_kernel<P, 3, ZEROS, TS, TG>)
+                                 : reinterpret_cast<const void *>(&w4a8_tile_kernel<P, 4, ZEROS, TS, TG>);
     void *args[] = {&a};
-    const hipError_t e = hipLaunchKernel(fn, dim3(unsigned(blocks), unsigned(a.parts)), dim3(256), args, 0, stream);
+    const hipError_t e = hipLaunchKernel(fn, dim3(unsigned(blocks), unsigned(a.parts)), dim3(256 * TG), args, 0, stream);
     if (e != hipSuccess || a.parts == 1) return e;
     return hipLaunchKernel(reinterpret_cast<const void *>(&w4a8_join_kernel),
                            dim3(unsigned(ceil_div(a.N, 256)), unsigned(a.M)), dim3(256), args, 0, stream);
