@@ -16,21 +16,27 @@ typedef v4u v4u_b __attribute__((aligned(1)));
 typedef v2u v2u_b __attribute__((aligned(1)));
 typedef v4f v4f_b __attribute__((aligned(4)));
 
-// BYTES (8 or 16) consecutive int8 of a row from k on; those past K are 0.
-template <int BYTES>
-__device__ __forceinline__ void load_int8_tail(const int8_t *row, int k, int K, uint32_t *w) {
-    uint64_t v[2] = {0, 0};
+// 16 consecutive int8 of a row of K from k on; those past K are 0.  One load of
+// the 16 that end with the row at the latest, shifted; rows below 16 by bytes.
+__device__ __forceinline__ v4u load_int8_tail(const int8_t *row, int k, int K) {
+    uint64_t lo = 0, hi = 0;
+    if (K >= 16) {
+        const int at = min(k, K - 16), s = 8 * min(k - at, 16);
+        const v4u v = *reinterpret_cast<const v4u_b *>(row + at);
+        const uint64_t a = (uint64_t(v[1]) << 32) | v[0], b = (uint64_t(v[3]) << 32) | v[2];
+        lo = s >= 128 ? 0 : s >= 64 ? b >> (s - 64) : s > 0 ? (a >> s) | (b << (64 - s)) : a;
+        hi = s >= 64 ? 0 : b >> s;
+    } else {
 #pragma unroll 1
-    for (int b = 0; b < BYTES; ++b)
-        if (k + b < K) {
-            const uint64_t byte = uint64_t(uint8_t(row[k + b])) << (8 * (b & 7));
-            if (b < 8)
-                v[0] |= byte;
+        for (int i = 0; k + i < K; ++i) {
+            const uint64_t byte = uint64_t(uint8_t(row[k + i])) << (8 * (i & 7));
+            if (i < 8)
+                lo |= byte;
             else
-                v[1] |= byte;
+                hi |= byte;
         }
-#pragma unroll
-    for (int i = 0; i < BYTES / 4; ++i) w[i] = uint32_t(v[i >> 1] >> (32 * (i & 1)));
+    }
+    return v4u{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
 }
 
 struct NormLaunch {
@@ -62,7 +68,7 @@ struct W4Launch {
     int parts;
 };
 // Most parts that k is split into (and the rows from which it may be).
-constexpr int kW4Parts = 8, kW4PartRows = 17;
+constexpr int kW4Parts = 8, kW4PartRows = 2;
 hipError_t launch_w4a8(const W4Launch &a, int cus, hipStream_t stream);
 
 // Mixture of experts: offsets into the workspace, all multiples of 256.

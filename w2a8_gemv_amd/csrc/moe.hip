@@ -249,9 +249,7 @@ __global__ __launch_bounds__(512) void moe_up_one_kernel(MoeLaunch a) {
             if (k + 16 <= a.H) {
                 xv[d] = *reinterpret_cast<const v4u_b *>(x + k);
             } else if (k < a.H) {
-                uint32_t w[4];
-                load_int8_tail<16>(x, k, a.H, w);
-                xv[d] = v4u{w[0], w[1], w[2], w[3]};
+                xv[d] = load_int8_tail(x, k, a.H);
             }
         };
         Dots dg, du;
@@ -481,14 +479,7 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeLaunch a, i
         }
         int sum = 0;
         for (int k = 16 * tid; k < Hp; k += 16 * kRouteThreads) {
-            v4u v;
-            if (k + 16 <= a.H) {
-                v = *reinterpret_cast<const v4u_b *>(row + k);
-            } else {
-                uint32_t w[4];
-                load_int8_tail<16>(row, k, a.H, w);
-                v = v4u{w[0], w[1], w[2], w[3]};
-            }
+            const v4u v = k + 16 <= a.H ? v4u(*reinterpret_cast<const v4u_b *>(row + k)) : load_int8_tail(row, k, a.H);
             *reinterpret_cast<v4u *>(out + k) = v;
             sum = add16(v, sum);
         }

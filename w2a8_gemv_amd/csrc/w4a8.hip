@@ -17,8 +17,6 @@
 // as int32 and as fp32.  What is left of the work, and the most of it, is one
 // conversion and one multiply-add for every result and group.
 //
-// A workgroup takes one strip of 16 weight rows; its waves take the strip's
-// tiles (16 x 128, 1 KiB) in turn and add their sums in LDS in wave order.
 #include "block.h"
 #include "mx4_device.h"
 
@@ -60,227 +58,154 @@ __device__ __forceinline__ v4i mfma32(v2u x, v2u w, v4i acc) {
                                                  acc, 0, 0, 0);
 }
 
-// What a tile needs: codes, activations of MB blocks of 16 rows, scales and
-// zero points of its P groups.
-template <int P, int MB, bool ZEROS>
-struct Tile {
+// A lane's part of a tile of weights: codes, and the scales and zero points of
+// its row in the tile's P groups, which share a quad of groups.
+template <int P>
+struct Weights {
     v4u w;
-    uint32_t x[MB][8];
-    uint32_t s[(P + 1) / 2];
-    uint32_t z;
+    uint32_t s[(P + 1) / 2], z;
+
+    template <bool ZEROS>
+    __device__ __forceinline__ void load(const uint8_t *wp, const uint16_t *sp, const uint8_t *zp, int t) {
+        w = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(wp + int64_t(t) * kW4TileBytes));
+        const int g = P * t, at = (g >> 2) * 64 + (g & 3);
+        if constexpr (P == 1)
+            s[0] = sp[at];
+        else
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) s[i] = reinterpret_cast<const uint32_t *>(sp + at)[i];
+        if constexpr (ZEROS)
+            z = P == 1   ? zp[at]
+                : P == 2 ? *reinterpret_cast<const uint16_t *>(zp + at)
+                         : *reinterpret_cast<const uint32_t *>(zp + at);
+    }
+    // The 16 values of piece j (of two).
+    template <bool ZEROS>
+    __device__ __forceinline__ v4u operand(int j, uint32_t zero) const {
+        return v4u{low_values<ZEROS>(w[2 * j], zero), high_values<ZEROS>(w[2 * j], zero),
+                   low_values<ZEROS>(w[2 * j + 1], zero), high_values<ZEROS>(w[2 * j + 1], zero)};
+    }
+    __device__ __forceinline__ float scale(int i, int bf16) const {
+        return scale_value((s[i >> 1] >> (16 * (i & 1))) & 0xFFFFu, bf16);
+    }
 };
 
-template <int P, int MB, bool ZEROS, bool ONE>
-__global__ __launch_bounds__(64 * kMaxWaves) void w4a8_kernel(W4Launch a) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    using T = Tile<P, MB, ZEROS>;
-    constexpr int D = MB == 4 ? 2 : 4;       // tiles of a wave on their way
-    constexpr int RES = ONE ? 1 : 4;         // results of a lane and block (ONE: all rows are the same)
-    const int lane = int(threadIdx.x) & 63;
-    const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-    const int nw = int(blockDim.x) >> 6;
+// One row.  A workgroup takes one strip; its waves take the strip's tiles in
+// turn, D of them on their way, and add their sums in LDS in wave order.  The
+// row is staged once (kRowChunk values at a time, zeros past its end), so the
+// loop loads weights alone and knows no ragged tile.  Every row of the first
+// operand is that row, so all results of a lane are the same: one is scaled.
+constexpr int kRowChunk = 32768;
+
+template <int P, bool ZEROS>
+__global__ __launch_bounds__(64 * kMaxWaves) void w4a8_row_kernel(W4Launch a) {
+    constexpr int D = 4;
+    extern __shared__ __attribute__((aligned(16))) uint8_t row[];
+    __shared__ float red[kMaxWaves][16];
+    const int tid = int(threadIdx.x), lane = tid & 63, r = lane & 15, c = lane >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), nw = int(blockDim.x) >> 6;
     const int s = int(blockIdx.x + blockIdx.y * gridDim.x);
     if (s >= a.strips) return;
-    const int r = lane & 15, c = lane >> 4;
-
     const uint8_t *wp = a.w + int64_t(s) * a.KT * kW4TileBytes + 16 * lane;
     const uint16_t *sp = a.scales + (int64_t(s) * a.GQ * 16 + r) * 4;
     const uint8_t *zp = ZEROS ? a.zeros + (int64_t(s) * a.GQ * 16 + r) * 4 : nullptr;
-    const int8_t *xp[MB];
+    Weights<P> d[D];
+    float y = 0.0f;
+    for (int t0 = 0; t0 < a.KT; t0 += kRowChunk / kTileK) {
+        // This wave's tiles of the chunk: t0 + wv + i * nw, i < n.
+        const int tiles = min(kRowChunk / kTileK, a.KT - t0);
+        const int n = wv < tiles ? (tiles - wv + nw - 1) / nw : 0;
+        const auto load = [&](int i, Weights<P> &t) __attribute__((always_inline)) {
+            t.template load<ZEROS>(wp, sp, zp, t0 + wv + i * nw);
+        };
 #pragma unroll
-    for (int b = 0; b < MB; ++b) xp[b] = a.x + int64_t(min(16 * b + r, a.M - 1)) * a.K;
-
-    // Tile t: groups P t .. P t + P - 1, which share a quad of groups.
-    auto load_w = [&](int t, T &d) __attribute__((always_inline)) {
-        d.w = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(wp + int64_t(t) * kW4TileBytes));
-        const int g = P * t, at = (g >> 2) * 64 + (g & 3);
-        if constexpr (P == 1)
-            d.s[0] = sp[at];
-        else
-#pragma unroll
-            for (int i = 0; i < P / 2; ++i) d.s[i] = reinterpret_cast<const uint32_t *>(sp + at)[i];
-        if constexpr (ZEROS)
-            d.z = P == 1   ? zp[at]
-                  : P == 2 ? *reinterpret_cast<const uint16_t *>(zp + at)
-                           : *reinterpret_cast<const uint32_t *>(zp + at);
-    };
-    auto load_x = [&](int t, T &d) __attribute__((always_inline)) {
-#pragma unroll
-        for (int b = 0; b < MB; ++b)
-#pragma unroll
-            for (int i = 0; i < (P == 4 ? 4 : 2); ++i) {
-                const int8_t *p = xp[b] + t * kTileK + (P == 1 ? 32 * c + 16 * i : P == 2 ? 64 * i + 16 * c : 32 * i + 8 * c);
-                if constexpr (P == 4) {
-                    const v2u v = *reinterpret_cast<const v2u_b *>(p);
-                    d.x[b][2 * i] = v[0];
-                    d.x[b][2 * i + 1] = v[1];
-                } else {
-                    const v4u v = *reinterpret_cast<const v4u_b *>(p);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) d.x[b][4 * i + j] = v[j];
-                }
-            }
-    };
-    auto load_x_tail = [&](int t, T &d) __attribute__((always_inline)) {
-#pragma unroll
-        for (int b = 0; b < MB; ++b)
-#pragma unroll
-            for (int i = 0; i < (P == 4 ? 4 : 2); ++i) {
-                const int k = t * kTileK + (P == 1 ? 32 * c + 16 * i : P == 2 ? 64 * i + 16 * c : 32 * i + 8 * c);
-                if constexpr (P == 4)
-                    load_int8_tail<8>(xp[b], k, a.K, d.x[b] + 2 * i);
-                else
-                    load_int8_tail<16>(xp[b], k, a.K, d.x[b] + 4 * i);
-            }
-    };
-
-    float y[MB][RES];
-#pragma unroll
-    for (int b = 0; b < MB; ++b)
-#pragma unroll
-        for (int e = 0; e < RES; ++e) y[b][e] = 0.0f;
-
-    auto use = [&](const T &d) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const float sc = scale_value((d.s[i >> 1] >> (16 * (i & 1))) & 0xFFFFu, a.bf16_scales);
-            const uint32_t z = ZEROS ? zero_bytes(d.z, i) : 0u;
-#pragma unroll
-            for (int b = 0; b < MB; ++b) {
-                v4i acc = {0, 0, 0, 0};
-                const uint32_t *x = d.x[b];
-                if constexpr (P == 4) {
-                    acc = mfma32(v2u{x[2 * i], x[2 * i + 1]}, v2u{low_values<ZEROS>(d.w[i], z), high_values<ZEROS>(d.w[i], z)}, acc);
-                } else {
-#pragma unroll
-                    for (int j = (P == 1 ? 0 : i); j < (P == 1 ? 2 : i + 1); ++j) {
-                        const uint32_t w0 = d.w[2 * j], w1 = d.w[2 * j + 1];
-                        acc = mfma64(v4u{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]},
-                                     v4u{low_values<ZEROS>(w0, z), high_values<ZEROS>(w0, z), low_values<ZEROS>(w1, z),
-                                         high_values<ZEROS>(w1, z)}, acc);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < RES; ++e) y[b][e] = __builtin_fmaf(float(acc[e]), sc, y[b][e]);
-            }
-        }
-    };
-
-    // This wave's whole tiles: wv, wv + nw, ...; the ragged one behind them.
-    const int whole = a.K / kTileK;
-    const int n = wv < whole ? (whole - wv + nw - 1) / nw : 0;
-    T d[D];
-    auto load = [&](int i, T &t) __attribute__((always_inline)) {
-        load_w(wv + i * nw, t);
-        load_x(wv + i * nw, t);
-    };
-#pragma unroll
-    for (int j = 0; j < D; ++j)
-        if (j < n) load(j, d[j]);
-    for (int i = 0; i < n; i += D) {
-#pragma unroll
-        for (int j = 0; j < D; ++j) {
-            if (i + j < n) use(d[j]);
-            if (i + j + D < n) load(i + j + D, d[j]);
-        }
-    }
-    if (whole < a.KT && wv == whole % nw) {
-        load_w(whole, d[0]);
-        load_x_tail(whole, d[0]);
-        use(d[0]);
-    }
-
-    // Lane (r, c) of block b: weight row r, activation rows 16b + 4c + e.
-    float *red = reinterpret_cast<float *>(lds);
-    constexpr int PER = MB * RES;
-    if (nw > 1) {
-#pragma unroll
-        for (int b = 0; b < MB; ++b)
-#pragma unroll
-            for (int e = 0; e < RES; ++e) red[(wv * PER + b * RES + e) * 64 + lane] = y[b][e];
+        for (int j = 0; j < D; ++j)
+            if (j < n) load(j, d[j]);
+        if (t0 > 0) __syncthreads();        // the chunk before has been read
+        for (int k = 16 * tid; k < tiles * kTileK; k += 16 * int(blockDim.x))
+            *reinterpret_cast<v4u *>(row + k) = load_int8_tail(a.x, t0 * kTileK + k, a.K);
         __syncthreads();
-    }
-    const int row = s * kW4Rows + r;
+        const auto use = [&](int i, const Weights<P> &t) __attribute__((always_inline)) {
+            const uint8_t *x = row + (wv + i * nw) * kTileK;
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-        if (b % nw != wv) continue;
+            for (int g = 0; g < P; ++g) {
+                const uint32_t z = ZEROS ? zero_bytes(t.z, g) : 0u;
+                v4i acc = {0, 0, 0, 0};
+                if constexpr (P == 4) {
+                    acc = mfma32(*reinterpret_cast<const v2u *>(x + 32 * g + 8 * c),
+                                 v2u{low_values<ZEROS>(t.w[g], z), high_values<ZEROS>(t.w[g], z)}, acc);
+                } else {
 #pragma unroll
-        for (int e = 0; e < RES; ++e) {
-            float v = y[b][e];
-            if (nw > 1) {
-                v = red[(b * RES + e) * 64 + lane];
-                for (int w = 1; w < nw; ++w) v += red[(w * PER + b * RES + e) * 64 + lane];
+                    for (int j = (P == 1 ? 0 : g); j < (P == 1 ? 2 : g + 1); ++j)
+                        acc = mfma64(*reinterpret_cast<const v4u *>(x + (P == 1 ? 32 * c + 16 * j : 64 * j + 16 * c)),
+                                     t.template operand<ZEROS>(j, z), acc);
+                }
+                y = __builtin_fmaf(float(acc[0]), t.scale(g, a.bf16_scales), y);
             }
-            const int m = ONE ? c : 16 * b + 4 * c + e;
-            if (m >= a.M || row >= a.N) continue;
-            v *= kBack<ZEROS> * a.sa[m];
-            const int64_t at = int64_t(m) * a.N + row;
-            if (a.y_f32) a.y_f32[at] = v;
-            if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
+        };
+        // While no load can be past the end none is asked for it: a load that may
+        // be skipped makes the compiler wait for all before it.
+        int i = 0;
+        for (; i + 2 * D <= n; i += D) {
+#pragma unroll
+            for (int j = 0; j < D; ++j) {
+                use(i + j, d[j]);
+                load(i + j + D, d[j]);
+            }
+        }
+        for (; i < n; i += D) {
+#pragma unroll
+            for (int j = 0; j < D; ++j) {
+                if (i + j < n) use(i + j, d[j]);
+                if (i + j + D < n) load(i + j + D, d[j]);
+            }
         }
     }
+    if (c == 0) red[wv][r] = y;
+    __syncthreads();
+    const int n = s * kW4Rows + tid;
+    if (tid >= 16 || n >= a.N) return;
+    float v = 0.0f;
+    for (int w = 0; w < nw; ++w) v += red[w][tid];
+    v *= kBack<ZEROS> * a.sa[0];
+    if (a.y_f32) a.y_f32[n] = v;
+    if (a.y_bf16) a.y_bf16[n] = uint16_t(bf16_bits(v));
 }
 
-// More rows (17 to 64): activations through LDS.  A workgroup of four waves
-// takes 4 * STRIPS strips, each wave STRIPS of them, and walks a range of the
-// tiles of k together; the rows' part of a tile (MB blocks of 16 rows x 128 k)
-// is staged once for all of them.  LDS holds it as [block][chunk of 16 k][row],
-// where every operand is 16 (or, for groups of 32, 8) bytes of a lane and a
-// quarter of a wave reads 256 bytes in a row; chunks are 16 bytes apart from
-// that, so that the stores of a row's chunks fall in different banks.  Rows
-// start anywhere, so they are staged through registers, a tile ahead.
-#ifndef TS
-#define TS 1
-#define WGC 2
-#define TG 2
-#define TD 2
-#endif
+// More rows (2 to 64): activations through LDS.  A workgroup takes four strips
+// and a range of the tiles of k, in GROUPS groups of four waves that take its
+// tiles in turn, a strip a wave; a group stages the rows' part of a tile (MB
+// blocks of 16 rows x 128 k) once for its four waves.  LDS holds it as
+// [block][chunk of 16 k][row], where every operand is 16 (or, for groups of 32,
+// 8) bytes of a lane and a quarter of a wave reads 256 bytes in a row; chunks
+// are 16 bytes apart from that, so that the stores of a row's chunks fall in
+// different banks.  Rows start anywhere, so they are staged through registers.
+//
+// Bound by the multiply-adds of the results (64 x 5120 x 27648, groups of 64:
+// some 120 vector instructions a tile, 8 of them on the matrix pipe; 27 us, of
+// which the instructions are 14 and the weights 15, side by side).  Each strip
+// reading its rows from the L2 by itself took 106 us for that product.
 constexpr int kChunkBytes = 272;
 
-template <int P, int MB, bool ZEROS, int STRIPS, int GROUPS>
+template <int P, int MB, bool ZEROS, int GROUPS>
 __global__ __launch_bounds__(256 * GROUPS, 2) void w4a8_tile_kernel(W4Launch a) {
     constexpr int STAGE = MB * 8 * kChunkBytes, PER = (MB * 128 + 255) / 256;
-    constexpr int D = TD;                    // tiles of weights on their way
+    constexpr int D = 2;                     // tiles of a wave on their way
     __shared__ __attribute__((aligned(16))) uint8_t stages[GROUPS][2][STAGE];
     const int tid = int(threadIdx.x) & 255, lane = tid & 63, r = lane & 15, c = lane >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int group = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 8);
     uint8_t(&lds)[2][STAGE] = stages[group];
-    const int s0 = (int(blockIdx.x) * 4 + wv) * STRIPS, part = int(blockIdx.y);
+    const int strip = int(blockIdx.x + blockIdx.z * gridDim.x) * 4 + wv, part = int(blockIdx.y);
     // The part's tiles of k from t0 on; this group's are t0 + group + i * GROUPS,
     // i < n (steps: the most that a group has).
     const int t0 = int(int64_t(a.KT) * part / a.parts), t1 = int(int64_t(a.KT) * (part + 1) / a.parts);
     const int steps = (t1 - t0 + GROUPS - 1) / GROUPS, n = (t1 - t0 - group + GROUPS - 1) / GROUPS;
 
-    const uint8_t *wp[STRIPS], *zp[STRIPS];
-    const uint16_t *sp[STRIPS];
-#pragma unroll
-    for (int k = 0; k < STRIPS; ++k) {
-        const int64_t s = min(s0 + k, a.strips - 1);       // (past the last: not stored)
-        wp[k] = a.w + s * a.KT * kW4TileBytes + 16 * lane;
-        sp[k] = a.scales + (s * a.GQ * 16 + r) * 4;
-        zp[k] = ZEROS ? a.zeros + (s * a.GQ * 16 + r) * 4 : nullptr;
-    }
-    struct Weights {
-        v4u w;
-        uint32_t s[(P + 1) / 2], z;
-    };
-    auto load_w = [&](int t, Weights (&d)[STRIPS]) __attribute__((always_inline)) {
-        const int g = P * t, at = (g >> 2) * 64 + (g & 3);
-#pragma unroll
-        for (int k = 0; k < STRIPS; ++k) {
-            d[k].w = __builtin_nontemporal_load(reinterpret_cast<const v4u *>(wp[k] + int64_t(t) * kW4TileBytes));
-            if constexpr (P == 1)
-                d[k].s[0] = sp[k][at];
-            else
-#pragma unroll
-                for (int i = 0; i < P / 2; ++i) d[k].s[i] = reinterpret_cast<const uint32_t *>(sp[k] + at)[i];
-            if constexpr (ZEROS)
-                d[k].z = P == 1   ? zp[k][at]
-                         : P == 2 ? *reinterpret_cast<const uint16_t *>(zp[k] + at)
-                                  : *reinterpret_cast<const uint32_t *>(zp[k] + at);
-        }
-    };
+    const int64_t s = min(strip, a.strips - 1);       // (past the last: not stored)
+    const uint8_t *wp = a.w + s * a.KT * kW4TileBytes + 16 * lane;
+    const uint16_t *sp = a.scales + (s * a.GQ * 16 + r) * 4;
+    const uint8_t *zp = ZEROS ? a.zeros + (s * a.GQ * 16 + r) * 4 : nullptr;
     // This thread's chunks of the rows: row id / 8, chunk id % 8 (rows past M
     // repeat the last one).
     const int8_t *xp[PER];
@@ -299,11 +224,7 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void w4a8_tile_kernel(W4Launch a) 
             for (int j = 0; j < PER; ++j) xv[j] = *reinterpret_cast<const v4u_b *>(xp[j] + k);
         } else {
 #pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                uint32_t w[4];
-                load_int8_tail<16>(xp[j], k, a.K, w);
-                xv[j] = v4u{w[0], w[1], w[2], w[3]};
-            }
+            for (int j = 0; j < PER; ++j) xv[j] = load_int8_tail(xp[j], k, a.K);
         }
     };
     auto store_x = [&](uint8_t *stage, const v4u (&xv)[PER]) __attribute__((always_inline)) {
@@ -312,58 +233,40 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void w4a8_tile_kernel(W4Launch a) 
             if (MB * 128 % 256 == 0 || tid + 256 * j < MB * 128) *reinterpret_cast<v4u *>(stage + to[j]) = xv[j];
     };
 
-    float y[STRIPS][MB][4];
+    float y[MB][4];
 #pragma unroll
-    for (int k = 0; k < STRIPS; ++k)
+    for (int b = 0; b < MB; ++b)
 #pragma unroll
-        for (int b = 0; b < MB; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[k][b][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) y[b][e] = 0.0f;
 
-    auto use = [&](const Weights (&d)[STRIPS], const uint8_t *stage) __attribute__((always_inline)) {
+    auto use = [&](const Weights<P> &d, const uint8_t *stage) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            float sc[STRIPS];
-            uint32_t z[STRIPS];
-#pragma unroll
-            for (int k = 0; k < STRIPS; ++k) {
-                sc[k] = scale_value((d[k].s[i >> 1] >> (16 * (i & 1))) & 0xFFFFu, a.bf16_scales);
-                z[k] = ZEROS ? zero_bytes(d[k].z, i) : 0u;
-            }
+            const float sc = d.scale(i, a.bf16_scales);
+            const uint32_t z = ZEROS ? zero_bytes(d.z, i) : 0u;
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
-                v4i acc[STRIPS];
-#pragma unroll
-                for (int k = 0; k < STRIPS; ++k) acc[k] = v4i{0, 0, 0, 0};
+                v4i acc = {0, 0, 0, 0};
                 if constexpr (P == 4) {
-                    const v2u x = *reinterpret_cast<const v2u *>(stage + (b * 8 + 2 * i + (c >> 1)) * kChunkBytes + 16 * r + 8 * (c & 1));
-#pragma unroll
-                    for (int k = 0; k < STRIPS; ++k)
-                        acc[k] = mfma32(x, v2u{low_values<ZEROS>(d[k].w[i], z[k]), high_values<ZEROS>(d[k].w[i], z[k])}, acc[k]);
+                    acc = mfma32(*reinterpret_cast<const v2u *>(stage + (b * 8 + 2 * i + (c >> 1)) * kChunkBytes + 16 * r + 8 * (c & 1)),
+                                 v2u{low_values<ZEROS>(d.w[i], z), high_values<ZEROS>(d.w[i], z)}, acc);
                 } else {
 #pragma unroll
-                    for (int j = (P == 1 ? 0 : i); j < (P == 1 ? 2 : i + 1); ++j) {
-                        const v4u x = *reinterpret_cast<const v4u *>(stage + (b * 8 + (P == 1 ? 2 * c + j : 4 * j + c)) * kChunkBytes + 16 * r);
-#pragma unroll
-                        for (int k = 0; k < STRIPS; ++k) {
-                            const uint32_t w0 = d[k].w[2 * j], w1 = d[k].w[2 * j + 1];
-                            acc[k] = mfma64(x, v4u{low_values<ZEROS>(w0, z[k]), high_values<ZEROS>(w0, z[k]),
-                                                   low_values<ZEROS>(w1, z[k]), high_values<ZEROS>(w1, z[k])}, acc[k]);
-                        }
-                    }
+                    for (int j = (P == 1 ? 0 : i); j < (P == 1 ? 2 : i + 1); ++j)
+                        acc = mfma64(*reinterpret_cast<const v4u *>(stage + (b * 8 + (P == 1 ? 2 * c + j : 4 * j + c)) * kChunkBytes + 16 * r),
+                                     d.template operand<ZEROS>(j, z), acc);
                 }
 #pragma unroll
-                for (int k = 0; k < STRIPS; ++k)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[k][b][e] = __builtin_fmaf(float(acc[k][e]), sc[k], y[k][b][e]);
+                for (int e = 0; e < 4; ++e) y[b][e] = __builtin_fmaf(float(acc[e]), sc, y[b][e]);
             }
         }
     };
 
     // Weights D tiles ahead; rows D + 1, the nearest of them in the other stage.
-    Weights d[D][STRIPS];
+    Weights<P> d[D];
     v4u xv[D][PER];
     const auto tile = [&](int i) { return t0 + group + i * GROUPS; };
+    const auto load_w = [&](int t, Weights<P> &w) __attribute__((always_inline)) { w.template load<ZEROS>(wp, sp, zp, t); };
     if (n > 0) load_x(tile(0), xv[0]);
 #pragma unroll
     for (int j = 0; j < D; ++j)
@@ -401,50 +304,42 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void w4a8_tile_kernel(W4Launch a) 
     }
 
     // The groups' sums, added in their order by the first one.
-    if constexpr (GROUPS > 1) {
-        static_assert(STRIPS * MB * 4096 <= 2 * STAGE, "a group's sums fit its stages");
-        float *mine = reinterpret_cast<float *>(&lds[0][0]);
-#pragma unroll
-        for (int k = 0; k < STRIPS; ++k)
-#pragma unroll
-            for (int b = 0; b < MB; ++b)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (group > 0) mine[((k * MB + b) * 4 + e) * 256 + tid] = y[k][b][e];
-        __syncthreads();
-        if (group > 0) return;
-#pragma unroll
-        for (int g = 1; g < GROUPS; ++g)
-#pragma unroll
-            for (int k = 0; k < STRIPS; ++k)
-#pragma unroll
-                for (int b = 0; b < MB; ++b)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[k][b][e] += reinterpret_cast<const float *>(&stages[g][0][0])[((k * MB + b) * 4 + e) * 256 + tid];
-    }
-
-    // Lane (r, c) of strip k and block b: weight row r, activation rows 16b + 4c + e.
-#pragma unroll
-    for (int k = 0; k < STRIPS; ++k) {
-        const int row = (s0 + k) * kW4Rows + r;
-        if (row >= a.N) continue;
+    static_assert(MB * 4096 <= 2 * STAGE, "a group's sums fit its stages");
+    float *mine = reinterpret_cast<float *>(&lds[0][0]);
+    if (group > 0) {
 #pragma unroll
         for (int b = 0; b < MB; ++b)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int m = 16 * b + 4 * c + e;
-                if (m >= a.M) continue;
-                const int64_t at = int64_t(m) * a.N + row;
-                if (a.parts > 1) {
-                    a.ws[part * (int64_t(a.M) * a.N) + at] = y[k][b][e];
-                    continue;
-                }
-                const float v = y[k][b][e] * (kBack<ZEROS> * a.sa[m]);
-                if (a.y_f32) a.y_f32[at] = v;
-                if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
-            }
+            for (int e = 0; e < 4; ++e) mine[(b * 4 + e) * 256 + tid] = y[b][e];
     }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g)
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[b][e] += reinterpret_cast<const float *>(&stages[g][0][0])[(b * 4 + e) * 256 + tid];
+
+    // Lane (r, c) of block b: weight row r, activation rows 16b + 4c + e.
+    const int row = strip * kW4Rows + r;
+    if (row >= a.N) return;
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int m = 16 * b + 4 * c + e;
+            if (m >= a.M) continue;
+            const int64_t at = int64_t(m) * a.N + row;
+            if (a.parts > 1) {
+                a.ws[part * (int64_t(a.M) * a.N) + at] = y[b][e];
+                continue;
+            }
+            const float v = y[b][e] * (kBack<ZEROS> * a.sa[m]);
+            if (a.y_f32) a.y_f32[at] = v;
+            if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
+        }
 }
 
 // The parts of k, added in order.
@@ -461,32 +356,56 @@ __global__ __launch_bounds__(256) void w4a8_join_kernel(W4Launch a) {
 }
 
 template <int P, bool ZEROS>
+const void *tile_kernel(int M, int groups) {
+    const auto fn = [](auto *k) { return reinterpret_cast<const void *>(k); };
+    return M <= 16   ? (groups == 4 ? fn(&w4a8_tile_kernel<P, 1, ZEROS, 4>) : fn(&w4a8_tile_kernel<P, 1, ZEROS, 2>))
+           : M <= 32 ? (groups == 4 ? fn(&w4a8_tile_kernel<P, 2, ZEROS, 4>) : fn(&w4a8_tile_kernel<P, 2, ZEROS, 2>))
+           : M <= 48 ? fn(&w4a8_tile_kernel<P, 3, ZEROS, 2>)
+                     : fn(&w4a8_tile_kernel<P, 4, ZEROS, 2>);
+}
+
+// Workgroups of four strips.  Where these are half the compute units or fewer,
+// k is split into parts, about two workgroups to a compute unit, with four
+// tiles for every wave; the sums of parts go through memory (4.5 us for their
+// joining, so not for grids that fill most of the device: 19 x 13824 x 2570
+// 13.5 us whole, 16.5 + 4 in two parts).  Four groups of waves share a
+// workgroup's k where it has a compute unit to itself: 16 x 13824 x 2560 7.8 us
+// against 9.8, 32 x 5120 x 5120 10.9 against 13.3; two otherwise: 16 x 55296 x
+// 5120 32.5 against 34.3, 32 x 5120 x 27648 24.0 against 26.8, and beyond 32
+// rows, whose stages are larger: 64 x 5120 x 27648 30.2 against 34.3.
+template <int P, bool ZEROS>
 hipError_t w4_tiles_launch(const W4Launch &la, int cus, hipStream_t stream) {
     W4Launch a = la;
-    const int blocks = int(ceil_div(a.strips, 4 * TS));
-    a.parts = 2 * blocks > cus ? 1 : std::max(1, std::min({WGC * cus / blocks, a.KT / 8, kW4Parts}));
-    const void *fn = a.M <= 32   ? reinterpret_cast<const void *>(&w4a8_tile_kernel<P, 2, ZEROS, TS, TG>)
-                     : a.M <= 48 ? reinterpret_cast<const void *>(&w4a8_tile_kernel<P, 3, ZEROS, TS, TG>)
-                                 : reinterpret_cast<const void *>(&w4a8_tile_kernel<P, 4, ZEROS, TS, TG>);
+    const int blocks = int(ceil_div(a.strips, 4));
+    const auto parts = [&](int groups) {
+        return 2 * blocks > cus ? 1 : std::max(1, std::min({2 * cus / blocks, a.KT / (4 * groups), kW4Parts}));
+    };
+    const bool four = a.M <= 16 ? blocks <= cus : a.M <= 32 && blocks * parts(4) <= cus;
+    const int groups = four ? 4 : 2;
+    a.parts = parts(groups);
     void *args[] = {&a};
-    const hipError_t e = hipLaunchKernel(fn, dim3(unsigned(blocks), unsigned(a.parts)), dim3(256 * TG), args, 0, stream);
+    const int gx = std::min(blocks, 1 << 20);
+    const hipError_t e = hipLaunchKernel(tile_kernel<P, ZEROS>(a.M, groups),
+                                         dim3(unsigned(gx), unsigned(a.parts), unsigned(ceil_div(blocks, gx))),
+                                         dim3(unsigned(256 * groups)), args, 0, stream);
     if (e != hipSuccess || a.parts == 1) return e;
     return hipLaunchKernel(reinterpret_cast<const void *>(&w4a8_join_kernel),
                            dim3(unsigned(ceil_div(a.N, 256)), unsigned(a.M)), dim3(256), args, 0, stream);
 }
 
+// Waves of a strip for one row: all that the sums bear where strips are few,
+// and four where they are many (us, eight and four waves: 2560 x 2560 3.7 and
+// 4.1, 5120 x 27648 19.2 and 23.3; 13824 x 2560 6.6 and 6.2, 27648 x 5120 19.0
+// and 15.3, 55296 x 5120 26.6 and 24.7; 8640 x 3200, 540 strips, 5.6 and 5.7).
 template <int P, bool ZEROS>
 hipError_t w4_launch(const W4Launch &a, int cus, hipStream_t stream) {
-    if (a.M > 16) return w4_tiles_launch<P, ZEROS>(a, cus, stream);
-    const void *fn = a.M == 1 ? reinterpret_cast<const void *>(&w4a8_kernel<P, 1, ZEROS, true>)
-                              : reinterpret_cast<const void *>(&w4a8_kernel<P, 1, ZEROS, false>);
-    const int per = a.M == 1 ? 1 : 4;
-    const int nw = std::min(kMaxWaves, a.KT);
+    if (a.M > 1) return w4_tiles_launch<P, ZEROS>(a, cus, stream);
+    const int nw = std::min(a.strips > 2 * cus ? 4 : kMaxWaves, a.KT), gx = std::min(a.strips, 1 << 20);
     W4Launch l = a;
     void *args[] = {&l};
-    const int gx = std::min(a.strips, 1 << 20);
-    return hipLaunchKernel(fn, dim3(unsigned(gx), unsigned(ceil_div(a.strips, gx))), dim3(unsigned(64 * nw)), args,
-                           size_t(nw) * per * 256, stream);
+    return hipLaunchKernel(reinterpret_cast<const void *>(&w4a8_row_kernel<P, ZEROS>),
+                           dim3(unsigned(gx), unsigned(ceil_div(a.strips, gx))), dim3(unsigned(64 * nw)), args,
+                           size_t(std::min(a.KT * kTileK, kRowChunk)), stream);
 }
 
 template <int P>
