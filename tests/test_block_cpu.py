@@ -2,13 +2,16 @@
 worked values, host packers and size queries against it, and the refusals of
 every entry point (rejected before any HIP call: the stand-in pointers are
 never read)."""
-import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
 import torch
 
 import w2a8_gemv_amd as w2a8
+from conftest import ROOT
 from oracle import block
 
 NULL, SHAPE, ALIGN, VALUE, BUFSIZE = 1, 2, 3, 4, 5
@@ -140,10 +143,10 @@ def norm_call(**kw):
 
 
 def w4_call(**kw):
-    a = dict(apart(["w", "x", "s", "f", "b"]), M=3, N=40, K=200, g=64, t=2, z=1)
+    a = dict(apart(["w", "x", "s", "f", "b", "ws"]), M=3, N=40, K=200, g=64, t=2, z=1, n=0)
     a.update(kw)
     return w2a8.lib().w4a8_gemm(a["w"], a["x"], a["s"], a["M"], a["N"], a["K"], a["g"], a["t"], a["z"], a["f"],
-                                a["b"], None)
+                                a["b"], a["ws"], a["n"], None)
 
 
 MOE_IN = {"x": 3 * 200, "sa": 12, "l": 3 * 6 * 2, "wg": 0, "wu": 0, "wd": 0, "sg": 24, "su": 24, "sd": 24}
@@ -199,6 +202,25 @@ def test_w4_gemm_refuses():
             if out != other:
                 assert w4_call(**{out: at[other] + (n[other] - 1) // 16 * 16}) == VALUE
                 assert w4_call(**{other: at[out] + (n[out] - 1) // 16 * 16}) == VALUE
+
+
+def test_w4_gemm_refuses_workspaces():
+    L = w2a8.lib()
+    assert L.w4a8_workspace_bytes(1, 1 << 30, 1048448) == 0 and L.w4a8_workspace_bytes(64, 40, 2047 - 128) == 0
+    for bad in ((0, 5, 5), (65, 5, 5), (5, 0, 5), (5, (1 << 30) + 1, 5), (5, 5, 0), (5, 5, 1048449)):
+        assert L.w4a8_workspace_bytes(*bad) == -1
+        with pytest.raises(w2a8.W2A8Error):
+            w2a8.w4a8_workspace_bytes(*bad)
+    big = dict(M=3, N=40, K=6400)
+    need = w2a8.w4a8_workspace_bytes(3, 40, 6400)
+    assert need == 4 * 3 * 40 * 6
+    assert w4_call(**big, ws=None, n=need) == NULL and w4_call(**big, n=need - 1) == BUFSIZE
+    assert w4_call(**big, ws=FAKE + 8, n=need) == ALIGN
+    at = apart(["w", "x", "s", "f", "b", "ws"])
+    n = {"w": w2a8.w4a8_packed_bytes(40, 6400, 64, True), "x": 3 * 6400, "s": 12, "f": 480, "b": 240, "ws": need}
+    for other in "wxsfb":
+        assert w4_call(**big, n=need, **{"ws": at[other] + (n[other] - 1) // 16 * 16}) == VALUE
+        assert w4_call(**big, n=need, **{other: at["ws"] + (need - 1) // 16 * 16}) == VALUE
 
 
 def test_moe_refuses():
@@ -289,6 +311,15 @@ def test_binding_checks_of_the_products(host_as_gpu):
     y = w2a8.gemm_w4a8(w, x[0], s[:1], 20, 40, 32, torch.bfloat16, True, torch.bfloat16)
     assert y.shape == (1, 20) and y.dtype == torch.bfloat16
     assert host_as_gpu[-1][1][7:9] == (1, 1) and host_as_gpu[-2][1][7:9] == (2, 1)
+    long = t((3, 6400), dtype=torch.int8)
+    wl = t(w2a8.w4a8_packed_bytes(20, 6400, 32), dtype=torch.uint8)
+    w2a8.gemm_w4a8(wl, long, s, 20, 6400, 32)
+    need = w2a8.w4a8_workspace_bytes(3, 20, 6400)
+    assert need > 0 and host_as_gpu[-1][1][-2] == need
+    y = t(3, 20)
+    w2a8.w4a8_gemm(wl, long, s, 3, 20, 6400, 32, y_f32=y, workspace=t(need, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        w2a8.w4a8_gemm(wl, long, s, 3, 20, 6400, 32, y_f32=y, workspace=t(need - 1, dtype=torch.uint8))
     for args, kw, err in (((w[:-1], x, s, 20, 40, 32), {"zeros": True}, ValueError), ((w, x, s, 20, 39, 32), {}, ValueError),
                           ((w, x, s[:2], 20, 40, 32), {}, ValueError), ((w, x.short(), s, 20, 40, 32), {}, TypeError),
                           ((w, x, s, 20, 40, 48), {}, w2a8.W2A8Error),
@@ -311,7 +342,8 @@ def test_binding_checks_of_the_mixture(host_as_gpu):
                     ({"logits": t(2, E)}, ValueError), ({"logits": t(3, E).double()}, TypeError), ({"logits": None}, TypeError),
                     ({"s_up": t(E - 1)}, ValueError), ({"w_gate": a["w_gate"][1:]}, ValueError),
                     ({"w_down": a["w_down"].int()}, TypeError), ({"activation": "gelu"}, ValueError),
-                    ({"s_a": t(4)}, ValueError), ({"out_dtype": torch.float16}, TypeError)):
+                    ({"s_a": t(4)}, ValueError), ({"out_dtype": torch.float16}, TypeError),
+                    ({"s_gate": [1.0] * E}, TypeError), ({"w_up": a["w_up"].t()}, ValueError)):
         with pytest.raises(err):
             w2a8.moe(**{**a, **kw})
     y = t(3, H)
@@ -321,3 +353,18 @@ def test_binding_checks_of_the_mixture(host_as_gpu):
     assert host_as_gpu[-1][1][-2] == need
     with pytest.raises(ValueError):
         w2a8.w2a8_moe(*raw, 3, H, I, E, 2, y_f32=y, workspace=t(need - 1, dtype=u8))
+
+
+# ---------------------------------------------------------------------------
+# sources
+# ---------------------------------------------------------------------------
+@pytest.mark.skipif(shutil.which("hipcc") is None, reason="needs hipcc")
+def test_kernels_claim_no_alignment_that_rows_lack():
+    """Rows start wherever their length puts them: no access may be made through a pointer whose
+    type claims more alignment than its elements have."""
+    csrc = os.path.join(ROOT, "w2a8_gemv_amd", "csrc")
+    srcs = [os.path.join(csrc, f) for f in ("rmsnorm.hip", "w4a8.hip", "moe.hip", "host_block.hip")]
+    res = subprocess.run(["hipcc", "--offload-arch=gfx950", "-std=c++17", "-fsyntax-only",
+                          "-Werror=align-mismatch", "-I", os.path.join(ROOT, "include"), "-I", csrc, *srcs],
+                         capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stderr[-2000:]

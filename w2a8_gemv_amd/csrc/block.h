@@ -47,7 +47,7 @@ struct NormLaunch {
     float eps;
     int M, K;
 };
-hipError_t launch_rmsnorm_quant(const NormLaunch &a, int type, hipStream_t stream);
+hipError_t launch_rmsnorm_quant(const NormLaunch &a, int type, int cus, hipStream_t stream);
 
 // Products with 4-bit weights (W4T16x128).
 constexpr int kW4Rows = 16;

@@ -80,7 +80,7 @@ int rmsnorm_quant_int8(const void *x, const void *residual, const void *weight, 
     const int st = current_device(&dev);
     if (st != W2A8_OK) return st;
     const NormLaunch a = {x, residual, weight, h, x_q, s_a, eps, int(M), int(K)};
-    const hipError_t e = launch_rmsnorm_quant(a, type, static_cast<hipStream_t>(stream));
+    const hipError_t e = launch_rmsnorm_quant(a, type, dev.cus, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? W2A8_OK : W2A8_ERR_LAUNCH;
 }
 

@@ -254,8 +254,13 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormLaunch a) {
     }
 }
 
+// Lanes of a row: with a row or less for every compute unit, one chunk to a
+// lane; beyond, half as many lanes of two chunks, so that more rows are on
+// their way (us, 1024 and 512 lanes at most: 8192 x 5120 bf16 with a residual
+// 69.6 and 62.1, 2048 x 6912 29.5 and 25.0, 2045 x 6907 fp32 without 24.7 and
+// 21.5; 256 lanes 62.2, 25.5 and 23.3).
 template <int TYPE>
-hipError_t norm_type(const NormLaunch &a, hipStream_t stream) {
+hipError_t norm_type(const NormLaunch &a, int cus, hipStream_t stream) {
     const int slots = (a.K + 7) / 8;
     const void *fn = reinterpret_cast<const void *>(&norm_long_kernel<TYPE>);
     int threads = 1024;
@@ -264,7 +269,8 @@ hipError_t norm_type(const NormLaunch &a, hipStream_t stream) {
                                            reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 2>),
                                            reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 3>),
                                            reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 4>)};
-        const int cpl = (slots + 1023) / 1024;
+        const int lanes = a.M > cus ? 512 : 1024;
+        const int cpl = std::max(std::min(4, (slots + lanes - 1) / lanes), (slots + 1023) / 1024);
         fn = fns[cpl - 1];
         threads = ((slots + cpl - 1) / cpl + 63) / 64 * 64;
     }
@@ -275,10 +281,10 @@ hipError_t norm_type(const NormLaunch &a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_rmsnorm_quant(const NormLaunch &a, int type, hipStream_t stream) {
-    return type == W2A8_F32    ? norm_type<W2A8_F32>(a, stream)
-           : type == W2A8_BF16 ? norm_type<W2A8_BF16>(a, stream)
-                               : norm_type<W2A8_F16>(a, stream);
+hipError_t launch_rmsnorm_quant(const NormLaunch &a, int type, int cus, hipStream_t stream) {
+    return type == W2A8_F32    ? norm_type<W2A8_F32>(a, cus, stream)
+           : type == W2A8_BF16 ? norm_type<W2A8_BF16>(a, cus, stream)
+                               : norm_type<W2A8_F16>(a, cus, stream);
 }
 
 }  // namespace w2a8
