@@ -558,32 +558,37 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeLaunch a, i
 // The matrix instruction (16x16x64, int8) takes activation rows as its first
 // operand and weight rows as its second: lane (r, c) brings row r and the 16
 // bytes of k-part c of both, and holds results of weight row r and activation
-// rows 4c .. 4c + 3.  A T32x128 slot holds four rows, so lane r stands for rows
-// 2r and 2r + 1 of the strip, the two words of 8 bytes of a slot, and reads
-// those of k-parts c and 4 + c: one tile in four instructions.  It multiplies the
-// codes w + 1 as they are; the sums are less the row's sum at the end.
-struct Words {
-    v2u h[2];
-};
+// rows 4c .. 4c + 3.  A T32x128 slot holds four rows of 16 k.  Lane r stands for
+// rows 2r and 2r + 1 of the strip and reads the slot of row group r / 2 and
+// k-part c + 4 (r % 2): its own two rows of one half of k, and two rows of its
+// neighbour's, which has those that it lacks.  A wave so reads a whole tile in
+// one load of 16 bytes a lane (64 tokens, 16 experts of 5120 x 6912: up 51 us,
+// down 29; with 8 bytes a lane, half a line at a time, 62 and 37).  The
+// instruction multiplies the codes w + 1 as they are; the sums are less the
+// row's sum at the end.
+typedef v4u Words;
 __device__ __forceinline__ Words load_words(const uint8_t *w) {
-    Words d;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) d.h[h] = __builtin_nontemporal_load(reinterpret_cast<const v2u *>(w + 64 * h));
-    return d;
+    return __builtin_nontemporal_load(reinterpret_cast<const v4u *>(w));
 }
-__device__ __forceinline__ int words_at(int r, int c) { return 16 * (8 * (r >> 1) + c) + 8 * (r & 1); }
+__device__ __forceinline__ int words_at(int r, int c) { return 16 * (8 * (r >> 1) + c + 4 * (r & 1)); }
+__device__ __forceinline__ uint32_t beside(uint32_t v) {      // lane ^ 1
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xF, 0xF, false));
+}
 // The 16 codes w + 1 of a word as bytes, in the order of k.
 __device__ __forceinline__ v4i code_bytes(uint32_t w) {
     return v4i{int(w & 0x03030303u), int((w >> 2) & 0x03030303u), int((w >> 4) & 0x03030303u),
                int((w >> 6) & 0x03030303u)};
 }
 __device__ __forceinline__ void add_tile(const Words &w, const v4u (&x)[2], v4i (&acc)[2]) {
+    const bool odd = threadIdx.x & 1;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t lo = beside(w[2 + j]), hi = beside(w[j]);
+        const uint32_t h[2] = {odd ? lo : w[j], odd ? w[2 + j] : hi};
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, x[h]), code_bytes(w.h[h][j]),
-                                                           acc[j], 0, 0, 0);
+        for (int i = 0; i < 2; ++i)
+            acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, x[i]), code_bytes(h[i]), acc[j], 0, 0, 0);
+    }
 }
 
 // Sums over tiles wv, wv + nw, ... of a strip of MATS matrices, against row x
