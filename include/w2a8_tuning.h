@@ -128,6 +128,29 @@ int w2a8_linear_plan(int64_t N, int64_t K, int cus, int int4, int *kernel, int *
 int w2a8_mx4_plan(int64_t M, int64_t N, int64_t K, int ternary, int outputs, int cus, int *kernel,
                   int *rows, int *cols, int *groups, int *pass);
 
+/* What w4a8_gemm (w2a8_block.h) runs for (M, N, K) on a device with `cus`
+ * (1..65536) compute units.  *kernel: 1 the one-row kernel (*groups waves
+ * that share a strip's k), 2 the tile kernel (*rows activation rows of its
+ * form, *groups groups of four waves that share a workgroup's k, *parts parts
+ * of k, joined by a second launch where there are several).  Returns W2A8_OK,
+ * W2A8_ERR_NULL, W2A8_ERR_SHAPE or W2A8_ERR_VALUE (cus). */
+int w2a8_w4a8_plan(int64_t M, int64_t N, int64_t K, int cus, int *kernel, int *rows, int *groups,
+                   int *parts);
+
+/* What w2a8_moe runs for these sizes on a device with `cus` (1..65536) compute
+ * units under the current knob.  *kernel: 1 one token at a time, 2 the token
+ * rows together, with *up and *down strips of weight rows to a workgroup of
+ * the two products.  Returns as w2a8_w4a8_plan. */
+int w2a8_moe_plan(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k, int cus, int *kernel,
+                  int *up, int *down);
+
+/* Measurement knob: kernels of w2a8_moe.  0 = automatic (default), 1 = one
+ * token at a time wherever its hidden rows fit LDS (top_k times I, rounded up
+ * to 128, at most 49152), 2 = the token rows together, 3 and 4 = together with
+ * one and with two strips to a workgroup.  Read when a call starts.  Returns
+ * W2A8_OK or W2A8_ERR_VALUE. */
+int w2a8_tune_moe(int kernel);
+
 #ifdef __cplusplus
 }
 #endif

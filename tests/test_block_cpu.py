@@ -2,6 +2,7 @@
 worked values, host packers and size queries against it, and the refusals of
 every entry point (rejected before any HIP call: the stand-in pointers are
 never read)."""
+import ctypes
 import os
 import shutil
 import subprocess
@@ -10,6 +11,7 @@ import numpy as np
 import pytest
 import torch
 
+import block_sizes
 import w2a8_gemv_amd as w2a8
 from conftest import ROOT
 from oracle import block
@@ -353,6 +355,57 @@ def test_binding_checks_of_the_mixture(host_as_gpu):
     assert host_as_gpu[-1][1][-2] == need
     with pytest.raises(ValueError):
         w2a8.w2a8_moe(*raw, 3, H, I, E, 2, y_f32=y, workspace=t(need - 1, dtype=u8))
+
+
+# ---------------------------------------------------------------------------
+# launch plans
+# ---------------------------------------------------------------------------
+def test_plan_queries_refuse():
+    L = w2a8.lib()
+    out = [ctypes.byref(ctypes.c_int()) for _ in range(4)]
+    for f, ok, n in ((L.w2a8_w4a8_plan, (40, 100, 200, 256), 4), (L.w2a8_moe_plan, (40, 100, 200, 8, 2, 256), 3)):
+        assert f(*ok, *out[:n]) == 0
+        for i in range(n):
+            assert f(*ok, *out[:i], None, *out[i + 1:n]) == NULL
+        for i in range(len(ok) - 1):
+            assert f(*ok[:i], 0, *ok[i + 1:], *out[:n]) == SHAPE
+        for bad in (0, 65537, (1 << 31) - 1):
+            assert f(*ok[:-1], bad, *out[:n]) == VALUE
+    assert L.w2a8_w4a8_plan(65, 100, 200, 256, *out) == SHAPE
+    assert L.w2a8_moe_plan(65, 100, 200, 8, 2, 256, *out[:3]) == SHAPE
+    assert L.w2a8_tune_moe(-1) == VALUE and L.w2a8_tune_moe(5) == VALUE and L.w2a8_tune_moe(0) == 0
+
+
+def test_test_sizes_reach_every_plan():
+    for want, sizes in block_sizes.W4.items():
+        for size in sizes:
+            p = w2a8.w4a8_plan(*size, block_sizes.CUS)
+            assert p[:3] + (p[3] > 1,) == want, (size, p)
+    for want, sizes in block_sizes.MOE.items():
+        for size in sizes:
+            assert w2a8.moe_plan(*size, block_sizes.CUS) == want, size
+    rng = np.random.default_rng(1)
+    for m, n, k in np.exp(rng.uniform(0, 1, (20000, 3)) * np.log([64, 200000, 100000])).round().astype(int).tolist():
+        p = w2a8.w4a8_plan(m, n, k, block_sizes.CUS)
+        waves = p[2] if p[0] == 1 else 0
+        assert p[:3] + (p[3] > 1,) in block_sizes.W4 or (waves and waves == min(-(-k // 128), 8 if n <= 8192 else 4)), (m, n, k, p)
+        assert p[3] == 1 or 4 * m * n * p[3] <= w2a8.w4a8_workspace_bytes(m, n, k)
+
+
+def test_moe_knob():
+    sizes = (8, 1300, 2000, 6, 3)
+    try:
+        want = {0: w2a8.moe_plan(*sizes, 256), 1: (1, 1, 1), 3: (2, 1, 1), 4: (2, 2, 2)}
+        assert want[0][0] == 2
+        for mode, plan in want.items():
+            w2a8.tune_moe(mode)
+            assert w2a8.moe_plan(*sizes, 256) == plan
+        w2a8.tune_moe(1)
+        assert w2a8.moe_plan(1, 40, 50000, 3, 1, 256)[0] == 2          # does not fit LDS
+        w2a8.tune_moe(2)
+        assert w2a8.moe_plan(1, 40, 40, 3, 1, 256)[0] == 2
+    finally:
+        w2a8.tune_moe(0)
 
 
 # ---------------------------------------------------------------------------

@@ -32,6 +32,7 @@ __all__ = [
     "w4mx4_linear_gemv", "w2mx4_linear_gemv", "gemm_w4mx4", "gemm_w2mx4", "linear_w4mx4",
     "linear_w2mx4", "rmsnorm_quant_int8", "w4a8_packed_bytes", "pack_w4a8", "unpack_w4a8",
     "w4a8_workspace_bytes", "w4a8_gemm", "gemm_w4a8", "linear_w4a8", "w2a8_moe_workspace_bytes", "w2a8_moe", "moe",
+    "w4a8_plan", "moe_plan", "tune_moe",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw2a8.so")
@@ -115,6 +116,12 @@ def lib():
             getattr(L, name).restype = I32
         L.w4a8_packed_bytes.argtypes = [I64, I64, I64, I32]
         L.w4a8_packed_bytes.restype = I64
+        L.w2a8_w4a8_plan.argtypes = [I64, I64, I64, I32, P, P, P, P]
+        L.w2a8_w4a8_plan.restype = I32
+        L.w2a8_moe_plan.argtypes = [I64, I64, I64, I64, I64, I32, P, P, P]
+        L.w2a8_moe_plan.restype = I32
+        L.w2a8_tune_moe.argtypes = [I32]
+        L.w2a8_tune_moe.restype = I32
         L.w4a8_workspace_bytes.argtypes = [I64, I64, I64]
         L.w4a8_workspace_bytes.restype = I64
         L.w2a8_moe_workspace_bytes.argtypes = [I64] * 5
@@ -1231,6 +1238,29 @@ def mx4_plan(M: int, N: int, K: int, cus: int, ternary: bool = False, f32: bool 
     _check(lib().w2a8_mx4_plan(M, N, K, int(bool(ternary)), int(bool(f32)) + 2 * int(bool(bf16)), cus,
                                *[ctypes.byref(x) for x in v]), "w2a8_mx4_plan")
     return tuple(x.value for x in v)
+
+
+def w4a8_plan(M: int, N: int, K: int, cus: int):
+    """What gemm_w4a8 runs for (M, N, K) on `cus` compute units: (kernel, rows, groups, parts),
+    see w2a8_tuning.h."""
+    v = [ctypes.c_int() for _ in range(4)]
+    _check(lib().w2a8_w4a8_plan(M, N, K, cus, *[ctypes.byref(x) for x in v]), "w2a8_w4a8_plan")
+    return tuple(x.value for x in v)
+
+
+def moe_plan(M: int, H: int, I: int, E: int, top_k: int, cus: int):
+    """What moe runs for these sizes on `cus` compute units: (kernel, up, down), see
+    w2a8_tuning.h."""
+    v = [ctypes.c_int() for _ in range(3)]
+    _check(lib().w2a8_moe_plan(M, H, I, E, top_k, cus, *[ctypes.byref(x) for x in v]),
+           "w2a8_moe_plan")
+    return tuple(x.value for x in v)
+
+
+def tune_moe(kernel: int = 0):
+    """Kernels of moe: 0 automatic, 1 one token at a time where its hidden rows fit LDS, 2 token
+    rows together, 3 and 4 together with one and two strips to a workgroup."""
+    _check(lib().w2a8_tune_moe(kernel), "w2a8_tune_moe")
 
 
 def gemv_plan(N: int, K: int, cus: int):

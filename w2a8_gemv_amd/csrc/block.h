@@ -69,6 +69,12 @@ struct W4Launch {
 };
 // Most parts that k is split into (and the rows from which it may be).
 constexpr int kW4Parts = 8, kW4PartRows = 2;
+// How a product is run (w2a8_w4a8_plan): blocks of 16 activation rows (0: the
+// one-row kernel), waves of a strip or groups of waves, parts of k.
+struct W4Plan {
+    int blocks, groups, parts;
+};
+W4Plan w4_plan(int M, int strips, int KT, int cus);
 hipError_t launch_w4a8(const W4Launch &a, int cus, hipStream_t stream);
 
 // Mixture of experts: offsets into the workspace, all multiples of 256.
@@ -89,6 +95,14 @@ struct MoeLaunch {
     int64_t wb1, wb2;          // bytes of an expert's w_gate or w_up, w_down
     int M, H, I, E, top_k, act, renormalize, logit_type;
 };
+// How a mixture is run (w2a8_moe_plan), and the knob over it (w2a8_tune_moe).
+struct MoePlan {
+    bool one;           // a token at a time
+    int up, down;       // together: strips of a workgroup
+};
+MoePlan moe_plan(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k, int cus);
+int moe_mode();
+void set_moe_mode(int mode);
 hipError_t launch_moe(const MoeLaunch &a, int cus, hipStream_t stream);
 
 }  // namespace w2a8

@@ -5,6 +5,7 @@
 
 #include "block.h"
 #include "host_checks.h"
+#include "w2a8_tuning.h"
 
 namespace w2a8 {
 namespace {
@@ -258,6 +259,36 @@ int w2a8_moe(const int8_t *x, const float *s_a, const void *logits, int logit_ty
     a.renormalize = renormalize != 0;
     const hipError_t e = launch_moe(a, dev.cus, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? W2A8_OK : W2A8_ERR_LAUNCH;
+}
+
+int w2a8_w4a8_plan(int64_t M, int64_t N, int64_t K, int cus, int *kernel, int *rows, int *groups, int *parts) {
+    if (!kernel || !rows || !groups || !parts) return W2A8_ERR_NULL;
+    if (M < 1 || M > W4A8_MAX_M || !matrix_ok(N, K)) return W2A8_ERR_SHAPE;
+    if (cus < 1 || cus > 65536) return W2A8_ERR_VALUE;
+    const W4Plan p = w4_plan(int(M), int(ceil_div(N, kW4Rows)), int(w4_tiles(K)), cus);
+    *kernel = p.blocks ? 2 : 1;
+    *rows = p.blocks ? 16 * p.blocks : 1;
+    *groups = p.groups;
+    *parts = p.parts;
+    return W2A8_OK;
+}
+
+int w2a8_moe_plan(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k, int cus, int *kernel, int *up,
+                  int *down) {
+    if (!kernel || !up || !down) return W2A8_ERR_NULL;
+    if (!moe_ok(M, H, I, E, top_k)) return W2A8_ERR_SHAPE;
+    if (cus < 1 || cus > 65536) return W2A8_ERR_VALUE;
+    const MoePlan p = moe_plan(M, H, I, E, top_k, cus);
+    *kernel = p.one ? 1 : 2;
+    *up = p.one ? 1 : p.up;
+    *down = p.one ? 1 : p.down;
+    return W2A8_OK;
+}
+
+int w2a8_tune_moe(int kernel) {
+    if (kernel < 0 || kernel > 4) return W2A8_ERR_VALUE;
+    set_moe_mode(kernel);
+    return W2A8_OK;
 }
 
 }  // extern "C"

@@ -12,6 +12,8 @@
 //
 // All sums of products are integers, so how they are split and joined does
 // not show.  Weights are in the T32x128 layout, one matrix an expert.
+#include <atomic>
+
 #include "block.h"
 
 namespace w2a8 {
@@ -311,20 +313,16 @@ __device__ __forceinline__ float code_scale(float top) {
     return top < __builtin_inff() ? top / 127.0f : __builtin_nanf("");
 }
 
-#ifndef DSL
-#define DSL 4
-#define DD 4
-#define DTH 1024
-#endif
-// Workgroup (8 rows of y, token) of eight waves: wave w takes slice w % 2 of
-// the rows and quarter w / 2 of the steps of all the token's experts.
-constexpr int kDownDepth = DD;
-constexpr int kDownSlices = DSL, kDownThreads = DTH, kDownWaves = DTH / 64,
-              kDownParts = kDownWaves / kDownSlices, kDownRows = 4 * kDownSlices;
-#ifndef DA
-#define DA 4
-#endif
-constexpr int kDownAhead = DA;      // groups of four hidden values that a lane loads ahead
+// Workgroup (16 rows of y, token) of 16 waves: wave w takes slice w % 4 of the
+// rows and quarter w / 4 of the steps of all the token's experts.  Every
+// workgroup rounds all of the token's hidden rows, which is as many bytes to
+// read as its weights: eight rows to a workgroup made it slower (8 experts of
+// 2560 x 6912, two taken, both launches: 16.9 us, 16 rows 15.2, 32 rows 17.1;
+// with eight waves 16.0).
+constexpr int kDownDepth = 4;       // steps of a wave on their way
+constexpr int kDownAhead = 4;       // groups of four hidden values that a lane loads ahead
+constexpr int kDownThreads = 1024, kDownWaves = kDownThreads / 64;
+constexpr int kDownSlices = 4, kDownParts = kDownWaves / kDownSlices, kDownRows = 4 * kDownSlices;
 
 __global__ __launch_bounds__(kDownThreads) void moe_down_one_kernel(MoeLaunch a) {
     extern __shared__ __attribute__((aligned(16))) int8_t q[];     // [rank][tiles * 128]
@@ -850,12 +848,7 @@ hipError_t launch(const void *fn, dim3 grid, int threads, size_t lds, void **arg
 
 // Most LDS of the hidden rows of a token (the kernel has some of its own).
 constexpr int64_t kOneLds = 49152;
-#ifndef ONE_M
-#define ONE_M 3
-#endif
-bool one_at_a_time(const MoeLaunch &a) {
-    return a.M <= ONE_M && a.top_k * round_up(a.I, kTileK) <= kOneLds;
-}
+std::atomic<int> g_mode{0};
 
 }  // namespace
 
@@ -883,34 +876,64 @@ MoeSpace moe_space(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k) {
     return s;
 }
 
+int moe_mode() { return g_mode.load(std::memory_order_relaxed); }
+void set_moe_mode(int mode) { g_mode.store(mode, std::memory_order_relaxed); }
+
+// One token at a time reads an expert's weights once for every token that
+// takes it, but in two launches of some 10 us together; token rows together
+// read them once, in five launches of some 20.  So tokens go by themselves up
+// to two, and up to 36 MB of weights over all pairs (us, one at a time and
+// together; 8 experts of 2560 x 6912, two taken: two tokens 25.8 and 26.9, three
+// 30.8 and 30.6, four 38.5 and 31.7; 64 of 2560 x 640, eight taken: three tokens,
+// 29 MB, 18.6 and 26.5, four, 39 MB, 25.8 and 27.5, six, 59 MB, 31.6 and 29.7; 8 of
+// 2560 x 2560, one taken: six tokens, 29 MB, 18.7 and 21.7, eight, 39 MB, 23.7 and
+// 22.3; 32 of 1024 x 512, two taken, twelve tokens, 9 MB: 14.1 and 19.1).
+//
+// Together, a workgroup takes two strips of an expert where that leaves four
+// workgroups to a compute unit, so that a wave reads its rows for twice the
+// weights (the layer, us, two strips and one; 64 tokens, 16 experts of 5120 x
+// 6912: 95.3 and 99.2, 128 of 5120 x 1536, eight taken: 155 and 173), and one where
+// strips are fewer (13 tokens, 8 experts of 2560 x 6912: 40.5 and 38.2).
+MoePlan moe_plan(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k, int cus) {
+    MoePlan p;
+    const int mode = moe_mode();
+    const bool fits = top_k * round_up(I, kTileK) <= kOneLds;
+    const bool few = M <= 2 || double(M * top_k) * (0.75 * double(H) * double(I)) <= 36e6;
+    p.one = fits && (mode == 0 ? few : mode == 1);
+    const int64_t slots = std::min(E, M * top_k);
+    const auto strips = [&](int64_t N) { return ceil_div(ceil_div(N, kTileRows), 2) * slots >= 4 * int64_t(cus) ? 2 : 1; };
+    p.up = mode == 3 ? 1 : mode == 4 ? 2 : strips(I);
+    p.down = mode == 3 ? 1 : mode == 4 ? 2 : strips(H);
+    return p;
+}
+
 hipError_t launch_moe(const MoeLaunch &la, int cus, hipStream_t stream) {
     MoeLaunch a = la;
     const auto fn = [](auto *k) { return reinterpret_cast<const void *>(k); };
+    const MoePlan p = moe_plan(a.M, a.H, a.I, a.E, a.top_k, cus);
     const int64_t up = ceil_div(a.I, kTileRows), down = ceil_div(a.H, kTileRows);
     int slots = std::min(a.E, a.M * a.top_k);
     void *args[] = {&a, &slots};
     hipError_t e;
-    if (one_at_a_time(a)) {
+    if (p.one) {
         e = launch(fn(&moe_up_one_kernel), dim3(unsigned(up + 1), unsigned(a.top_k), unsigned(a.M)), 512, 0, args,
                    stream);
         if (e != hipSuccess) return e;
         return launch(fn(&moe_down_one_kernel), dim3(unsigned(ceil_div(a.H, kDownRows)), unsigned(a.M)), kDownThreads,
                       size_t(a.top_k * round_up(a.I, kTileK)), args, stream);
     }
-    const int64_t KT1 = ceil_div(a.H, kTileK), KT2 = ceil_div(a.I, kTileK);
-        // Two strips to a workgroup where that leaves four workgroups to a compute unit.
-    const bool up2 = ceil_div(up, 2) * slots >= 4 * cus, down2 = ceil_div(down, 2) * slots >= 4 * cus;
-    const int nw1 = int(std::min<int64_t>(kMoeWaves, KT1)), nw2 = int(std::min<int64_t>(kMoeWaves, KT2));
-    const size_t lds1 = size_t(nw1) * (up2 ? 8192 : 4096), lds2 = size_t(nw2) * (down2 ? 4096 : 2048);
-    if ((e = launch(fn(&moe_route_kernel), dim3(unsigned(1 + a.M)), kRouteThreads, 0, args, stream)) != hipSuccess) return e;
-    if ((e = launch(up2 ? fn(&moe_up_kernel<2, 2>) : fn(&moe_up_kernel<1, 3>),
-                    dim3(unsigned(ceil_div(up, up2 ? 2 : 1)), unsigned(slots)), 64 * nw1, lds1, args, stream)) != hipSuccess)
-        return e;
-    if ((e = launch(fn(&moe_quant_kernel), dim3(unsigned(a.M * a.top_k)), kQuantThreads, 0, args, stream)) != hipSuccess)
-        return e;
-    if ((e = launch(down2 ? fn(&moe_down_kernel<2, 3>) : fn(&moe_down_kernel<1, 4>),
-                    dim3(unsigned(ceil_div(down, down2 ? 2 : 1)), unsigned(slots)), 64 * nw2, lds2, args, stream)) != hipSuccess)
-        return e;
+    const int nw1 = int(std::min<int64_t>(kMoeWaves, ceil_div(a.H, kTileK)));
+    const int nw2 = int(std::min<int64_t>(kMoeWaves, ceil_div(a.I, kTileK)));
+    e = launch(fn(&moe_route_kernel), dim3(unsigned(1 + a.M)), kRouteThreads, 0, args, stream);
+    if (e != hipSuccess) return e;
+    e = launch(p.up == 2 ? fn(&moe_up_kernel<2, 2>) : fn(&moe_up_kernel<1, 3>),
+               dim3(unsigned(ceil_div(up, p.up)), unsigned(slots)), 64 * nw1, size_t(nw1 * p.up) * 4096, args, stream);
+    if (e != hipSuccess) return e;
+    e = launch(fn(&moe_quant_kernel), dim3(unsigned(a.M * a.top_k)), kQuantThreads, 0, args, stream);
+    if (e != hipSuccess) return e;
+    e = launch(p.down == 2 ? fn(&moe_down_kernel<2, 3>) : fn(&moe_down_kernel<1, 4>),
+               dim3(unsigned(ceil_div(down, p.down)), unsigned(slots)), 64 * nw2, size_t(nw2 * p.down) * 2048, args, stream);
+    if (e != hipSuccess) return e;
     return launch(fn(&moe_combine_kernel), dim3(unsigned(ceil_div(a.H, 256)), unsigned(a.M)), 256, 0, args, stream);
 }
 

@@ -104,7 +104,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4a8_row_kernel(W4Launch a) {
     __shared__ float red[kMaxWaves][16];
     const int tid = int(threadIdx.x), lane = tid & 63, r = lane & 15, c = lane >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), nw = int(blockDim.x) >> 6;
-    const int s = int(blockIdx.x + blockIdx.y * gridDim.x);
+    const int s = int(blockIdx.x + blockIdx.z * gridDim.x);
     if (s >= a.strips) return;
     const uint8_t *wp = a.w + int64_t(s) * a.KT * kW4TileBytes + 16 * lane;
     const uint16_t *sp = a.scales + (int64_t(s) * a.GQ * 16 + r) * 4;
@@ -356,56 +356,31 @@ __global__ __launch_bounds__(256) void w4a8_join_kernel(W4Launch a) {
 }
 
 template <int P, bool ZEROS>
-const void *tile_kernel(int M, int groups) {
+const void *w4_kernel(const W4Plan &p) {
     const auto fn = [](auto *k) { return reinterpret_cast<const void *>(k); };
-    return M <= 16   ? (groups == 4 ? fn(&w4a8_tile_kernel<P, 1, ZEROS, 4>) : fn(&w4a8_tile_kernel<P, 1, ZEROS, 2>))
-           : M <= 32 ? (groups == 4 ? fn(&w4a8_tile_kernel<P, 2, ZEROS, 4>) : fn(&w4a8_tile_kernel<P, 2, ZEROS, 2>))
-           : M <= 48 ? fn(&w4a8_tile_kernel<P, 3, ZEROS, 2>)
-                     : fn(&w4a8_tile_kernel<P, 4, ZEROS, 2>);
+    const bool four = p.groups == 4;
+    switch (p.blocks) {
+    case 0: return fn(&w4a8_row_kernel<P, ZEROS>);
+    case 1: return four ? fn(&w4a8_tile_kernel<P, 1, ZEROS, 4>) : fn(&w4a8_tile_kernel<P, 1, ZEROS, 2>);
+    case 2: return four ? fn(&w4a8_tile_kernel<P, 2, ZEROS, 4>) : fn(&w4a8_tile_kernel<P, 2, ZEROS, 2>);
+    case 3: return fn(&w4a8_tile_kernel<P, 3, ZEROS, 2>);
+    default: return fn(&w4a8_tile_kernel<P, 4, ZEROS, 2>);
+    }
 }
 
-// Workgroups of four strips.  Where these are half the compute units or fewer,
-// k is split into parts, about two workgroups to a compute unit, with four
-// tiles for every wave; the sums of parts go through memory (4.5 us for their
-// joining, so not for grids that fill most of the device: 19 x 13824 x 2570
-// 13.5 us whole, 16.5 + 4 in two parts).  Four groups of waves share a
-// workgroup's k where it has a compute unit to itself: 16 x 13824 x 2560 7.8 us
-// against 9.8, 32 x 5120 x 5120 10.9 against 13.3; two otherwise: 16 x 55296 x
-// 5120 32.5 against 34.3, 32 x 5120 x 27648 24.0 against 26.8, and beyond 32
-// rows, whose stages are larger: 64 x 5120 x 27648 30.2 against 34.3.
 template <int P, bool ZEROS>
-hipError_t w4_tiles_launch(const W4Launch &la, int cus, hipStream_t stream) {
+hipError_t w4_launch(const W4Launch &la, int cus, hipStream_t stream) {
     W4Launch a = la;
-    const int blocks = int(ceil_div(a.strips, 4));
-    const auto parts = [&](int groups) {
-        return 2 * blocks > cus ? 1 : std::max(1, std::min({2 * cus / blocks, a.KT / (4 * groups), kW4Parts}));
-    };
-    const bool four = a.M <= 16 ? blocks <= cus : a.M <= 32 && blocks * parts(4) <= cus;
-    const int groups = four ? 4 : 2;
-    a.parts = parts(groups);
+    const W4Plan p = w4_plan(a.M, a.strips, a.KT, cus);
+    a.parts = p.parts;
+    const int units = p.blocks ? int(ceil_div(a.strips, 4)) : a.strips, gx = std::min(units, 1 << 20);
+    const unsigned far = unsigned(ceil_div(units, gx)), threads = unsigned((p.blocks ? 256 : 64) * p.groups);
     void *args[] = {&a};
-    const int gx = std::min(blocks, 1 << 20);
-    const hipError_t e = hipLaunchKernel(tile_kernel<P, ZEROS>(a.M, groups),
-                                         dim3(unsigned(gx), unsigned(a.parts), unsigned(ceil_div(blocks, gx))),
-                                         dim3(unsigned(256 * groups)), args, 0, stream);
+    const hipError_t e = hipLaunchKernel(w4_kernel<P, ZEROS>(p), dim3(unsigned(gx), unsigned(a.parts), far), dim3(threads),
+                                         args, p.blocks ? 0 : size_t(std::min(a.KT * kTileK, kRowChunk)), stream);
     if (e != hipSuccess || a.parts == 1) return e;
     return hipLaunchKernel(reinterpret_cast<const void *>(&w4a8_join_kernel),
                            dim3(unsigned(ceil_div(a.N, 256)), unsigned(a.M)), dim3(256), args, 0, stream);
-}
-
-// Waves of a strip for one row: all that the sums bear where strips are few,
-// and four where they are many (us, eight and four waves: 2560 x 2560 3.7 and
-// 4.1, 5120 x 27648 19.2 and 23.3; 13824 x 2560 6.6 and 6.2, 27648 x 5120 19.0
-// and 15.3, 55296 x 5120 26.6 and 24.7; 8640 x 3200, 540 strips, 5.6 and 5.7).
-template <int P, bool ZEROS>
-hipError_t w4_launch(const W4Launch &a, int cus, hipStream_t stream) {
-    if (a.M > 1) return w4_tiles_launch<P, ZEROS>(a, cus, stream);
-    const int nw = std::min(a.strips > 2 * cus ? 4 : kMaxWaves, a.KT), gx = std::min(a.strips, 1 << 20);
-    W4Launch l = a;
-    void *args[] = {&l};
-    return hipLaunchKernel(reinterpret_cast<const void *>(&w4a8_row_kernel<P, ZEROS>),
-                           dim3(unsigned(gx), unsigned(ceil_div(a.strips, gx))), dim3(unsigned(64 * nw)), args,
-                           size_t(std::min(a.KT * kTileK, kRowChunk)), stream);
 }
 
 template <int P>
@@ -414,6 +389,31 @@ hipError_t w4_zeros(const W4Launch &a, int cus, hipStream_t stream) {
 }
 
 }  // namespace
+
+// One row: waves of a strip, all that the sums bear where strips are few, and
+// four where they are many (us, eight and four waves: 2560 x 2560 3.7 and 4.1,
+// 5120 x 27648 19.2 and 23.3; 13824 x 2560 6.6 and 6.2, 27648 x 5120 19.0 and 15.3,
+// 55296 x 5120 26.6 and 24.7; 8640 x 3200, 540 strips, 5.6 and 5.7).
+//
+// More rows: workgroups of four strips.  Where these are half the compute units
+// or fewer, k is split into parts, about two workgroups to a compute unit, with
+// four tiles for every wave; the sums of parts go through memory (4.5 us for
+// their joining, so not for grids that fill most of the device: 19 x 13824 x 2570
+// 13.5 us whole, 16.5 + 4 in two parts).  Four groups of waves share a
+// workgroup's k where it has a compute unit to itself: 16 x 13824 x 2560 7.8 us
+// against 9.8, 32 x 5120 x 5120 10.9 against 13.3; two otherwise: 16 x 55296 x
+// 5120 32.5 against 34.3, 32 x 5120 x 27648 24.0 against 26.8, and beyond 32
+// rows, whose stages are larger: 64 x 5120 x 27648 30.2 against 34.3.
+W4Plan w4_plan(int M, int strips, int KT, int cus) {
+    if (M == 1) return {0, std::min(strips > 2 * cus ? 4 : kMaxWaves, KT), 1};
+    const int units = int(ceil_div(strips, 4));
+    const auto parts = [&](int groups) {
+        return 2 * units > cus ? 1 : std::max(1, std::min({2 * cus / units, KT / (4 * groups), kW4Parts}));
+    };
+    const bool four = M <= 16 ? units <= cus : M <= 32 && units * parts(4) <= cus;
+    const int groups = four ? 4 : 2;
+    return {(M + 15) / 16, groups, parts(groups)};
+}
 
 hipError_t launch_w4a8(const W4Launch &a, int cus, hipStream_t stream) {
     return a.group == 128 ? w4_zeros<1>(a, cus, stream)
