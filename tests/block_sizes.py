@@ -25,6 +25,6 @@ W4 = {
 # By moe_plan's (kernel, up, down).
 MOE = {
     (1, 1, 1): [(1, 640, 1000, 64, 8), (2, 1300, 2001, 6, 3), (40, 100, 130, 5, 2)],
-    (2, 1, 1): [(5, 1300, 2000, 6, 3), (1, 40, 3500, 16, 16)],
+    (2, 1, 1): [(5, 1300, 4001, 6, 3), (1, 40, 3500, 16, 16)],
     (2, 2, 2): [(64, 1300, 1500, 64, 6)],
 }

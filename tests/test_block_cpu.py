@@ -393,7 +393,7 @@ def test_test_sizes_reach_every_plan():
 
 
 def test_moe_knob():
-    sizes = (8, 1300, 2000, 6, 3)
+    sizes = (8, 1300, 4001, 6, 3)
     try:
         want = {0: w2a8.moe_plan(*sizes, 256), 1: (1, 1, 1), 3: (2, 1, 1), 4: (2, 2, 2)}
         assert want[0][0] == 2
