@@ -589,16 +589,16 @@ __device__ __forceinline__ void add_tile(const Words &w, const v4u (&x)[2], v4i 
     }
 }
 
-// Sums over tiles wv, wv + nw, ... of a strip of MATS matrices, against row x
+// Sums over tiles wv, wv + kMoeWaves, ... of a strip of MATS matrices, against row x
 // (padded to whole tiles), D tiles of a wave on their way.
 template <int MATS, int D>
-__device__ __forceinline__ void strip_sums(const uint8_t *const (&w)[MATS], const int8_t *x, int KT, int wv, int nw,
+__device__ __forceinline__ void strip_sums(const uint8_t *const (&w)[MATS], const int8_t *x, int KT, int wv,
                                            v4i (&acc)[MATS][2]) {
     Words d[D][MATS];
     v4u xv[D][2];
-    const int n = wv < KT ? (KT - wv + nw - 1) / nw : 0;
+    const int n = wv < KT ? (KT - wv + kMoeWaves - 1) / kMoeWaves : 0;
     auto load = [&](int i, int j) __attribute__((always_inline)) {
-        const int t = wv + i * nw;
+        const int t = wv + i * kMoeWaves;
 #pragma unroll
         for (int k = 0; k < MATS; ++k) d[j][k] = load_words(w[k] + int64_t(t) * kTileBytes);
 #pragma unroll
@@ -632,26 +632,20 @@ __device__ __forceinline__ void strip_sums(const uint8_t *const (&w)[MATS], cons
     }
 }
 
-// Sums of the waves' words; wave w is left with the words of rows 4c + i, i %
-// nw == w (v[COUNT / 4 blocks][4]), the others' are its own.
+// Sums of the waves' results; wave w is left with those of rows 4c + w.
 template <int BLOCKS>
-__device__ __forceinline__ void join_waves(int *red, int lane, int wv, int nw, v4i (&v)[BLOCKS]) {
-    if (nw == 1) return;
+__device__ __forceinline__ void join_waves(int *red, int lane, int wv, const v4i (&v)[BLOCKS], int (&sum)[BLOCKS]) {
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < BLOCKS; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) red[((wv * BLOCKS + k) * 4 + i) * 64 + lane] = v[k][i];
+        for (int i = 0; i < kMoeWaves; ++i) red[((i * BLOCKS + k) * kMoeWaves + wv) * 64 + lane] = v[k][i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (i % nw != wv) continue;
+    for (int k = 0; k < BLOCKS; ++k) {
+        sum[k] = 0;
 #pragma unroll
-        for (int k = 0; k < BLOCKS; ++k) {
-            int s = 0;
-            for (int w = 0; w < nw; ++w) s += red[((w * BLOCKS + k) * 4 + i) * 64 + lane];
-            v[k][i] = s;
-        }
+        for (int w = 0; w < kMoeWaves; ++w) sum[k] += red[((wv * BLOCKS + k) * kMoeWaves + w) * 64 + lane];
     }
 }
 
@@ -673,7 +667,7 @@ typedef v2f v2f_a __attribute__((aligned(4)));
 // STRIPS strips of a slot's expert to a workgroup (those past the last are
 // read as the last, and not stored): its rows are read once for all of them.
 template <int STRIPS, int D>
-__global__ __launch_bounds__(512) void moe_up_kernel(MoeLaunch a) {
+__global__ __launch_bounds__(64 * kMoeWaves) void moe_up_kernel(MoeLaunch a) {
     extern __shared__ __attribute__((aligned(16))) int red[];
     const Slot slot = reinterpret_cast<const Slot *>(a.ws + a.sp.slot)[blockIdx.y];
     if (slot.expert < 0) return;
@@ -682,7 +676,7 @@ __global__ __launch_bounds__(512) void moe_up_kernel(MoeLaunch a) {
     const uint64_t mask = (uint64_t(slot.mask[1]) << 32) | slot.mask[0];
     const int tokens = __popcll(mask);
     const int lane = int(threadIdx.x) & 63, r = lane & 15, c = lane >> 4;
-    const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), nw = int(blockDim.x) >> 6;
+    const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int KT = (a.H + kTileK - 1) / kTileK, last = (a.I - 1) / kTileRows;
     const uint8_t *w[2 * STRIPS];
 #pragma unroll
@@ -700,42 +694,37 @@ __global__ __launch_bounds__(512) void moe_up_kernel(MoeLaunch a) {
         const float mine = a.sa[token];            // of row r
         const int sum = row_sums[token];
         v4i acc[2 * STRIPS][2];
-        strip_sums<2 * STRIPS, D>(w, rows + int64_t(token) * KT * kTileK, KT, wv, nw, acc);
+        strip_sums<2 * STRIPS, D>(w, rows + int64_t(token) * KT * kTileK, KT, wv, acc);
         v4i v[4 * STRIPS];
 #pragma unroll
         for (int k = 0; k < 4 * STRIPS; ++k) v[k] = acc[k >> 1][k & 1];
-        join_waves(red, lane, wv, nw, v);
-        // Lane (r, c): weight rows 2r + j, pairs m0 + 4c + i.
+        int all[4 * STRIPS];
+        join_waves(red, lane, wv, v, all);
+        // Lane (r, c): weight rows 2r + j, pair m.
+        const float sa = __shfl(mine, 4 * c + wv);
+        const int sx = __shfl(sum, 4 * c + wv), m = m0 + 4 * c + wv;
+        float *out = hidden + int64_t(slot.begin + m) * a.I;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i % nw != wv) continue;
-            const float sa = __shfl(mine, 4 * c + i);
-            const int sx = __shfl(sum, 4 * c + i), m = m0 + 4 * c + i;
-            if (m >= tokens) continue;
+        for (int k = 0; k < STRIPS; ++k) {
+            const int row = (s0 + k) * kTileRows + 2 * r;
+            float h[2];
 #pragma unroll
-            for (int k = 0; k < STRIPS; ++k) {
-                const int row = (s0 + k) * kTileRows + 2 * r;
-                float h[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    h[j] = activate(a.act, (float(v[4 * k + j][i] - sx) * sa) * sg, (float(v[4 * k + 2 + j][i] - sx) * sa) * su);
-                float *out = hidden + int64_t(slot.begin + m) * a.I + row;
-                if (row + 1 < a.I)
-                    *reinterpret_cast<v2f_a *>(out) = v2f{h[0], h[1]};
-                else if (row < a.I)
-                    out[0] = h[0];
-            }
+            for (int j = 0; j < 2; ++j)
+                h[j] = activate(a.act, (float(all[4 * k + j] - sx) * sa) * sg, (float(all[4 * k + 2 + j] - sx) * sa) * su);
+            if (m < tokens && row + 1 < a.I)
+                *reinterpret_cast<v2f_a *>(out + row) = v2f{h[0], h[1]};
+            else if (m < tokens && row < a.I)
+                out[row] = h[0];
         }
     }
 }
 
 // One workgroup per pair: its hidden row to int8, padded with zeros to whole
 // tiles; the first values stay in registers between the two walks.
-constexpr int kQuantThreads = 512, kQuantKept = 4;
+constexpr int kQuantThreads = 512, kQuantWaves = kQuantThreads / 64, kQuantKept = 4;
 
 __global__ __launch_bounds__(kQuantThreads) void moe_quant_kernel(MoeLaunch a) {
-    __shared__ uint32_t most[kQuantThreads / 64];
-    __shared__ int red[kQuantThreads / 64];
+    __shared__ uint32_t most[kQuantWaves];
     const int pair = int(blockIdx.x), tid = int(threadIdx.x);
     const float *h = reinterpret_cast<const float *>(a.ws + a.sp.hidden) + int64_t(pair) * a.I;
     const int Ip = (a.I + kTileK - 1) / kTileK * kTileK;
@@ -755,7 +744,7 @@ __global__ __launch_bounds__(kQuantThreads) void moe_quant_kernel(MoeLaunch a) {
     if ((tid & 63) == 0) most[tid >> 6] = top;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kQuantThreads / 64; ++i) top = max(top, most[i]);
+    for (int i = 0; i < kQuantWaves; ++i) top = max(top, most[i]);
     const float factor = code_factor(__uint_as_float(top));
     uint32_t *out = reinterpret_cast<uint32_t *>(a.ws + a.sp.codes + int64_t(pair) * Ip);
     int sum = 0;
@@ -768,14 +757,14 @@ __global__ __launch_bounds__(kQuantThreads) void moe_quant_kernel(MoeLaunch a) {
     for (int i = 0; i < kQuantKept; ++i)
         if (4 * (tid + kQuantThreads * i) < Ip) store(tid + kQuantThreads * i, kept[i]);
     for (int g = tid + kQuantThreads * kQuantKept; 4 * g < Ip; g += kQuantThreads) store(g, load4(h, 4 * g, a.I));
-    sum = block_sum(red, sum);
-    if (tid != 0) return;
-    reinterpret_cast<float *>(a.ws + a.sp.scales)[pair] = code_scale(__uint_as_float(top));
-    reinterpret_cast<int *>(a.ws + a.sp.code_sums)[pair] = sum;
+    // (The waves' sums as they are: their reader adds them.)
+    sum = wave_sum(sum);
+    if ((tid & 63) == 0) reinterpret_cast<int *>(a.ws + a.sp.code_sums)[pair * kQuantWaves + (tid >> 6)] = sum;
+    if (tid == 0) reinterpret_cast<float *>(a.ws + a.sp.scales)[pair] = code_scale(__uint_as_float(top));
 }
 
 template <int STRIPS, int D>
-__global__ __launch_bounds__(512) void moe_down_kernel(MoeLaunch a) {
+__global__ __launch_bounds__(64 * kMoeWaves) void moe_down_kernel(MoeLaunch a) {
     extern __shared__ __attribute__((aligned(16))) int red[];
     const Slot slot = reinterpret_cast<const Slot *>(a.ws + a.sp.slot)[blockIdx.y];
     if (slot.expert < 0) return;
@@ -785,7 +774,7 @@ __global__ __launch_bounds__(512) void moe_down_kernel(MoeLaunch a) {
     float *part = reinterpret_cast<float *>(a.ws + a.sp.part);
     const int tokens = __popc(slot.mask[0]) + __popc(slot.mask[1]);
     const int lane = int(threadIdx.x) & 63, r = lane & 15, c = lane >> 4;
-    const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), nw = int(blockDim.x) >> 6;
+    const int wv = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int KT = (a.I + kTileK - 1) / kTileK, last = (a.H - 1) / kTileRows;
     const uint8_t *w[STRIPS];
 #pragma unroll
@@ -797,29 +786,27 @@ __global__ __launch_bounds__(512) void moe_down_kernel(MoeLaunch a) {
     for (int m0 = 0; m0 < tokens; m0 += kMoeRows) {
         const int at = slot.begin + min(m0 + r, tokens - 1);
         const float mine = scales[at];             // of row r
-        const int sum = code_sums[at];
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < kQuantWaves; ++i) sum += code_sums[at * kQuantWaves + i];
         v4i acc[STRIPS][2];
-        strip_sums<STRIPS, D>(w, codes + int64_t(at) * KT * kTileK, KT, wv, nw, acc);
+        strip_sums<STRIPS, D>(w, codes + int64_t(at) * KT * kTileK, KT, wv, acc);
         v4i v[2 * STRIPS];
 #pragma unroll
         for (int k = 0; k < 2 * STRIPS; ++k) v[k] = acc[k >> 1][k & 1];
-        join_waves(red, lane, wv, nw, v);
+        int all[2 * STRIPS];
+        join_waves(red, lane, wv, v, all);
+        const float sh = __shfl(mine, 4 * c + wv);
+        const int sx = __shfl(sum, 4 * c + wv), m = m0 + 4 * c + wv;
+        float *out = part + int64_t(slot.begin + m) * a.H;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i % nw != wv) continue;
-            const float sh = __shfl(mine, 4 * c + i);
-            const int sx = __shfl(sum, 4 * c + i), m = m0 + 4 * c + i;
-            if (m >= tokens) continue;
-#pragma unroll
-            for (int k = 0; k < STRIPS; ++k) {
-                const int row = (s0 + k) * kTileRows + 2 * r;
-                float *out = part + int64_t(slot.begin + m) * a.H + row;
-                const v2f y = {(float(v[2 * k][i] - sx) * sh) * sd, (float(v[2 * k + 1][i] - sx) * sh) * sd};
-                if (row + 1 < a.H)
-                    *reinterpret_cast<v2f_a *>(out) = y;
-                else if (row < a.H)
-                    out[0] = y[0];
-            }
+        for (int k = 0; k < STRIPS; ++k) {
+            const int row = (s0 + k) * kTileRows + 2 * r;
+            const v2f y = {(float(all[2 * k] - sx) * sh) * sd, (float(all[2 * k + 1] - sx) * sh) * sd};
+            if (m < tokens && row + 1 < a.H)
+                *reinterpret_cast<v2f_a *>(out + row) = y;
+            else if (m < tokens && row < a.H)
+                out[row] = y[0];
         }
     }
 }
@@ -866,7 +853,7 @@ MoeSpace moe_space(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k) {
     s.slot = take(W2A8_MOE_MAX_E * sizeof(Slot));
     s.pair = take(sizeof(Pairs));
     s.scales = take(4 * pairs);
-    s.code_sums = take(4 * pairs);
+    s.code_sums = take(4 * kQuantWaves * pairs);
     s.row_sums = take(4 * M);
     s.rows = take(M * round_up(H, kTileK));
     s.codes = take(pairs * round_up(I, kTileK));
@@ -922,17 +909,17 @@ hipError_t launch_moe(const MoeLaunch &la, int cus, hipStream_t stream) {
         return launch(fn(&moe_down_one_kernel), dim3(unsigned(ceil_div(a.H, kDownRows)), unsigned(a.M)), kDownThreads,
                       size_t(a.top_k * round_up(a.I, kTileK)), args, stream);
     }
-    const int nw1 = int(std::min<int64_t>(kMoeWaves, ceil_div(a.H, kTileK)));
-    const int nw2 = int(std::min<int64_t>(kMoeWaves, ceil_div(a.I, kTileK)));
     e = launch(fn(&moe_route_kernel), dim3(unsigned(1 + a.M)), kRouteThreads, 0, args, stream);
     if (e != hipSuccess) return e;
     e = launch(p.up == 2 ? fn(&moe_up_kernel<2, 2>) : fn(&moe_up_kernel<1, 3>),
-               dim3(unsigned(ceil_div(up, p.up)), unsigned(slots)), 64 * nw1, size_t(nw1 * p.up) * 4096, args, stream);
+               dim3(unsigned(ceil_div(up, p.up)), unsigned(slots)), 64 * kMoeWaves, size_t(kMoeWaves * p.up) * 4096, args,
+               stream);
     if (e != hipSuccess) return e;
     e = launch(fn(&moe_quant_kernel), dim3(unsigned(a.M * a.top_k)), kQuantThreads, 0, args, stream);
     if (e != hipSuccess) return e;
     e = launch(p.down == 2 ? fn(&moe_down_kernel<2, 3>) : fn(&moe_down_kernel<1, 4>),
-               dim3(unsigned(ceil_div(down, p.down)), unsigned(slots)), 64 * nw2, size_t(nw2 * p.down) * 2048, args, stream);
+               dim3(unsigned(ceil_div(down, p.down)), unsigned(slots)), 64 * kMoeWaves, size_t(kMoeWaves * p.down) * 2048,
+               args, stream);
     if (e != hipSuccess) return e;
     return launch(fn(&moe_combine_kernel), dim3(unsigned(ceil_div(a.H, 256)), unsigned(a.M)), 256, 0, args, stream);
 }
