@@ -818,11 +818,20 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(MoeLaunch a) {
     const float *part = reinterpret_cast<const float *>(a.ws + a.sp.part);
     if (n >= a.H) return;
     float y = picked[0].expert == -2 ? __builtin_nanf("") : 0.0f;
-#pragma unroll 4
-    for (int j = 0; j < a.top_k; ++j) {
-        const int at = of[j];
-        const float p = part[int64_t(max(at, 0)) * a.H + n];
-        y += at >= 0 ? picked[j].weight * p : 0.0f;
+    // Four ranks a wait; those past the last are read as the last.
+    for (int j = 0; j < a.top_k; j += 4) {
+        float p[4], weight[4];
+        int at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = min(j + i, a.top_k - 1);
+            at[i] = of[k];
+            weight[i] = picked[k].weight;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = part[int64_t(max(at[i], 0)) * a.H + n];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y += j + i < a.top_k && at[i] >= 0 ? weight[i] * p[i] : 0.0f;
     }
     const int64_t at = int64_t(m) * a.H + n;
     if (a.y_f32) a.y_f32[at] = y;

@@ -348,8 +348,14 @@ __global__ __launch_bounds__(256) void w4a8_join_kernel(W4Launch a) {
     if (n >= a.N) return;
     const int64_t at = int64_t(m) * a.N + n, all = int64_t(a.M) * a.N;
     float v = 0.0f;
-#pragma unroll 8
-    for (int p = 0; p < a.parts; ++p) v += a.ws[p * all + at];
+    // Eight parts a wait; those past the last are read as the last.
+    for (int p = 0; p < a.parts; p += 8) {
+        float t[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = a.ws[min(p + i, a.parts - 1) * all + at];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += p + i < a.parts ? t[i] : 0.0f;
+    }
     v *= (a.zeros ? kBack<true> : kBack<false>) * a.sa[m];
     if (a.y_f32) a.y_f32[at] = v;
     if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
