@@ -8,7 +8,7 @@
 //   route     every token's experts and weights, every expert's tokens: pairs
 //             (token, expert) in the order of experts; rows padded to tiles
 //   up        hidden[pair]          quant  hidden to int8
-//   down      part[pair]            combine  y[token], pairs in order of rank
+//   down      part[token][rank]     combine  y[token], ranks in order
 //
 // All sums of products are integers, so how they are split and joined does
 // not show.  Weights are in the T32x128 layout, one matrix an expert.
@@ -34,7 +34,7 @@ struct Slot {
 };
 struct Pairs {
     int count;
-    int of[kMaxPairs];                  // [token][rank]: pair, -1 none
+    int row[kMaxPairs];                 // of a pair: token * top_k + rank
 };
 struct Picked {                         // [token][rank]
     int expert;                         // -1: none, -2: a broken token
@@ -542,14 +542,11 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeLaunch a, i
 #pragma unroll
     for (int i = 0; i < kRouteTokens; ++i) {
         const int m = wv + i * kRouteWaves, e = expert[i];
-        if (m >= a.M || lane >= a.top_k) continue;
-        int at = -1;
-        if (e >= 0) {
-            const uint32_t lo = mask[e][0], hi = mask[e][1];
-            at = begins[e] + (m < 32 ? __popc(lo & ((1u << m) - 1u))
-                                     : __popc(lo) + __popc(hi & ((1u << (m - 32)) - 1u)));
-        }
-        pairs->of[m * a.top_k + lane] = at;
+        if (e < 0) continue;
+        const uint32_t lo = mask[e][0], hi = mask[e][1];
+        const int at = begins[e] + (m < 32 ? __popc(lo & ((1u << m) - 1u))
+                                           : __popc(lo) + __popc(hi & ((1u << (m - 32)) - 1u)));
+        pairs->row[at] = m * a.top_k + lane;
     }
 }
 
@@ -771,6 +768,7 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_down_kernel(MoeLaunch a) {
     const int s0 = STRIPS * int(blockIdx.x);
     const float *scales = reinterpret_cast<const float *>(a.ws + a.sp.scales);
     const int *code_sums = reinterpret_cast<const int *>(a.ws + a.sp.code_sums);
+    const int *row_of = reinterpret_cast<const Pairs *>(a.ws + a.sp.pair)->row;
     float *part = reinterpret_cast<float *>(a.ws + a.sp.part);
     const int tokens = __popc(slot.mask[0]) + __popc(slot.mask[1]);
     const int lane = int(threadIdx.x) & 63, r = lane & 15, c = lane >> 4;
@@ -785,7 +783,8 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_down_kernel(MoeLaunch a) {
 
     for (int m0 = 0; m0 < tokens; m0 += kMoeRows) {
         const int at = slot.begin + min(m0 + r, tokens - 1);
-        const float mine = scales[at];             // of row r
+        const float mine = scales[at];
+        const int my_row = row_of[at];             // of row r
         int sum = 0;
 #pragma unroll
         for (int i = 0; i < kQuantWaves; ++i) sum += code_sums[at * kQuantWaves + i];
@@ -798,7 +797,7 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_down_kernel(MoeLaunch a) {
         join_waves(red, lane, wv, v, all);
         const float sh = __shfl(mine, 4 * c + wv);
         const int sx = __shfl(sum, 4 * c + wv), m = m0 + 4 * c + wv;
-        float *out = part + int64_t(slot.begin + m) * a.H;
+        float *out = part + int64_t(__shfl(my_row, 4 * c + wv)) * a.H;
 #pragma unroll
         for (int k = 0; k < STRIPS; ++k) {
             const int row = (s0 + k) * kTileRows + 2 * r;
@@ -813,25 +812,23 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_down_kernel(MoeLaunch a) {
 
 __global__ __launch_bounds__(256) void moe_combine_kernel(MoeLaunch a) {
     const int n = int(blockIdx.x) * 256 + int(threadIdx.x), m = int(blockIdx.y);
-    const int *of = reinterpret_cast<const Pairs *>(a.ws + a.sp.pair)->of + m * a.top_k;
     const Picked *picked = reinterpret_cast<const Picked *>(a.ws + a.sp.picked) + m * a.top_k;
-    const float *part = reinterpret_cast<const float *>(a.ws + a.sp.part);
+    const float *part = reinterpret_cast<const float *>(a.ws + a.sp.part) + int64_t(m) * a.top_k * a.H + n;
     if (n >= a.H) return;
     float y = picked[0].expert == -2 ? __builtin_nanf("") : 0.0f;
-    // Four ranks a wait; those past the last are read as the last.
+    // Four ranks a wait; those past the last are read as the last.  (Nothing was
+    // written for a rank that has no expert.)
     for (int j = 0; j < a.top_k; j += 4) {
-        float p[4], weight[4];
-        int at[4];
+        Picked of[4];
+        float p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int k = min(j + i, a.top_k - 1);
-            at[i] = of[k];
-            weight[i] = picked[k].weight;
+            of[i] = picked[k];
+            p[i] = part[int64_t(k) * a.H];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = part[int64_t(max(at[i], 0)) * a.H + n];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y += j + i < a.top_k && at[i] >= 0 ? weight[i] * p[i] : 0.0f;
+        for (int i = 0; i < 4; ++i) y += j + i < a.top_k && of[i].expert >= 0 ? of[i].weight * p[i] : 0.0f;
     }
     const int64_t at = int64_t(m) * a.H + n;
     if (a.y_f32) a.y_f32[at] = y;
