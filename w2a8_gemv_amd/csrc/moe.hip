@@ -873,25 +873,32 @@ int moe_mode() { return g_mode.load(std::memory_order_relaxed); }
 void set_moe_mode(int mode) { g_mode.store(mode, std::memory_order_relaxed); }
 
 // One token at a time reads an expert's weights once for every token that
-// takes it, but in two launches of some 10 us together; token rows together
-// read them once, in five launches of some 20.  So tokens go by themselves up
-// to two, and up to 36 MB of weights over all pairs (us, one at a time and
-// together; 8 experts of 2560 x 6912, two taken: two tokens 25.8 and 26.9, three
-// 30.8 and 30.6, four 38.5 and 31.7; 64 of 2560 x 640, eight taken: three tokens,
-// 29 MB, 18.6 and 26.5, four, 39 MB, 25.8 and 27.5, six, 59 MB, 31.6 and 29.7; 8 of
-// 2560 x 2560, one taken: six tokens, 29 MB, 18.7 and 21.7, eight, 39 MB, 23.7 and
-// 22.3; 32 of 1024 x 512, two taken, twelve tokens, 9 MB: 14.1 and 19.1).
+// takes it, in two launches; token rows together read them once, in five.  So
+// tokens go by themselves while the first launch is one round of workgroups
+// (two to a compute unit; one token, which shares no expert, up to four) and
+// the second is no more than four to a compute unit (us, one at a time and
+// together; 8 experts of 2560 x 6912, two taken: one token 15.6 and 21.6, two, 868
+// workgroups, 24.9 and 24.1; 16 of them, four taken, one token, 864, 24.4 and 25.8;
+// 64 of 2560 x 640, eight taken: three tokens, 480, 18.3 and 22.4, four, 640, 25.5
+// and 23.6; 8 of 2560 x 2560, one taken: six tokens, 480, 18.9 and 20.2, seven, 560,
+// 23.5 and 20.4; 16 of 5120 x 1280, two taken, four tokens, 320 and 1280 of the
+// second launch, 25.4 and 23.5; 32 of 1024 x 512, two taken: twelve tokens, 384 and
+// 768, 14.2 and 17.0, 24 tokens 22.9 and 18.0; 16 of 1024 x 4096, eight taken, one
+// token, 1024, 24.3 and 21.0).
 //
 // Together, a workgroup takes two strips of an expert where that leaves four
 // workgroups to a compute unit, so that a wave reads its rows for twice the
 // weights (the layer, us, two strips and one; 64 tokens, 16 experts of 5120 x
-// 6912: 95.3 and 99.2, 128 of 5120 x 1536, eight taken: 155 and 173), and one where
-// strips are fewer (13 tokens, 8 experts of 2560 x 6912: 40.5 and 38.2).
+// 6912: 93.9 and 99.2, 128 of 5120 x 1536, eight taken: 147 and 159), and one where
+// strips are fewer (8 tokens, 16 experts of 2560 x 2560, four taken: 30.1 and
+// 29.3; 8 of 2560 x 6912, two taken: four tokens 30.6 and 30.0, 64 tokens 57.3 and
+// 58.4).
 MoePlan moe_plan(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k, int cus) {
     MoePlan p;
     const int mode = moe_mode();
     const bool fits = top_k * round_up(I, kTileK) <= kOneLds;
-    const bool few = M <= 2 || double(M * top_k) * (0.75 * double(H) * double(I)) <= 36e6;
+    const bool few = M * top_k * ceil_div(I, kTileRows) <= (M == 1 ? 4 * cus - 1 : 2 * cus) &&
+                     M * ceil_div(H, kDownRows) <= 4 * cus;
     p.one = fits && (mode == 0 ? few : mode == 1);
     const int64_t slots = std::min(E, M * top_k);
     const auto strips = [&](int64_t N) { return ceil_div(ceil_div(N, kTileRows), 2) * slots >= 4 * int64_t(cus) ? 2 : 1; };
