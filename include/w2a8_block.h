@@ -81,8 +81,9 @@ int pack_w4a8(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros
 int unpack_w4a8(const void *packed, int64_t packed_bytes, int64_t N, int64_t K, int64_t group,
                 uint8_t *codes, uint16_t *scales, uint8_t *zeros);
 
-/* Device workspace bytes of w4a8_gemm, or -1 if a size is out of range: 0 up
- * to 16 rows, else room for the sums of up to 8 parts of k. */
+/* Device workspace bytes of w4a8_gemm, or -1 if a size is out of range: 0 for
+ * one row and for rows of 1920 values or fewer, else room for the sums of up to
+ * 8 parts of k. */
 int64_t w4a8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
 /* Product of int8 rows with them, 1 <= M <= W4A8_MAX_M (W2A8_ERR_SHAPE above):

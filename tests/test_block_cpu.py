@@ -331,6 +331,31 @@ def test_binding_checks_of_the_products(host_as_gpu):
             w2a8.gemm_w4a8(*args, **kw)
 
 
+def test_binding_refuses_weights_of_another_form(host_as_gpu):
+    t = torch.zeros
+    x, s = t((3, 300), dtype=torch.int8), t(3)
+    for group in (32, 64, 128):
+        for zeros in (False, True):
+            w = t(w2a8.w4a8_packed_bytes(20, 300, group, zeros), dtype=torch.uint8)
+            w2a8.gemm_w4a8(w, x, s, 20, 300, group, zeros=zeros)
+            with pytest.raises(ValueError):
+                w2a8.gemm_w4a8(w, x, s, 20, 300, group, zeros=not zeros)
+            with pytest.raises(ValueError):
+                w2a8.gemm_w4a8(torch.cat([w, w[:16]]), x, s, 20, 300, group, zeros=zeros)
+
+
+def test_workspace_of_the_products():
+    """None for one row and for short rows; room for the parts that are planned everywhere."""
+    for K in (1, 1919, 1920):
+        assert w2a8.w4a8_workspace_bytes(64, 100, K) == 0
+    assert w2a8.w4a8_workspace_bytes(1, 100, 50000) == 0
+    for M in (2, 16, 17, 33, 64):
+        for N in (1, 17, 640, 5120, 9000):
+            for K in (100, 1920, 1921, 2049, 5120, 50000):
+                parts = w2a8.w4a8_plan(M, N, K, 256)[3]
+                assert parts == 1 or 4 * M * N * parts <= w2a8.w4a8_workspace_bytes(M, N, K)
+
+
 def test_binding_checks_of_the_mixture(host_as_gpu):
     t, u8 = torch.zeros, torch.uint8
     H, I, E = 40, 33, 5

@@ -532,3 +532,60 @@ def test_repeated_calls_are_equal(mode, kernels):
     for _ in range(30):
         for got, w in zip(b.step(b.x, b.r), want):
             assert torch.equal(got, w)
+
+
+# ---------------------------------------------------------------------------
+# offsets past 32 bits
+# ---------------------------------------------------------------------------
+def test_norm_past_32_bits():
+    """2^20 rows of 2050: the last ones are those of a call on them alone (whose sum may round
+    another way)."""
+    x = torch.empty((1 << 20, 2050), dtype=torch.bfloat16, device=dev()).normal_()
+    w = torch.rand(2050, device=dev()).bfloat16()
+    q, s_a, _ = w2a8.rmsnorm_quant_int8(x, w)
+    few = x[-300:].clone()
+    qf, sf, _ = w2a8.rmsnorm_quant_int8(few, w)
+    torch.cuda.synchronize()
+    assert torch.equal(q[-300:], qf)
+    assert ((s_a[-300:] - sf).abs() <= 2 * UNIT * sf).all()
+
+
+@pytest.mark.parametrize("M", [1, 5, 40])
+def test_w4_past_32_bits(M):
+    """More than 2^31 bytes of codes: the last strips are those of a call on them alone.  Scales of
+    1 and rows of -1..1 make every sum an exact one (below 16384 * 8 < 2^24)."""
+    N, K = 264_000, 16384
+    tiles = N // 16 * (K // 128) * 1024
+    total = w2a8.w4a8_packed_bytes(N, K, 128)
+    assert tiles > 2 ** 31
+    p = torch.randint(0, 256, (total,), dtype=torch.uint8, device=dev())
+    p[tiles:].view(torch.int16).fill_(0x3C00)
+    x = torch.randint(-1, 2, (M, K), dtype=torch.int8, device=dev())
+    s_a = torch.ones(M, device=dev())
+    y = w2a8.gemm_w4a8(p, x, s_a, N, K, 128)
+    n = 160
+    last = torch.cat([p[tiles - n * K // 2:tiles], p[-2 * n * K // 128:]])
+    part = w2a8.gemm_w4a8(last, x, s_a, n, K, 128)
+    torch.cuda.synchronize()
+    assert torch.equal(y[:, -n:], part) and part.abs().max() > 0
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_moe_past_32_bits(M):
+    """The last of 256 experts, past 2^31 bytes of each of the matrices, is the one of a call with
+    it alone."""
+    H, I, E = 5120, 6912, 256
+    c = Moe(1, H, I, 1, 3)
+    x = torch.randint(-127, 128, (M, H), dtype=torch.int8, device=dev())
+    s_a, one = torch.full((M,), 0.01, device=dev()), torch.zeros((M, 1), device=dev())
+    scales = [torch.from_numpy(s).to(dev()) for s in c.s]
+    want = w2a8.moe(x, s_a, one, *c.packed, *scales, H, I, 1)
+    all_w = [torch.full((E, w.numel()), 0x55, dtype=torch.uint8, device=dev()) for w in c.packed]   # (weights 0)
+    for w, last in zip(all_w, c.packed):
+        w[-1] = last[0]
+    assert all_w[0].numel() > 2 ** 31 and all_w[2].numel() > 2 ** 31
+    logits = torch.full((M, E), -1.0, device=dev())
+    logits[:, -1] = 1.0
+    got = w2a8.moe(x, s_a, logits, *all_w, *[s.expand(E).contiguous() for s in scales], H, I, 1)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and want.abs().max() > 0

@@ -1026,7 +1026,7 @@ def unpack_w4a8(packed: torch.Tensor, N: int, K: int, group: int, scale_dtype=to
 
 @functools.lru_cache(maxsize=4096)
 def w4a8_workspace_bytes(M: int, N: int, K: int) -> int:
-    """Workspace bytes of w4a8_gemm (not to be cleared): 0 up to 16 rows."""
+    """Workspace bytes of w4a8_gemm (not to be cleared): 0 for one row and for short K."""
     v = int(lib().w4a8_workspace_bytes(M, N, K))
     if v < 0:
         raise W2A8Error(2, "w4a8_gemm")
@@ -1034,10 +1034,12 @@ def w4a8_workspace_bytes(M: int, N: int, K: int) -> int:
 
 
 def _w4_gemm(w_packed, x, s_a, M, N, K, group, scale_dtype, zeros, yf, yb, dev, workspace, stream):
-    pw = _mx4_ptr(w_packed, "w_packed", dev, torch.uint8, w4a8_packed_bytes(N, K, group, zeros))
+    nw, need, pws = w4a8_packed_bytes(N, K, group, zeros), w4a8_workspace_bytes(M, N, K), None
     px = _mx4_ptr(x, "x", dev, torch.int8, M * K, M * K)
     ps = _mx4_ptr(s_a, "s_a", dev, torch.float32, M, M)
-    code, need, pws = _w4_scale_type(scale_dtype), w4a8_workspace_bytes(M, N, K), None
+    code = _w4_scale_type(scale_dtype)
+    # (Exactly these bytes: with zero points or groups of their own they are another number.)
+    pw = _mx4_ptr(w_packed, "w_packed", dev, torch.uint8, nw, nw)
     if need:
         if workspace is None:
             workspace = _mx4_empty(x, (need,), torch.uint8, stream)

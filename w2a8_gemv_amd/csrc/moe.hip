@@ -346,13 +346,11 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_one_kernel(MoeLaunch a)
         const int g = tid + kDownThreads * i, j = g / per;
         if (g < groups) ahead[i] = load4(hidden + int64_t(j) * a.I, 4 * (g - j * per), a.I);
     }
-    // Each rank's largest hidden value, from the strips' (two ranks at most a wave).
-    uint32_t most[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (wv + kDownWaves * i < a.top_k)
-            for (int n = lane; n < strips; n += 64)
-                most[i] = max(most[i], __float_as_uint(tops[int64_t(wv + kDownWaves * i) * strips + n]));
+    // Each rank's largest hidden value, from the strips': a rank a wave.
+    static_assert(W2A8_MOE_MAX_TOP_K <= kDownWaves);
+    uint32_t most = 0;
+    if (wv < a.top_k)
+        for (int n = lane; n < strips; n += 64) most = max(most, __float_as_uint(tops[int64_t(wv) * strips + n]));
     if (tid < W2A8_MOE_MAX_TOP_K * kDownRows) (&sums[0][0])[tid] = 0;
 
     // This wave's steps, and the first of its weights.
@@ -372,14 +370,10 @@ __global__ __launch_bounds__(kDownThreads) void moe_down_one_kernel(MoeLaunch a)
         if (u0 + d < u1) load(u0 + d, d);
 
     const float sd = mine.expert >= 0 ? a.s_down[mine.expert] : 0.0f;     // of rank `lane`
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int j = wv + kDownWaves * i;
-        const float top = __uint_as_float(wave_max_u32(most[i]));
-        if (j < ranks && lane == 0) {
-            factor[j] = code_factor(top);
-            scale[j] = code_scale(top);
-        }
+    const float top = __uint_as_float(wave_max_u32(most));
+    if (wv < ranks && lane == 0) {
+        factor[wv] = code_factor(top);
+        scale[wv] = code_scale(top);
     }
     __syncthreads();
 #pragma unroll
@@ -557,10 +551,10 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeLaunch a, i
 // rows 2r and 2r + 1 of the strip and reads the slot of row group r / 2 and
 // k-part c + 4 (r % 2): its own two rows of one half of k, and two rows of its
 // neighbour's, which has those that it lacks.  A wave so reads a whole tile in
-// one load of 16 bytes a lane (64 tokens, 16 experts of 5120 x 6912: up 51 us,
-// down 29; with 8 bytes a lane, half a line at a time, 62 and 37).  The
-// instruction multiplies the codes w + 1 as they are; the sums are less the
-// row's sum at the end.
+// one load of 16 bytes a lane (64 tokens, 16 experts of 5120 x 6912: up 48 us,
+// down 27; with 8 bytes a lane, half a line at a time, 62 and 37 where this had
+// 51 and 29).  The instruction multiplies the codes w + 1 as they are; the sums
+// are less the row's sum at the end.
 typedef v4u Words;
 __device__ __forceinline__ Words load_words(const uint8_t *w) {
     return __builtin_nontemporal_load(reinterpret_cast<const v4u *>(w));
