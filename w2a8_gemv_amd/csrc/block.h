@@ -79,7 +79,7 @@ hipError_t launch_w4a8(const W4Launch &a, int cus, hipStream_t stream);
 
 // Mixture of experts: offsets into the workspace, all multiples of 256.
 struct MoeSpace {
-    int64_t picked, tops, slot, pair, scales, code_sums, row_sums, rows, codes, hidden, part, total;
+    int64_t picked, tops, slot, row_of, scales, code_sums, row_sums, rows, codes, hidden, part, total;
 };
 MoeSpace moe_space(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k);
 struct MoeLaunch {

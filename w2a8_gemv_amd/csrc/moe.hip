@@ -24,17 +24,12 @@ constexpr int kMoeWaves = 4;       // waves of a workgroup of them
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / 64;
 constexpr int kRouteTokens = W2A8_MOE_MAX_M / kRouteWaves;   // of a wave
-constexpr int kMaxPairs = W2A8_MOE_MAX_M * W2A8_MOE_MAX_TOP_K;
 constexpr int kPerLane = W2A8_MOE_MAX_E / 64;
 
 // What the route leaves behind.
 struct Slot {
     int expert, begin;                  // -1: none; the first of its pairs
     uint32_t mask[2];                   // its tokens
-};
-struct Pairs {
-    int count;
-    int row[kMaxPairs];                 // of a pair: token * top_k + rank
 };
 struct Picked {                         // [token][rank]
     int expert;                         // -1: none, -2: a broken token
@@ -480,7 +475,7 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeLaunch a, i
         return;
     }
     Slot *slot = reinterpret_cast<Slot *>(a.ws + a.sp.slot);
-    Pairs *pairs = reinterpret_cast<Pairs *>(a.ws + a.sp.pair);
+    int *row_of = reinterpret_cast<int *>(a.ws + a.sp.row_of);     // a pair's token * top_k + rank
     Router r[kRouteTokens];
 #pragma unroll
     for (int i = 0; i < kRouteTokens; ++i)
@@ -530,7 +525,6 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeLaunch a, i
             }
             if (e >= used >> 16 && e < slots) slot[e] = Slot{-1, 0, {0, 0}};
         }
-        if (lane == 0) pairs->count = used & 0xFFFF;
     }
     __syncthreads();
 #pragma unroll
@@ -540,7 +534,7 @@ __global__ __launch_bounds__(kRouteThreads) void moe_route_kernel(MoeLaunch a, i
         const uint32_t lo = mask[e][0], hi = mask[e][1];
         const int at = begins[e] + (m < 32 ? __popc(lo & ((1u << m) - 1u))
                                            : __popc(lo) + __popc(hi & ((1u << (m - 32)) - 1u)));
-        pairs->row[at] = m * a.top_k + lane;
+        row_of[at] = m * a.top_k + lane;
     }
 }
 
@@ -711,7 +705,9 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_up_kernel(MoeLaunch a) {
 }
 
 // One workgroup per pair: its hidden row to int8, padded with zeros to whole
-// tiles; the first values stay in registers between the two walks.
+// tiles; the first values stay in registers between the two walks.  (Places of
+// pairs that tokens left are rounded too, and not read: their number would
+// be a load ahead of all others, 0.3 us.)
 constexpr int kQuantThreads = 512, kQuantWaves = kQuantThreads / 64, kQuantKept = 4;
 
 __global__ __launch_bounds__(kQuantThreads) void moe_quant_kernel(MoeLaunch a) {
@@ -721,7 +717,6 @@ __global__ __launch_bounds__(kQuantThreads) void moe_quant_kernel(MoeLaunch a) {
     const int Ip = (a.I + kTileK - 1) / kTileK * kTileK;
     v4f kept[kQuantKept];
     uint32_t top = 0;
-    if (pair >= reinterpret_cast<const Pairs *>(a.ws + a.sp.pair)->count) return;
     auto largest = [&](v4f f) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
@@ -762,7 +757,7 @@ __global__ __launch_bounds__(64 * kMoeWaves) void moe_down_kernel(MoeLaunch a) {
     const int s0 = STRIPS * int(blockIdx.x);
     const float *scales = reinterpret_cast<const float *>(a.ws + a.sp.scales);
     const int *code_sums = reinterpret_cast<const int *>(a.ws + a.sp.code_sums);
-    const int *row_of = reinterpret_cast<const Pairs *>(a.ws + a.sp.pair)->row;
+    const int *row_of = reinterpret_cast<const int *>(a.ws + a.sp.row_of);
     float *part = reinterpret_cast<float *>(a.ws + a.sp.part);
     const int tokens = __popc(slot.mask[0]) + __popc(slot.mask[1]);
     const int lane = int(threadIdx.x) & 63, r = lane & 15, c = lane >> 4;
@@ -851,7 +846,7 @@ MoeSpace moe_space(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k) {
     s.picked = take(pairs * sizeof(Picked));
     s.tops = take(4 * pairs * ceil_div(I, kTileRows));
     s.slot = take(W2A8_MOE_MAX_E * sizeof(Slot));
-    s.pair = take(sizeof(Pairs));
+    s.row_of = take(4 * pairs);
     s.scales = take(4 * pairs);
     s.code_sums = take(4 * kQuantWaves * pairs);
     s.row_sums = take(4 * M);

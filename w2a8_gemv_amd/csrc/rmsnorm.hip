@@ -16,6 +16,8 @@
 namespace w2a8 {
 namespace {
 
+typedef v4u v4u_f __attribute__((aligned(4)));
+
 constexpr int kNormRowsMaxK = 32768;   // 4 chunks of 8 values for each of 1024 lanes
 
 __device__ __forceinline__ float half_value(uint32_t bits) {
@@ -25,26 +27,27 @@ __device__ __forceinline__ uint32_t half_bits(float v) {
     return uint32_t(__builtin_bit_cast(uint16_t, _Float16(v)));
 }
 
-// Values i..i+7 of a float row (at any alignment of its elements).
+// Values i..i+7 of a float row (at any alignment of its elements), as they are.
 template <int TYPE>
-__device__ __forceinline__ void load8(const void *p, int64_t i, float (&v)[8]) {
-    if constexpr (TYPE == W2A8_F32) {
-        const float *f = static_cast<const float *>(p) + i;
-        const v4f a = *reinterpret_cast<const v4f_b *>(f), b = *reinterpret_cast<const v4f_b *>(f + 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[j] = a[j];
-            v[4 + j] = b[j];
-        }
-    } else {
-        const v4u a = *reinterpret_cast<const v4u_any *>(static_cast<const uint16_t *>(p) + i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = TYPE == W2A8_BF16 ? lo_bf16(a[j]) : half_value(a[j] & 0xFFFFu);
-            v[2 * j + 1] = TYPE == W2A8_BF16 ? hi_bf16(a[j]) : half_value(a[j] >> 16);
+struct Raw8 {
+    v4u w[TYPE == W2A8_F32 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const void *p, int64_t i) {
+        if constexpr (TYPE == W2A8_F32) {
+            const v4u_f *f = reinterpret_cast<const v4u_f *>(static_cast<const float *>(p) + i);
+            w[0] = f[0];
+            w[1] = f[1];
+        } else {
+            w[0] = *reinterpret_cast<const v4u_any *>(static_cast<const uint16_t *>(p) + i);
         }
     }
-}
+    __device__ __forceinline__ float value(int j) const {
+        if constexpr (TYPE == W2A8_F32) return __uint_as_float(w[j >> 2][j & 3]);
+        const uint32_t u = w[0][j >> 1];
+        if constexpr (TYPE == W2A8_BF16) return j & 1 ? hi_bf16(u) : lo_bf16(u);
+        return half_value(j & 1 ? u >> 16 : u & 0xFFFFu);
+    }
+};
 
 // Rounds v to TYPE, stores it as values i..i+7, and leaves the rounded values.
 template <int TYPE>
@@ -78,39 +81,46 @@ __device__ __forceinline__ float store1(void *p, int64_t i, float v) {
     }
 }
 
-// Chunk c (8 values) of row m: h, stored, and v; values past K are 0.
+// The operands of a chunk of 8 values.
 template <int TYPE>
-__device__ __forceinline__ void norm_chunk(const NormLaunch &a, int64_t row, int c, float (&v)[8],
-                                           double &sum) {
-    const int k = 8 * c;
-    if (k + 8 <= a.K) {
-        load8<TYPE>(a.x, row + k, v);
-        if (a.residual) {
-            float r[8];
-            load8<TYPE>(a.residual, row + k, r);
+struct Chunk {
+    Raw8<TYPE> x, r, w;
+
+    __device__ __forceinline__ void load(const NormLaunch &a, int64_t row, int c) {
+        x.load(a.x, row + 8 * c);
+        if (a.residual) r.load(a.residual, row + 8 * c);
+        if (a.weight) w.load(a.weight, 8 * c);
+    }
+    // h, stored, and v.
+    __device__ __forceinline__ void use(const NormLaunch &a, int64_t row, int c, float (&v)[8], double &sum) const {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += r[j];
-            store8<TYPE>(a.h, row + k, v);
+        for (int j = 0; j < 8; ++j) v[j] = x.value(j);
+        if (a.residual) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += r.value(j);
+            store8<TYPE>(a.h, row + 8 * c, v);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum += double(v[j]) * double(v[j]);
         if (a.weight) {
-            float w[8];
-            load8<TYPE>(a.weight, k, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= w[j];
+            for (int j = 0; j < 8; ++j) v[j] *= w.value(j);
         }
-        return;
     }
+};
+
+// The same of the chunk that ends the row; values past K are 0.
+template <int TYPE>
+__device__ __forceinline__ void norm_last(const NormLaunch &a, int64_t row, int c, float (&v)[8], double &sum) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
+        const int k = 8 * c + j;
         v[j] = 0.0f;
-        if (k + j >= a.K) continue;
-        float f = mx4_load1<TYPE>(a.x, row + k + j);
-        if (a.residual)
-            f = store1<TYPE>(a.h, row + k + j, f + mx4_load1<TYPE>(a.residual, row + k + j));
+        if (k >= a.K) continue;
+        float f = mx4_load1<TYPE>(a.x, row + k);
+        if (a.residual) f = store1<TYPE>(a.h, row + k, f + mx4_load1<TYPE>(a.residual, row + k));
         sum += double(f) * double(f);
-        v[j] = a.weight ? f * mx4_load1<TYPE>(a.weight, k + j) : f;
+        v[j] = a.weight ? f * mx4_load1<TYPE>(a.weight, k) : f;
     }
 }
 
@@ -199,13 +209,24 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormLaunch a) {
     const int tid = int(threadIdx.x), bd = int(blockDim.x), m = int(blockIdx.x);
     const int nc = (a.K + 7) >> 3;
     const int64_t row = int64_t(m) * a.K;
+    const int full = a.K >> 3;
     float v[CPL][8], amax = 0.0f;
     double sum = 0.0;
+    // All loads first (lanes past the row's last whole chunk read it again).
+    Chunk<TYPE> q[CPL];
+    if (full > 0) {
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) q[i].load(a, row, min(tid + i * bd, full - 1));
+    }
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
+        const int c = tid + i * bd;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-        if (tid + i * bd < nc) norm_chunk<TYPE>(a, row, tid + i * bd, v[i], sum);
+        if (c < full)
+            q[i].use(a, row, c, v[i], sum);
+        else if (c < nc)
+            norm_last<TYPE>(a, row, c, v[i], sum);
     }
 #pragma unroll
     for (int i = 0; i < CPL; ++i)
@@ -234,8 +255,17 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormLaunch a) {
     const int64_t row = int64_t(m) * a.K;
     float amax = 0.0f, v[8];
     double sum = 0.0;
+    const auto chunk = [&](const NormLaunch &l, int c) __attribute__((always_inline)) {
+        if (c < a.K >> 3) {
+            Chunk<TYPE> q;
+            q.load(l, row, c);
+            q.use(l, row, c, v, sum);
+        } else {
+            norm_last<TYPE>(l, row, c, v, sum);
+        }
+    };
     for (int c = tid; c < nc; c += bd) {
-        norm_chunk<TYPE>(a, row, c, v, sum);
+        chunk(a, c);
 #pragma unroll
         for (int j = 0; j < 8; ++j) amax = abs_max(amax, v[j]);
     }
@@ -245,7 +275,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormLaunch a) {
     if (a.residual) again.x = a.h;
     again.residual = nullptr;
     for (int c = tid; c < nc; c += bd) {
-        norm_chunk<TYPE>(again, row, c, v, sum);
+        chunk(again, c);
         if (inv == 0.0f) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = 0.0f;
