@@ -92,6 +92,24 @@ def test_norm_matches_reference(M, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("K", [1, 3, 7, 8, 9, 10, 12, 14, 15, 17, 20, 23, 511, 513, 519, 1283, 1284, 4095, 8191, 8197, 32767,
+                               32775, 32776, 32777])
+def test_norm_rows_begin_anywhere(K, dtype):
+    """Nine rows of each length begin at every place that it allows, and write no byte of another."""
+    M = 9
+    x, r, w = norm_inputs(M, K, dtype, K)
+    q, s, h = guarded(M * K, torch.int8), guarded(M, torch.float32), guarded(M * K, dtype)
+    out = w2a8.rmsnorm_quant_int8(x.to(dev()), w.to(dev()), r.to(dev()), 1e-5, q[:M * K].view(M, K), s[:M], h[:M * K].view(M, K))
+    torch.cuda.synchronize()
+    assert_guard(q, M * K), assert_guard(s, M), assert_guard(h, M * K)
+    norm_check(x, r, w, float(np.float32(1e-5)), *out)
+    rd = r.to(dev())
+    again = w2a8.rmsnorm_quant_int8(x.to(dev()), w.to(dev()), rd, 1e-5, h=rd)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, again))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("K", [40, 1003, 33001])
 def test_norm_in_place(K, dtype):
     x, r, w = norm_inputs(3, K, dtype, K)

@@ -9,8 +9,8 @@
 // none passes its range.
 //
 // Bound by memory: a row is read once, held in registers as v (fp32), reduced
-// over the workgroup, rounded and stored.  Rows past 32768 values are walked
-// twice, the second time from h.
+// over the workgroup, rounded and stored.  Rows past 4096 chunks of 8 values are
+// walked twice, the second time from h.
 #include "block.h"
 
 namespace w2a8 {
@@ -18,7 +18,7 @@ namespace {
 
 typedef v4u v4u_f __attribute__((aligned(4)));
 
-constexpr int kNormRowsMaxK = 32768;   // 4 chunks of 8 values for each of 1024 lanes
+constexpr int kMaxChunks = 4096;       // 4 for each of 1024 lanes
 
 __device__ __forceinline__ float half_value(uint32_t bits) {
     return float(__builtin_bit_cast(_Float16, uint16_t(bits)));
@@ -81,24 +81,24 @@ __device__ __forceinline__ float store1(void *p, int64_t i, float v) {
     }
 }
 
-// The operands of a chunk of 8 values.
+// The operands of 8 values from k on, 0 <= k <= K - 8.
 template <int TYPE>
 struct Chunk {
     Raw8<TYPE> x, r, w;
 
-    __device__ __forceinline__ void load(const NormLaunch &a, int64_t row, int c) {
-        x.load(a.x, row + 8 * c);
-        if (a.residual) r.load(a.residual, row + 8 * c);
-        if (a.weight) w.load(a.weight, 8 * c);
+    __device__ __forceinline__ void load(const NormLaunch &a, int64_t row, int k) {
+        x.load(a.x, row + k);
+        if (a.residual) r.load(a.residual, row + k);
+        if (a.weight) w.load(a.weight, k);
     }
     // h, stored, and v.
-    __device__ __forceinline__ void use(const NormLaunch &a, int64_t row, int c, float (&v)[8], double &sum) const {
+    __device__ __forceinline__ void use(const NormLaunch &a, int64_t row, int k, float (&v)[8], double &sum) const {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = x.value(j);
         if (a.residual) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] += r.value(j);
-            store8<TYPE>(a.h, row + 8 * c, v);
+            store8<TYPE>(a.h, row + k, v);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum += double(v[j]) * double(v[j]);
@@ -109,37 +109,50 @@ struct Chunk {
     }
 };
 
-// The same of the chunk that ends the row; values past K are 0.
-template <int TYPE>
-__device__ __forceinline__ void norm_last(const NormLaunch &a, int64_t row, int c, float (&v)[8], double &sum) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int k = 8 * c + j;
-        v[j] = 0.0f;
-        if (k >= a.K) continue;
-        float f = mx4_load1<TYPE>(a.x, row + k);
-        if (a.residual) f = store1<TYPE>(a.h, row + k, f + mx4_load1<TYPE>(a.residual, row + k));
-        sum += double(f) * double(f);
-        v[j] = a.weight ? f * mx4_load1<TYPE>(a.weight, k) : f;
-    }
+__device__ __forceinline__ float abs_max(float amax, float v) {
+    return __int_as_float(max(__float_as_int(amax), __float_as_int(v) & 0x7FFFFFFF));
 }
 
-__device__ __forceinline__ void store_codes(const NormLaunch &a, int64_t row, int c,
-                                            const float (&v)[8], float inv) {
+__device__ __forceinline__ void store_codes(const NormLaunch &a, int64_t at, const float (&v)[8], float inv) {
     uint32_t o[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         o[i] = q8(v[4 * i], inv) | (q8(v[4 * i + 1], inv) << 8) | (q8(v[4 * i + 2], inv) << 16) |
                (q8(v[4 * i + 3], inv) << 24);
-    int8_t *out = a.xq + row + 8 * c;
-    if (8 * c + 8 <= a.K) {
-        *reinterpret_cast<v2u_b *>(out) = v2u{o[0], o[1]};
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 7; ++j)
-        if (8 * c + j < a.K) out[j] = int8_t(o[j >> 2] >> (8 * (j & 3)));
+    *reinterpret_cast<v2u_b *>(a.xq + at) = v2u{o[0], o[1]};
 }
+
+// Chunks begin at multiples of 8 values of the whole buffer, so that rows of any
+// length are read and written at aligned addresses (their weight is not).  The
+// values of a row ahead of its chunks, and those behind them, are one each to the
+// workgroup's last 16 lanes (8191 x 1287 fp16 with a residual 20.0 us; from the
+// row's start on 22.4; that with all ends by one lane 29.3; 8191 x 1288 18.5).
+template <int TYPE>
+struct Ends {
+    float x, r, w;
+    int k;                              // -1: none
+
+    __device__ __forceinline__ void load(const NormLaunch &a, int64_t row, int head, int nc) {
+        const int j = int(threadIdx.x) - int(blockDim.x) + 16;
+        k = j < 0 ? -1 : j < 8 ? (j < head ? j : -1) : head + 8 * nc + j - 8;
+        if (k >= a.K) k = -1;
+        if (k < 0) return;
+        x = mx4_load1<TYPE>(a.x, row + k);
+        r = a.residual ? mx4_load1<TYPE>(a.residual, row + k) : 0.0f;
+        w = a.weight ? mx4_load1<TYPE>(a.weight, k) : 1.0f;
+    }
+    // h, stored, and v, left in w.
+    __device__ __forceinline__ void use(const NormLaunch &a, int64_t row, double &sum, float &amax) {
+        if (k < 0) return;
+        if (a.residual) x = store1<TYPE>(a.h, row + k, x + r);
+        sum += double(x) * double(x);
+        w *= x;
+        amax = abs_max(amax, w);
+    }
+    __device__ __forceinline__ void store(const NormLaunch &a, int64_t row, float inv) const {
+        if (k >= 0) a.xq[row + k] = int8_t(q8(inv == 0.0f ? 0.0f : w, inv));
+    }
+};
 
 template <int CTRL>
 __device__ __forceinline__ double add_moved(double v) {
@@ -188,9 +201,6 @@ __device__ __forceinline__ void block_norm(NormSums &s, float &amax, double &sum
     }
     amax = __int_as_float(b);
 }
-__device__ __forceinline__ float abs_max(float amax, float v) {
-    return __int_as_float(max(__float_as_int(amax), __float_as_int(v) & 0x7FFFFFFF));
-}
 
 // The factor of the codes, and the row's scale by one lane.
 __device__ __forceinline__ float norm_scale(const NormLaunch &a, int m, float amax, double sum) {
@@ -202,36 +212,36 @@ __device__ __forceinline__ float norm_scale(const NormLaunch &a, int m, float am
     return fine && amax != 0.0f ? fminf(127.0f / amax, __FLT_MAX__) : 0.0f;
 }
 
-// One workgroup per row, CPL chunks of 8 values per lane.
-template <int TYPE, int CPL>
+// One workgroup per row, CPL chunks of 8 values per lane, and ENDS by the last lanes.
+template <int TYPE, int CPL, bool ENDS>
 __global__ __launch_bounds__(1024) void norm_rows_kernel(NormLaunch a) {
     __shared__ NormSums red;
     const int tid = int(threadIdx.x), bd = int(blockDim.x), m = int(blockIdx.x);
-    const int nc = (a.K + 7) >> 3;
     const int64_t row = int64_t(m) * a.K;
-    const int full = a.K >> 3;
+    const int head = ENDS ? min(int(-row) & 7, a.K) : 0, nc = (a.K - head) >> 3;
     float v[CPL][8], amax = 0.0f;
     double sum = 0.0;
-    // All loads first (lanes past the row's last whole chunk read it again).
+    // All loads first (2045 x 6912 fp32 17.5 us, 19.7 a chunk after the other);
+    // lanes without a chunk read the row's last.
     Chunk<TYPE> q[CPL];
-    if (full > 0) {
+    Ends<TYPE> ends;
+    if (nc > 0) {
 #pragma unroll
-        for (int i = 0; i < CPL; ++i) q[i].load(a, row, min(tid + i * bd, full - 1));
+        for (int i = 0; i < CPL; ++i) q[i].load(a, row, head + 8 * min(tid + i * bd, nc - 1));
     }
+    if (ENDS) ends.load(a, row, head, nc);
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
         const int c = tid + i * bd;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-        if (c < full)
-            q[i].use(a, row, c, v[i], sum);
-        else if (c < nc)
-            norm_last<TYPE>(a, row, c, v[i], sum);
+        if (c < nc) q[i].use(a, row, head + 8 * c, v[i], sum);
     }
 #pragma unroll
     for (int i = 0; i < CPL; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) amax = abs_max(amax, v[i][j]);
+    if (ENDS) ends.use(a, row, sum, amax);
     block_norm(red, amax, sum);
     const float inv = norm_scale(a, m, amax, sum);
 #pragma unroll
@@ -241,8 +251,9 @@ __global__ __launch_bounds__(1024) void norm_rows_kernel(NormLaunch a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
         }
-        if (tid + i * bd < nc) store_codes(a, row, tid + i * bd, v[i], inv);
+        if (tid + i * bd < nc) store_codes(a, row + head + 8 * (tid + i * bd), v[i], inv);
     }
+    if (ENDS) ends.store(a, row, inv);
 }
 
 // Rows of any length: the second walk reads h, which this lane wrote (x
@@ -251,57 +262,60 @@ template <int TYPE>
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormLaunch a) {
     __shared__ NormSums red;
     const int tid = int(threadIdx.x), bd = int(blockDim.x), m = int(blockIdx.x);
-    const int nc = (a.K + 7) >> 3;
     const int64_t row = int64_t(m) * a.K;
+    const int head = min(int(-row) & 7, a.K), nc = (a.K - head) >> 3;
     float amax = 0.0f, v[8];
     double sum = 0.0;
-    const auto chunk = [&](const NormLaunch &l, int c) __attribute__((always_inline)) {
-        if (c < a.K >> 3) {
-            Chunk<TYPE> q;
-            q.load(l, row, c);
-            q.use(l, row, c, v, sum);
-        } else {
-            norm_last<TYPE>(l, row, c, v, sum);
-        }
-    };
+    Chunk<TYPE> q;
+    Ends<TYPE> ends;
+    ends.load(a, row, head, nc);
     for (int c = tid; c < nc; c += bd) {
-        chunk(a, c);
+        q.load(a, row, head + 8 * c);
+        q.use(a, row, head + 8 * c, v, sum);
 #pragma unroll
         for (int j = 0; j < 8; ++j) amax = abs_max(amax, v[j]);
     }
+    ends.use(a, row, sum, amax);
     block_norm(red, amax, sum);
     const float inv = norm_scale(a, m, amax, sum);
     NormLaunch again = a;
     if (a.residual) again.x = a.h;
     again.residual = nullptr;
     for (int c = tid; c < nc; c += bd) {
-        chunk(again, c);
+        q.load(again, row, head + 8 * c);
+        q.use(again, row, head + 8 * c, v, sum);
         if (inv == 0.0f) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = 0.0f;
         }
-        store_codes(a, row, c, v, inv);
+        store_codes(a, row + head + 8 * c, v, inv);
     }
+    ends.store(a, row, inv);
 }
 
 // Lanes of a row: with a row or less for every compute unit, one chunk to a
 // lane; beyond, half as many lanes of two chunks, so that more rows are on
 // their way (us, 1024 and 512 lanes at most: 8192 x 5120 bf16 with a residual
-// 69.6 and 62.1, 2048 x 6912 29.5 and 25.0, 2045 x 6907 fp32 without 24.7 and
-// 21.5; 256 lanes 62.2, 25.5 and 23.3).
+// 69.6 and 62.1, 2048 x 6912 29.5 and 25.0; 256 lanes 62.2 and 25.5.  With all
+// loads ahead 512 lanes take 57.0 and 23.7).
 template <int TYPE>
 hipError_t norm_type(const NormLaunch &a, int cus, hipStream_t stream) {
-    const int slots = (a.K + 7) / 8;
+    const int slots = std::max(1, a.K / 8);
     const void *fn = reinterpret_cast<const void *>(&norm_long_kernel<TYPE>);
     int threads = 1024;
-    if (a.K <= kNormRowsMaxK) {
-        static const void *const fns[4] = {reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 1>),
-                                           reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 2>),
-                                           reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 3>),
-                                           reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 4>)};
+    if (slots <= kMaxChunks) {
+        static const void *const fns[2][4] = {
+            {reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 1, false>),
+             reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 2, false>),
+             reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 3, false>),
+             reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 4, false>)},
+            {reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 1, true>),
+             reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 2, true>),
+             reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 3, true>),
+             reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 4, true>)}};
         const int lanes = a.M > cus ? 512 : 1024;
         const int cpl = std::max(std::min(4, (slots + lanes - 1) / lanes), (slots + 1023) / 1024);
-        fn = fns[cpl - 1];
+        fn = fns[a.K % 8 != 0][cpl - 1];
         threads = ((slots + cpl - 1) / cpl + 63) / 64 * 64;
     }
     NormLaunch l = a;
