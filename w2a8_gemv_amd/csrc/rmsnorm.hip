@@ -294,10 +294,10 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormLaunch a) {
 }
 
 // Lanes of a row: with a row or less for every compute unit, one chunk to a
-// lane; beyond, half as many lanes of two chunks, so that more rows are on
-// their way (us, 1024 and 512 lanes at most: 8192 x 5120 bf16 with a residual
-// 69.6 and 62.1, 2048 x 6912 29.5 and 25.0; 256 lanes 62.2 and 25.5.  With all
-// loads ahead 512 lanes take 57.0 and 23.7).
+// lane; beyond, lanes of up to four chunks, so that more rows are on their way
+// (us, rows of 1024, 512 and 256 lanes where these are enough: 8192 x 5120 bf16
+// with a residual 60.5, 56.5 and 56.0, 2048 x 6912 26.5, 23.7 and 23.4, 2045 x 6912
+// fp32 without 22.1, 17.8 and 17.4, 8192 x 2560 30.1, 30.4 and 30.7).
 template <int TYPE>
 hipError_t norm_type(const NormLaunch &a, int cus, hipStream_t stream) {
     const int slots = std::max(1, a.K / 8);
@@ -313,7 +313,7 @@ hipError_t norm_type(const NormLaunch &a, int cus, hipStream_t stream) {
              reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 2, true>),
              reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 3, true>),
              reinterpret_cast<const void *>(&norm_rows_kernel<TYPE, 4, true>)}};
-        const int lanes = a.M > cus ? 512 : 1024;
+        const int lanes = a.M > cus ? 256 : 1024;
         const int cpl = std::max(std::min(4, (slots + lanes - 1) / lanes), (slots + 1023) / 1024);
         fn = fns[a.K % 8 != 0][cpl - 1];
         threads = ((slots + cpl - 1) / cpl + 63) / 64 * 64;
