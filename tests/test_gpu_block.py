@@ -110,6 +110,18 @@ def test_norm_rows_begin_anywhere(K, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("K", [2048, 2049, 4096, 4097, 5123, 6144, 6151, 8192, 8201, 16390, 24583])
+def test_norm_of_more_rows_than_compute_units(K, dtype):
+    """Every count of chunks a lane, with and without ends."""
+    M = 300
+    x, r, w = norm_inputs(M, K, dtype, K)
+    for residual in (r, None):
+        out = w2a8.rmsnorm_quant_int8(x.to(dev()), w.to(dev()), None if residual is None else r.to(dev()), 1e-5)
+        torch.cuda.synchronize()
+        norm_check(x, residual, w, float(np.float32(1e-5)), *out)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
 @pytest.mark.parametrize("K", [40, 1003, 33001])
 def test_norm_in_place(K, dtype):
     x, r, w = norm_inputs(3, K, dtype, K)
