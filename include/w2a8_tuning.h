@@ -128,13 +128,14 @@ int w2a8_linear_plan(int64_t N, int64_t K, int cus, int int4, int *kernel, int *
 int w2a8_mx4_plan(int64_t M, int64_t N, int64_t K, int ternary, int outputs, int cus, int *kernel,
                   int *rows, int *cols, int *groups, int *pass);
 
-/* What w4a8_gemm (w2a8_block.h) runs for (M, N, K) on a device with `cus`
- * (1..65536) compute units.  *kernel: 1 the one-row kernel (*groups waves
- * that share a strip's k), 2 the tile kernel (*rows activation rows of its
- * form, *groups groups of four waves that share a workgroup's k, *parts parts
- * of k, joined by a second launch where there are several).  Returns W2A8_OK,
- * W2A8_ERR_NULL, W2A8_ERR_SHAPE or W2A8_ERR_VALUE (cus). */
-int w2a8_w4a8_plan(int64_t M, int64_t N, int64_t K, int cus, int *kernel, int *rows, int *groups,
+/* What w4a8_gemm (w2a8_block.h) runs for (M, N, K) and groups of `group` on a
+ * device with `cus` (1..65536) compute units.  *kernel: 1 the one-row kernel
+ * (*groups waves that share a strip's k), 2 the tile kernel (*rows activation
+ * rows of its form, *groups groups of four waves that share a workgroup's k,
+ * *parts parts of k, joined by a second launch where there are several), 3 the
+ * few-strip kernel (*rows, and *groups waves that share a strip's k).  Returns
+ * W2A8_OK, W2A8_ERR_NULL, W2A8_ERR_SHAPE or W2A8_ERR_VALUE (group, cus). */
+int w2a8_w4a8_plan(int64_t M, int64_t N, int64_t K, int64_t group, int cus, int *kernel, int *rows, int *groups,
                    int *parts);
 
 /* What w2a8_moe runs for these sizes on a device with `cus` (1..65536) compute

@@ -352,8 +352,9 @@ def test_workspace_of_the_products():
     for M in (2, 16, 17, 33, 64):
         for N in (1, 17, 640, 5120, 9000):
             for K in (100, 1920, 1921, 2049, 5120, 50000):
-                parts = w2a8.w4a8_plan(M, N, K, 256)[3]
-                assert parts == 1 or 4 * M * N * parts <= w2a8.w4a8_workspace_bytes(M, N, K)
+                for group in (32, 64, 128):
+                    parts = w2a8.w4a8_plan(M, N, K, group, 256)[3]
+                    assert parts == 1 or 4 * M * N * parts <= w2a8.w4a8_workspace_bytes(M, N, K)
 
 
 def test_binding_checks_of_the_mixture(host_as_gpu):
@@ -388,15 +389,16 @@ def test_binding_checks_of_the_mixture(host_as_gpu):
 def test_plan_queries_refuse():
     L = w2a8.lib()
     out = [ctypes.byref(ctypes.c_int()) for _ in range(4)]
-    for f, ok, n in ((L.w2a8_w4a8_plan, (40, 100, 200, 256), 4), (L.w2a8_moe_plan, (40, 100, 200, 8, 2, 256), 3)):
+    for f, ok, n in ((L.w2a8_w4a8_plan, (40, 100, 200, 64, 256), 4), (L.w2a8_moe_plan, (40, 100, 200, 8, 2, 256), 3)):
         assert f(*ok, *out[:n]) == 0
         for i in range(n):
             assert f(*ok, *out[:i], None, *out[i + 1:n]) == NULL
         for i in range(len(ok) - 1):
-            assert f(*ok[:i], 0, *ok[i + 1:], *out[:n]) == SHAPE
+            assert f(*ok[:i], 0, *ok[i + 1:], *out[:n]) == (VALUE if n == 4 and i == 3 else SHAPE)
         for bad in (0, 65537, (1 << 31) - 1):
             assert f(*ok[:-1], bad, *out[:n]) == VALUE
-    assert L.w2a8_w4a8_plan(65, 100, 200, 256, *out) == SHAPE
+    assert L.w2a8_w4a8_plan(65, 100, 200, 64, 256, *out) == SHAPE
+    assert L.w2a8_w4a8_plan(40, 100, 200, 48, 256, *out) == VALUE
     assert L.w2a8_moe_plan(65, 100, 200, 8, 2, 256, *out[:3]) == SHAPE
     assert L.w2a8_tune_moe(-1) == VALUE and L.w2a8_tune_moe(5) == VALUE and L.w2a8_tune_moe(0) == 0
 
@@ -404,16 +406,17 @@ def test_plan_queries_refuse():
 def test_test_sizes_reach_every_plan():
     for want, sizes in block_sizes.W4.items():
         for size in sizes:
-            p = w2a8.w4a8_plan(*size, block_sizes.CUS)
-            assert p[:3] + (p[3] > 1,) == want, (size, p)
+            for group in (32, 64, 128):
+                p = w2a8.w4a8_plan(*size, group, block_sizes.CUS)
+                assert p[:3] + (p[3] > 1,) == want, (size, group, p)
     for want, sizes in block_sizes.MOE.items():
         for size in sizes:
             assert w2a8.moe_plan(*size, block_sizes.CUS) == want, size
     rng = np.random.default_rng(1)
     for m, n, k in np.exp(rng.uniform(0, 1, (20000, 3)) * np.log([64, 200000, 100000])).round().astype(int).tolist():
-        p = w2a8.w4a8_plan(m, n, k, block_sizes.CUS)
-        waves = p[2] if p[0] == 1 else 0
-        assert p[:3] + (p[3] > 1,) in block_sizes.W4 or (waves and waves == min(-(-k // 128), 8 if n <= 8192 else 4)), (m, n, k, p)
+        p = w2a8.w4a8_plan(m, n, k, 32 << (m + n + k) % 3, block_sizes.CUS)
+        waves = p[2] if p[0] != 2 else 0
+        assert p[:3] + (p[3] > 1,) in block_sizes.W4 or (waves and waves == min(-(-k // 128), 4 if p[0] == 1 and n > 8192 else 8)), (m, n, k, p)
         assert p[3] == 1 or 4 * m * n * p[3] <= w2a8.w4a8_workspace_bytes(m, n, k)
 
 

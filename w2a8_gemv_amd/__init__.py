@@ -116,7 +116,7 @@ def lib():
             getattr(L, name).restype = I32
         L.w4a8_packed_bytes.argtypes = [I64, I64, I64, I32]
         L.w4a8_packed_bytes.restype = I64
-        L.w2a8_w4a8_plan.argtypes = [I64, I64, I64, I32, P, P, P, P]
+        L.w2a8_w4a8_plan.argtypes = [I64, I64, I64, I64, I32, P, P, P, P]
         L.w2a8_w4a8_plan.restype = I32
         L.w2a8_moe_plan.argtypes = [I64, I64, I64, I64, I64, I32, P, P, P]
         L.w2a8_moe_plan.restype = I32
@@ -1242,11 +1242,11 @@ def mx4_plan(M: int, N: int, K: int, cus: int, ternary: bool = False, f32: bool 
     return tuple(x.value for x in v)
 
 
-def w4a8_plan(M: int, N: int, K: int, cus: int):
-    """What gemm_w4a8 runs for (M, N, K) on `cus` compute units: (kernel, rows, groups, parts),
+def w4a8_plan(M: int, N: int, K: int, group: int, cus: int):
+    """What gemm_w4a8 runs for (M, N, K) and groups of `group` on `cus` compute units: (kernel, rows, groups, parts),
     see w2a8_tuning.h."""
     v = [ctypes.c_int() for _ in range(4)]
-    _check(lib().w2a8_w4a8_plan(M, N, K, cus, *[ctypes.byref(x) for x in v]), "w2a8_w4a8_plan")
+    _check(lib().w2a8_w4a8_plan(M, N, K, group, cus, *[ctypes.byref(x) for x in v]), "w2a8_w4a8_plan")
     return tuple(x.value for x in v)
 
 

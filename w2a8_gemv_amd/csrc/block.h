@@ -70,11 +70,13 @@ struct W4Launch {
 // Most parts that k is split into (and the rows from which it may be).
 constexpr int kW4Parts = 8, kW4PartRows = 2;
 // How a product is run (w2a8_w4a8_plan): blocks of 16 activation rows (0: the
-// one-row kernel), waves of a strip or groups of waves, parts of k.
+// one-row kernel), waves of a strip or groups of waves, parts of k; few: a strip
+// to a workgroup.
 struct W4Plan {
     int blocks, groups, parts;
+    bool few;
 };
-W4Plan w4_plan(int M, int strips, int KT, int cus);
+W4Plan w4_plan(int M, int strips, int KT, int K, int group, int cus);
 hipError_t launch_w4a8(const W4Launch &a, int cus, hipStream_t stream);
 
 // Mixture of experts: offsets into the workspace, all multiples of 256.

@@ -261,12 +261,13 @@ int w2a8_moe(const int8_t *x, const float *s_a, const void *logits, int logit_ty
     return e == hipSuccess ? W2A8_OK : W2A8_ERR_LAUNCH;
 }
 
-int w2a8_w4a8_plan(int64_t M, int64_t N, int64_t K, int cus, int *kernel, int *rows, int *groups, int *parts) {
+int w2a8_w4a8_plan(int64_t M, int64_t N, int64_t K, int64_t group, int cus, int *kernel, int *rows, int *groups,
+                   int *parts) {
     if (!kernel || !rows || !groups || !parts) return W2A8_ERR_NULL;
     if (M < 1 || M > W4A8_MAX_M || !matrix_ok(N, K)) return W2A8_ERR_SHAPE;
-    if (cus < 1 || cus > 65536) return W2A8_ERR_VALUE;
-    const W4Plan p = w4_plan(int(M), int(ceil_div(N, kW4Rows)), int(w4_tiles(K)), cus);
-    *kernel = p.blocks ? 2 : 1;
+    if (!group_ok(group) || cus < 1 || cus > 65536) return W2A8_ERR_VALUE;
+    const W4Plan p = w4_plan(int(M), int(ceil_div(N, kW4Rows)), int(w4_tiles(K)), int(K), int(group), cus);
+    *kernel = p.few ? 3 : p.blocks ? 2 : 1;
     *rows = p.blocks ? 16 * p.blocks : 1;
     *groups = p.groups;
     *parts = p.parts;

@@ -172,7 +172,130 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4a8_row_kernel(W4Launch a) {
     if (a.y_bf16) a.y_bf16[n] = uint16_t(bf16_bits(v));
 }
 
-// More rows (2 to 64): activations through LDS.  A workgroup takes four strips
+constexpr int kFewWaves = 8;
+
+// Few strips, 2 to 64 rows.  A workgroup takes one strip, up to eight waves take
+// its tiles in turn and add their sums in LDS in wave order; a wave reads the
+// rows' part of a tile as operands, without LDS.  A ragged tile is the last of
+// the wave whose turn it is.  Bound by latency: a launch, two loads, one sum
+// (16 x 2560 x 2560: 4.3 us, 3.4 for one row of it; 16 waves 4.4).
+template <int P, int MB>
+struct Rows {
+    v4u v[MB][2];                       // P = 4: 8 bytes for every group
+
+    template <bool TAIL>
+    __device__ __forceinline__ void load(const int8_t *const (&xp)[MB], int t, int c, int K) {
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int j = 0; j < (P == 4 ? 4 : 2); ++j) {
+                const int k = t * kTileK + (P == 4 ? 32 * j + 8 * c : P == 2 ? 64 * j + 16 * c : 32 * c + 16 * j);
+                if constexpr (P == 4) {
+                    v2u x = TAIL ? v2u(load_int8_tail(xp[b], k, K).xy) : v2u(*reinterpret_cast<const v2u_b *>(xp[b] + k));
+                    v[b][j >> 1][2 * (j & 1)] = x[0];
+                    v[b][j >> 1][2 * (j & 1) + 1] = x[1];
+                } else {
+                    v[b][j] = TAIL ? load_int8_tail(xp[b], k, K) : v4u(*reinterpret_cast<const v4u_b *>(xp[b] + k));
+                }
+            }
+    }
+};
+
+template <int P, int MB, bool ZEROS>
+__global__ __launch_bounds__(64 * kFewWaves) void w4a8_few_kernel(W4Launch a) {
+    constexpr int D = 2;
+    extern __shared__ __attribute__((aligned(16))) float part[];       // [wave][block][e][lane]
+    const int tid = int(threadIdx.x), lane = tid & 63, r = lane & 15, c = lane >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), nw = int(blockDim.x) >> 6;
+    const int s = int(blockIdx.x);
+    const uint8_t *wp = a.w + int64_t(s) * a.KT * kW4TileBytes + 16 * lane;
+    const uint16_t *sp = a.scales + (int64_t(s) * a.GQ * 16 + r) * 4;
+    const uint8_t *zp = ZEROS ? a.zeros + (int64_t(s) * a.GQ * 16 + r) * 4 : nullptr;
+    const int8_t *xp[MB];
+    float y[MB][4];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+        xp[b] = a.x + int64_t(min(16 * b + r, a.M - 1)) * a.K;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[b][e] = 0.0f;
+    }
+    const auto use = [&](const Weights<P> &t, const Rows<P, MB> &x) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float sc = t.scale(i, a.bf16_scales);
+            const uint32_t z = ZEROS ? zero_bytes(t.z, i) : 0u;
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                v4i acc = {0, 0, 0, 0};
+                if constexpr (P == 4) {
+                    acc = mfma32(v2u{x.v[b][i >> 1][2 * (i & 1)], x.v[b][i >> 1][2 * (i & 1) + 1]},
+                                 v2u{low_values<ZEROS>(t.w[i], z), high_values<ZEROS>(t.w[i], z)}, acc);
+                } else {
+#pragma unroll
+                    for (int j = (P == 1 ? 0 : i); j < (P == 1 ? 2 : i + 1); ++j)
+                        acc = mfma64(x.v[b][j], t.template operand<ZEROS>(j, z), acc);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[b][e] = __builtin_fmaf(float(acc[e]), sc, y[b][e]);
+            }
+        }
+    };
+    const int whole = a.K / kTileK, n = wv < whole ? (whole - wv + nw - 1) / nw : 0;
+    Weights<P> d[D];
+    Rows<P, MB> x[D];
+    const auto load = [&](int i, int j) __attribute__((always_inline)) {
+        d[j].template load<ZEROS>(wp, sp, zp, wv + i * nw);
+        x[j].template load<false>(xp, wv + i * nw, c, a.K);
+    };
+#pragma unroll
+    for (int j = 0; j < D; ++j)
+        if (j < n) load(j, j);
+    int i = 0;
+    for (; i + 2 * D <= n; i += D) {
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+            use(d[j], x[j]);
+            load(i + j + D, j);
+        }
+    }
+    for (; i < n; i += D) {
+#pragma unroll
+        for (int j = 0; j < D; ++j) {
+            if (i + j < n) use(d[j], x[j]);
+            if (i + j + D < n) load(i + j + D, j);
+        }
+    }
+    if (whole < a.KT && wv == whole % nw) {
+        d[0].template load<ZEROS>(wp, sp, zp, whole);
+        x[0].template load<true>(xp, whole, c, a.K);
+        use(d[0], x[0]);
+    }
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[((wv * MB + b) * 4 + e) * 64 + lane] = y[b][e];
+    __syncthreads();
+    // Place o is lane o % 64's result e of block b: weight row o % 16, activation
+    // row 16b + 4c + e.
+    for (int o = tid; o < 256 * MB; o += 64 * nw) {
+        float v = 0.0f;
+        for (int w = 0; w < nw; w += 4) {
+            float t[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) t[q] = part[min(w + q, nw - 1) * 256 * MB + o];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v += w + q < nw ? t[q] : 0.0f;
+        }
+        const int n = s * kW4Rows + (o & 15), m = 16 * (o >> 8) + 4 * ((o >> 4) & 3) + ((o >> 6) & 3);
+        if (m >= a.M || n >= a.N) continue;
+        const int64_t at = int64_t(m) * a.N + n;
+        v *= kBack<ZEROS> * a.sa[m];
+        if (a.y_f32) a.y_f32[at] = v;
+        if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
+    }
+}
+
+// More strips: activations through LDS.  A workgroup takes four strips
 // and a range of the tiles of k, in GROUPS groups of four waves that take its
 // tiles in turn, a strip a wave; a group stages the rows' part of a tile (MB
 // blocks of 16 rows x 128 k) once for its four waves.  LDS holds it as
@@ -364,6 +487,11 @@ __global__ __launch_bounds__(256) void w4a8_join_kernel(W4Launch a) {
 template <int P, bool ZEROS>
 const void *w4_kernel(const W4Plan &p) {
     const auto fn = [](auto *k) { return reinterpret_cast<const void *>(k); };
+    if (p.few)
+        return p.blocks == 1   ? fn(&w4a8_few_kernel<P, 1, ZEROS>)
+               : p.blocks == 2 ? fn(&w4a8_few_kernel<P, 2, ZEROS>)
+               : p.blocks == 3 ? fn(&w4a8_few_kernel<P, 3, ZEROS>)
+                               : fn(&w4a8_few_kernel<P, 4, ZEROS>);
     const bool four = p.groups == 4;
     switch (p.blocks) {
     case 0: return fn(&w4a8_row_kernel<P, ZEROS>);
@@ -377,11 +505,14 @@ const void *w4_kernel(const W4Plan &p) {
 template <int P, bool ZEROS>
 hipError_t w4_launch(const W4Launch &la, int cus, hipStream_t stream) {
     W4Launch a = la;
-    const W4Plan p = w4_plan(a.M, a.strips, a.KT, cus);
+    const W4Plan p = w4_plan(a.M, a.strips, a.KT, a.K, a.group, cus);
     a.parts = p.parts;
     const int units = p.blocks ? int(ceil_div(a.strips, 4)) : a.strips, gx = std::min(units, 1 << 20);
     const unsigned far = unsigned(ceil_div(units, gx)), threads = unsigned((p.blocks ? 256 : 64) * p.groups);
     void *args[] = {&a};
+    if (p.few)
+        return hipLaunchKernel(w4_kernel<P, ZEROS>(p), dim3(unsigned(a.strips)), dim3(unsigned(64 * p.groups)), args,
+                               size_t(p.groups * p.blocks) * 1024, stream);
     const hipError_t e = hipLaunchKernel(w4_kernel<P, ZEROS>(p), dim3(unsigned(gx), unsigned(a.parts), far), dim3(threads),
                                          args, p.blocks ? 0 : size_t(std::min(a.KT * kTileK, kRowChunk)), stream);
     if (e != hipSuccess || a.parts == 1) return e;
@@ -410,15 +541,35 @@ hipError_t w4_zeros(const W4Launch &a, int cus, hipStream_t stream) {
 // against 9.8, 32 x 5120 x 5120 10.9 against 13.3; two otherwise: 16 x 55296 x
 // 5120 32.5 against 34.3, 32 x 5120 x 27648 24.0 against 26.8, and beyond 32
 // rows, whose stages are larger: 64 x 5120 x 27648 30.2 against 34.3.
-W4Plan w4_plan(int M, int strips, int KT, int cus) {
-    if (M == 1) return {0, std::min(strips > 2 * cus ? 4 : kMaxWaves, KT), 1};
+//
+// Few strips and 2 rows or more: a workgroup for each strip, while its waves have
+// few steps to make (tiles of a wave, by blocks of rows, by strips to a compute
+// unit).  Its waves read the rows from the L2 as operands, all strips the same, so
+// that no step may be one of many (us, this and workgroups of four strips; groups of
+// 128, 64 and 32: 16 x 2560 x 2560, 3 steps, 4.3, 4.3, 5.4 and 7.0, 7.3, 8.1; 64 rows,
+// 12 steps, 8.3, 8.6, 13.2 and 10.0, 10.5, 12.2; 32 x 2560 x 6912, 14 steps, 10.7, 10.2,
+// 16.2 and 10.2, 10.8, 12.4; two strips to a unit: 16 x 5120 x 1280, 4 steps, 4.2, 4.2,
+// 5.5 and 5.2, 5.5, 6.0; 32 x 8192 x 640, 4 steps, 4.8, 4.8, 7.5 and 5.2, 5.5, 6.0, 64
+// rows, 8 steps, 9.1, 9.3, 11.8 and 7.0, 7.4, 8.3; four: 16 x 13824 x 1024 5.4, 5.4, 8.0
+// and 5.2, 5.4, 6.0; rows that begin at odd addresses: 16 x 2560 x 2565, 3 steps, 6.9,
+// 6.9, 7.3 and 8.8, 9.0, 9.7, 32 rows, 6 steps, 10.1, 10.3, 10.7 and 9.6, 9.7, 10.9).
+static bool few_strips(int M, int strips, int KT, int K, int group, int cus) {
+    const int blocks = (M + 15) / 16, rounds = int(ceil_div(strips, cus));
+    const int steps = std::min(rounds, 3) * blocks * int(ceil_div(KT, kFewWaves));
+    if (rounds > 2 || (rounds == 2 && (K % 8 || blocks > (group == 32 ? 1 : 2)))) return false;
+    return steps <= (K % 8 ? 4 : (group == 32 ? 8 : 12) - 4 * (rounds - 1));
+}
+
+W4Plan w4_plan(int M, int strips, int KT, int K, int group, int cus) {
+    if (M == 1) return {0, std::min(strips > 2 * cus ? 4 : kMaxWaves, KT), 1, false};
+    if (few_strips(M, strips, KT, K, group, cus)) return {(M + 15) / 16, std::min(kFewWaves, KT), 1, true};
     const int units = int(ceil_div(strips, 4));
     const auto parts = [&](int groups) {
         return 2 * units > cus ? 1 : std::max(1, std::min({2 * cus / units, KT / (4 * groups), kW4Parts}));
     };
     const bool four = M <= 16 ? units <= cus : M <= 32 && units * parts(4) <= cus;
     const int groups = four ? 4 : 2;
-    return {(M + 15) / 16, groups, parts(groups)};
+    return {(M + 15) / 16, groups, parts(groups), false};
 }
 
 hipError_t launch_w4a8(const W4Launch &a, int cus, hipStream_t stream) {
