@@ -112,8 +112,9 @@ int w4a8_gemm(const void *w_packed, const int8_t *x, const float *s_a, int64_t M
  *   q, s_h: h quantized as quant_act_int8 does (on fp32 values);
  *   y[m] += p * (((float)(w_down[e] . q) * s_h) * s_down[e]),
  * added in the order of rank.  A token that takes no expert gives 0.  Logits
- * that hold a NaN or +infinity, and rows whose s_a is not finite or whose h
- * passes fp32, give a row of NaN.
+ * that hold a NaN or +infinity, and tokens that take an expert for which s_a or
+ * a g, u or h of the row is not finite (a g of -infinity is no 0), give a row of
+ * NaN.
  *
  * x: device, int8 [M][H]; s_a: device, fp32 [M]; logits: device, [M][E] of
  * logit_type.  w_gate, w_up: device, E matrices [I][H] in the T32x128 layout,

@@ -192,9 +192,11 @@ __device__ __forceinline__ int add16(v4u x, int s) {
     return s;
 }
 
+// A g that is not finite gives no finite value: silu of it is infinite or NaN by
+// its own steps, and relu, whose maximum drops a NaN and -infinity, has 0 * g for it.
 __device__ __forceinline__ float activate(int act, float g, float u) {
     if (act == W2A8_ACT_SILU) return (g / (1.0f + expf(-g))) * u;
-    const float p = fmaxf(g, 0.0f);
+    const float p = fmaxf(g, 0.0f) + 0.0f * g;
     return (p * p) * u;
 }
 
