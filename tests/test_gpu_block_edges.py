@@ -53,3 +53,57 @@ def test_moe_broken_expert_marks_its_tokens_alone(mode, act, which, value, kerne
         assert (np.abs(got[fine] - want[fine]) <= bound[fine]).all()
         if not np.isfinite(value) and which != "down":
             assert np.isnan(got[takes]).all()
+
+
+# ---------------------------------------------------------------------------
+# 4-bit weights at both ends of fp32
+# ---------------------------------------------------------------------------
+# Every kernel: a row of one and of several stages, few strips, whole k and parts of k.
+W4_ENDS = [(1, 100, 300), (1, 40, 33000), (7, 33, 4095), (50, 31, 1023), (9, 900, 6001), (20, 500, 9000), (9, 8300, 130),
+           (33, 8300, 31), (49, 8300, 65)]
+
+
+def w4_ends_case(M, N, K, group, zeros, seed):
+    """Codes, rows and zero points whose groups' sums have one sign, so that no sum passes the last:
+    x, q, z, groups."""
+    rng = np.random.default_rng(seed)
+    groups = -(-K // group)
+    x = rng.integers(0, 9, (M, K)).astype(np.int8)
+    q = rng.integers(8, 16, (N, K)).astype(np.uint8)
+    z = rng.integers(0, 9, (N, groups)).astype(np.uint8) if zeros else None
+    return x, q, z, groups
+
+
+def w4_ends_check(x, s_a, q, sc, z, group, dtype):
+    """Sums that are exact in fp32 (below 33000 * 15 * 8 * 3 < 2^24 units, of one scale or three): the
+    output is that sum times s_a, rounded once.  The product of 24 bits and 24 is exact in 64."""
+    (M, K), N = x.shape, q.shape[0]
+    assert sc.dtype == torch.float64 and torch.equal(sc.to(dtype).double(), sc)
+    packed = w2a8.pack_w4a8(torch.from_numpy(block.w4_interchange(q)), sc.to(dtype), N, K, group,
+                            None if z is None else torch.from_numpy(z)).to(dev())
+    y, size = block.w4_product(x, np.ones(M), q, sc.numpy(), z, group)
+    assert size.max() <= np.finfo(np.float32).max
+    with np.errstate(over="ignore"):
+        want = torch.from_numpy((y * s_a.astype(np.float64)[:, None]).astype(np.float32))
+    f = torch.empty((M, N), device=dev())
+    b = torch.empty((M, N), dtype=torch.bfloat16, device=dev())
+    w2a8.w4a8_gemm(packed, torch.from_numpy(x).to(dev()), torch.from_numpy(s_a).to(dev()), M, N, K, group, dtype,
+                   z is not None, f, b)
+    torch.cuda.synchronize()
+    assert torch.equal(f.cpu(), want)
+    assert torch.equal(b.cpu(), want.bfloat16())
+    return y, want
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", W4_ENDS)
+def test_w4_smallest_token_scales(M, N, K, group, zeros, dtype):
+    """Token scales down to the smallest subnormal keep all of their bits."""
+    x, q, z, groups = w4_ends_case(M, N, K, group, zeros, M + N + K)
+    rng = np.random.default_rng(K)
+    sign = torch.from_numpy(rng.choice([-1.0, 1.0], (N, 1))).expand(N, groups).contiguous()
+    ends = np.array([1.1e-38, 1e-40, 3e-42, 2.0 ** -149], np.float32)
+    for i in range(4 if M == 1 else 1):
+        w4_ends_check(x, ends[(np.arange(M) + i) % 4], q, sign, z, group, dtype)

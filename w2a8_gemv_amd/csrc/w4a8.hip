@@ -38,7 +38,8 @@ __device__ __forceinline__ uint32_t high_values(uint32_t w, uint32_t z) {
     if constexpr (!ZEROS) return w & 0xF0F0F0F0u;
     return low_values<true>(w >> 4, z);
 }
-// What the sums of such bytes are multiplied by, in the end.
+// What the sums of such bytes are multiplied by, in the end (the sums themselves: a
+// token scale would lose bits below 2^-122).
 template <bool ZEROS>
 constexpr float kBack = ZEROS ? 1.0f : 0.0625f;
 // Zero point byte i (z - 8) of a word, as z in every byte.
@@ -167,7 +168,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4a8_row_kernel(W4Launch a) {
     if (tid >= 16 || n >= a.N) return;
     float v = 0.0f;
     for (int w = 0; w < nw; ++w) v += red[w][tid];
-    v *= kBack<ZEROS> * a.sa[0];
+    v = (v * kBack<ZEROS>) * a.sa[0];
     if (a.y_f32) a.y_f32[n] = v;
     if (a.y_bf16) a.y_bf16[n] = uint16_t(bf16_bits(v));
 }
@@ -289,7 +290,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void w4a8_few_kernel(W4Launch a) {
         const int n = s * kW4Rows + (o & 15), m = 16 * (o >> 8) + 4 * ((o >> 4) & 3) + ((o >> 6) & 3);
         if (m >= a.M || n >= a.N) continue;
         const int64_t at = int64_t(m) * a.N + n;
-        v *= kBack<ZEROS> * a.sa[m];
+        v = (v * kBack<ZEROS>) * a.sa[m];
         if (a.y_f32) a.y_f32[at] = v;
         if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
     }
@@ -459,7 +460,7 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void w4a8_tile_kernel(W4Launch a) 
                 a.ws[part * (int64_t(a.M) * a.N) + at] = y[b][e];
                 continue;
             }
-            const float v = y[b][e] * (kBack<ZEROS> * a.sa[m]);
+            const float v = (y[b][e] * kBack<ZEROS>) * a.sa[m];
             if (a.y_f32) a.y_f32[at] = v;
             if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
         }
@@ -479,7 +480,7 @@ __global__ __launch_bounds__(256) void w4a8_join_kernel(W4Launch a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v += p + i < a.parts ? t[i] : 0.0f;
     }
-    v *= (a.zeros ? kBack<true> : kBack<false>) * a.sa[m];
+    v = (v * (a.zeros ? kBack<true> : kBack<false>)) * a.sa[m];
     if (a.y_f32) a.y_f32[at] = v;
     if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
 }
