@@ -107,3 +107,31 @@ def test_w4_smallest_token_scales(M, N, K, group, zeros, dtype):
     ends = np.array([1.1e-38, 1e-40, 3e-42, 2.0 ** -149], np.float32)
     for i in range(4 if M == 1 else 1):
         w4_ends_check(x, ends[(np.arange(M) + i) % 4], q, sign, z, group, dtype)
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", W4_ENDS)
+def test_w4_sums_up_to_the_largest_value(M, N, K, group, zeros):
+    """bf16 scales whose largest sum is in the top two powers of two of fp32."""
+    x, q, z, groups = w4_ends_case(M, N, K, group, zeros, M + N + K + 1)
+    rng = np.random.default_rng(K)
+    sign = rng.choice([-1.0, 1.0], (N, 1)) * np.ones((N, groups))
+    most = block.w4_product(x, np.ones(M), q, sign, z, group)[1].max()
+    sc = torch.from_numpy(sign * 2.0 ** (128 - int(np.ceil(np.log2(most)) + (np.log2(most) % 1 == 0))))
+    for s_a in (np.ones(M), rng.uniform(0.5, 1, M) * 2.0 ** -100):
+        y, want = w4_ends_check(x, s_a.astype(np.float32), q, sc, z, group, torch.bfloat16)
+        assert np.abs(y).max() >= 2.0 ** 126 and want.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", W4_ENDS)
+def test_w4_smallest_group_scales(M, N, K, group, zeros, dtype):
+    """One and three times the smallest subnormal of the scales' type."""
+    x, q, z, groups = w4_ends_case(M, N, K, group, zeros, M + N + K + 2)
+    rng = np.random.default_rng(K)
+    sc = torch.from_numpy(rng.choice([1.0, 3.0], (N, groups)) * torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps)
+    w4_ends_check(x, (rng.uniform(0.5, 1, M) * (2.0 ** 100 if dtype == torch.bfloat16 else 1)).astype(np.float32), q, sc, z, group,
+                  dtype)

@@ -11,11 +11,13 @@
 //
 // Two values share a byte.  In the high half, as two's complement of q - 8, a
 // value is a signed byte of 16 times itself: the high values are one AND, the
-// low ones a shift and an AND, and the 16 goes out in the end (a power of two,
-// so exactly).  With zero points a byte is q - z itself, three to four
-// operations a word.  A group's sum is at most 16 * 8 * 127 * 128 < 2^22, exact
-// as int32 and as fp32.  What is left of the work, and the most of it, is one
-// conversion and one multiply-add for every result and group.
+// low ones a shift and an AND, and the 16 goes out with the group's scale, one
+// multiplication each: exactly (the least bit of a bf16 scale is 2^-133, of fp32
+// 2^-149), and no sum is larger than the formula's.  With zero points a byte is
+// q - z itself, three to four operations a word.  A group's sum is at most
+// 16 * 8 * 128 * 128 = 2^21, exact as int32 and as fp32.  What is left of the work,
+// and the most of it, is one conversion and one multiply-add for every result and
+// group.
 //
 #include "block.h"
 #include "mx4_device.h"
@@ -38,16 +40,15 @@ __device__ __forceinline__ uint32_t high_values(uint32_t w, uint32_t z) {
     if constexpr (!ZEROS) return w & 0xF0F0F0F0u;
     return low_values<true>(w >> 4, z);
 }
-// What the sums of such bytes are multiplied by, in the end (the sums themselves: a
-// token scale would lose bits below 2^-122).
-template <bool ZEROS>
-constexpr float kBack = ZEROS ? 1.0f : 0.0625f;
 // Zero point byte i (z - 8) of a word, as z in every byte.
 __device__ __forceinline__ uint32_t zero_bytes(uint32_t z, int i) {
     return __builtin_amdgcn_perm(0u, (z & 0x0F0F0F0Fu) ^ 0x08080808u, 0x01010101u * uint32_t(i));
 }
+// A group's scale, for sums of such bytes: divided by 16 where these are.
+template <bool ZEROS>
 __device__ __forceinline__ float scale_value(uint32_t bits, int bf16) {
-    return bf16 ? __uint_as_float(bits << 16) : float(__builtin_bit_cast(_Float16, uint16_t(bits)));
+    const float s = bf16 ? __uint_as_float(bits << 16) : float(__builtin_bit_cast(_Float16, uint16_t(bits)));
+    return ZEROS ? s : s * 0.0625f;
 }
 
 __device__ __forceinline__ v4i mfma64(v4u x, v4u w, v4i acc) {
@@ -86,8 +87,9 @@ struct Weights {
         return v4u{low_values<ZEROS>(w[2 * j], zero), high_values<ZEROS>(w[2 * j], zero),
                    low_values<ZEROS>(w[2 * j + 1], zero), high_values<ZEROS>(w[2 * j + 1], zero)};
     }
+    template <bool ZEROS>
     __device__ __forceinline__ float scale(int i, int bf16) const {
-        return scale_value((s[i >> 1] >> (16 * (i & 1))) & 0xFFFFu, bf16);
+        return scale_value<ZEROS>((s[i >> 1] >> (16 * (i & 1))) & 0xFFFFu, bf16);
     }
 };
 
@@ -141,7 +143,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4a8_row_kernel(W4Launch a) {
                         acc = mfma64(*reinterpret_cast<const v4u *>(x + (P == 1 ? 32 * c + 16 * j : 64 * j + 16 * c)),
                                      t.template operand<ZEROS>(j, z), acc);
                 }
-                y = __builtin_fmaf(float(acc[0]), t.scale(g, a.bf16_scales), y);
+                y = __builtin_fmaf(float(acc[0]), t.template scale<ZEROS>(g, a.bf16_scales), y);
             }
         };
         // While no load can be past the end none is asked for it: a load that may
@@ -168,7 +170,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4a8_row_kernel(W4Launch a) {
     if (tid >= 16 || n >= a.N) return;
     float v = 0.0f;
     for (int w = 0; w < nw; ++w) v += red[w][tid];
-    v = (v * kBack<ZEROS>) * a.sa[0];
+    v *= a.sa[0];
     if (a.y_f32) a.y_f32[n] = v;
     if (a.y_bf16) a.y_bf16[n] = uint16_t(bf16_bits(v));
 }
@@ -223,7 +225,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void w4a8_few_kernel(W4Launch a) {
     const auto use = [&](const Weights<P> &t, const Rows<P, MB> &x) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const float sc = t.scale(i, a.bf16_scales);
+            const float sc = t.template scale<ZEROS>(i, a.bf16_scales);
             const uint32_t z = ZEROS ? zero_bytes(t.z, i) : 0u;
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
@@ -290,7 +292,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void w4a8_few_kernel(W4Launch a) {
         const int n = s * kW4Rows + (o & 15), m = 16 * (o >> 8) + 4 * ((o >> 4) & 3) + ((o >> 6) & 3);
         if (m >= a.M || n >= a.N) continue;
         const int64_t at = int64_t(m) * a.N + n;
-        v = (v * kBack<ZEROS>) * a.sa[m];
+        v *= a.sa[m];
         if (a.y_f32) a.y_f32[at] = v;
         if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
     }
@@ -366,7 +368,7 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void w4a8_tile_kernel(W4Launch a) 
     auto use = [&](const Weights<P> &d, const uint8_t *stage) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            const float sc = d.scale(i, a.bf16_scales);
+            const float sc = d.template scale<ZEROS>(i, a.bf16_scales);
             const uint32_t z = ZEROS ? zero_bytes(d.z, i) : 0u;
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
@@ -460,7 +462,7 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void w4a8_tile_kernel(W4Launch a) 
                 a.ws[part * (int64_t(a.M) * a.N) + at] = y[b][e];
                 continue;
             }
-            const float v = (y[b][e] * kBack<ZEROS>) * a.sa[m];
+            const float v = y[b][e] * a.sa[m];
             if (a.y_f32) a.y_f32[at] = v;
             if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
         }
@@ -480,7 +482,7 @@ __global__ __launch_bounds__(256) void w4a8_join_kernel(W4Launch a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v += p + i < a.parts ? t[i] : 0.0f;
     }
-    v = (v * (a.zeros ? kBack<true> : kBack<false>)) * a.sa[m];
+    v *= a.sa[m];
     if (a.y_f32) a.y_f32[at] = v;
     if (a.y_bf16) a.y_bf16[at] = uint16_t(bf16_bits(v));
 }
