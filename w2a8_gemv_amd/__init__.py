@@ -1013,7 +1013,10 @@ def unpack_w4a8(packed: torch.Tensor, N: int, K: int, group: int, scale_dtype=to
                 zeros: bool = False):
     """Packed 4-bit weights (CPU) -> (codes, scales, zeros or None) in the interchange form."""
     _need(packed, "packed", torch.uint8, "cpu")
-    w4a8_packed_bytes(N, K, group, zeros)
+    nb = w4a8_packed_bytes(N, K, group, zeros)
+    # (Exactly these bytes, as for the products: more are those of another form.)
+    if packed.numel() > nb:
+        raise ValueError(f"packed must have {nb} elements, got {packed.numel()}")
     _w4_scale_type(scale_dtype)
     groups = -(-K // group)
     codes = torch.empty((N, -(-K // 2)), dtype=torch.uint8)
