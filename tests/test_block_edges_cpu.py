@@ -27,3 +27,17 @@ def test_w4_unpacking_refuses_weights_of_another_form():
             for other in {32, 64, 128} - {group}:
                 with pytest.raises((ValueError, w2a8.W2A8Error)):
                     w2a8.unpack_w4a8(p, N, K, other, zeros=z is not None)
+
+
+def test_moe_plan_of_one_token():
+    """One or two experts go by themselves as long as their hidden rows fit LDS; of more, fewer
+    workgroups the more maxima each has to take.  The border is where it is for any device."""
+    one = lambda I, E, top_k, cus=256: w2a8.moe_plan(1, 2048, I, E, top_k, cus)[0] == 1  # noqa: E731
+    for I in (32736, 32768, 40960, 49152):
+        assert one(I, 8, 1) and one(I // 2, 8, 2)
+    assert not one(49153, 8, 1) and not one(24577, 8, 2)
+    for cus in (64, 256, 304):
+        for top_k in (3, 4, 8, 12, 16):
+            most = 40 * cus // (top_k + 8)                   # workgroups: strips of 32 times top_k
+            assert one(32 * (most // top_k), 16, top_k, cus)
+            assert not one(32 * (most // top_k) + 1, 16, top_k, cus)

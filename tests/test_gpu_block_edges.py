@@ -135,3 +135,14 @@ def test_w4_smallest_group_scales(M, N, K, group, zeros, dtype):
     sc = torch.from_numpy(rng.choice([1.0, 3.0], (N, groups)) * torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps)
     w4_ends_check(x, (rng.uniform(0.5, 1, M) * (2.0 ** 100 if dtype == torch.bfloat16 else 1)).astype(np.float32), q, sc, z, group,
                   dtype)
+
+
+@pytest.mark.parametrize("H,I,E,top_k", [(48, 49152, 2, 1), (33, 24576, 3, 2), (33, 24577, 3, 2), (100, 2560, 10, 8), (100, 2561, 10, 8)])
+def test_moe_one_token_round_the_border(H, I, E, top_k, kernels):
+    """One token's longest hidden rows, both kernels: the reference's result, and the same bits."""
+    c = Moe(1, H, I, E, H + I)
+    got = w2a8.moe(*c.args(), H, I, top_k, "relu2")
+    c.check(got, top_k, "relu2", True)
+    for mode in (1, 2):
+        kernels(mode)
+        assert torch.equal(w2a8.moe(*c.args(), H, I, top_k, "relu2"), got)

@@ -864,18 +864,32 @@ int moe_mode() { return g_mode.load(std::memory_order_relaxed); }
 void set_moe_mode(int mode) { g_mode.store(mode, std::memory_order_relaxed); }
 
 // One token at a time reads an expert's weights once for every token that
-// takes it, in two launches; token rows together read them once, in five.  So
-// tokens go by themselves while the first launch is one round of workgroups
-// (two to a compute unit; one token, which shares no expert, up to four) and
-// the second is no more than four to a compute unit (us, one at a time and
-// together; 8 experts of 2560 x 6912, two taken: one token 15.6 and 21.6, two, 868
-// workgroups, 24.9 and 24.1; 16 of them, four taken, one token, 864, 24.4 and 25.8;
-// 64 of 2560 x 640, eight taken: three tokens, 480, 18.3 and 22.4, four, 640, 25.5
-// and 23.6; 8 of 2560 x 2560, one taken: six tokens, 480, 18.9 and 20.2, seven, 560,
-// 23.5 and 20.4; 16 of 5120 x 1280, two taken, four tokens, 320 and 1280 of the
-// second launch, 25.4 and 23.5; 32 of 1024 x 512, two taken: twelve tokens, 384 and
-// 768, 14.2 and 17.0, 24 tokens 22.9 and 18.0; 16 of 1024 x 4096, eight taken, one
-// token, 1024, 24.3 and 21.0).
+// takes it, in two launches; token rows together read them once, in five (us
+// below: one at a time and together).
+//
+// Several tokens go by themselves while the first launch is one round of
+// workgroups (two to a compute unit) and the second is no more than four to a
+// compute unit (8 experts of 2560 x 6912, two taken: two tokens, 868 workgroups,
+// 24.9 and 24.1; 64 of 2560 x 640, eight taken: three tokens, 480, 18.3 and 22.4,
+// four, 640, 25.5 and 23.6; 8 of 2560 x 2560, one taken: six tokens, 480, 18.9 and
+// 20.2, seven, 560, 23.5 and 20.4; 16 of 5120 x 1280, two taken, four tokens, 320
+// and 1280 of the second launch, 25.4 and 23.5; 32 of 1024 x 512, two taken: twelve
+// tokens, 384 and 768, 14.2 and 17.0, 24 tokens 22.9 and 18.0).
+//
+// One token shares no expert.  Of one or two, together is the slower at every
+// size whose hidden rows fit LDS: its products have a strip of few experts to a
+// workgroup, and its other launches nothing to do (8 experts of 512 x 40960, one
+// taken, 1280 workgroups, 30.0 and 45.3, of 5120 x 12288 25.2 and 30.2; two taken, 512 x
+// 20480, 27.1 and 29.9, 5120 x 20480 52.9 and 54.2; the other way within 6%, at
+// 8192 x 13600: 49.2 and 46.4).  Of more, every workgroup of the first launch takes
+// up to top_k maxima one after the other, on top of a work that is worth some
+// eight of them, so their sum is what is bounded (16 of 2560 x 6400, four taken,
+// 800 workgroups, 24.3 and 25.7, 2560 x 8192, 1024, 28.5 and 28.0; 32 of 512 x 2048,
+// eight taken, 512, 16.2 and 17.0, 512 x 4096, 1024, 23.9 and 18.7, 2048 x 2560,
+// 640, 20.2 and 22.2, 2048 x 4096, 1024, 27.4 and 25.7; 64 of 2048 x 768, sixteen
+// taken, 384, 17.9 and 21.8, 2048 x 1536, 768, 26.2 and 25.2.  Over 252 sizes the
+// choice costs 0.6% on average, 10% at most, and 4.2% and 56% if all are bounded by
+// four workgroups to a compute unit).
 //
 // Together, a workgroup takes two strips of an expert where that leaves four
 // workgroups to a compute unit, so that a wave reads its rows for twice the
@@ -888,7 +902,8 @@ MoePlan moe_plan(int64_t M, int64_t H, int64_t I, int64_t E, int64_t top_k, int 
     MoePlan p;
     const int mode = moe_mode();
     const bool fits = top_k * round_up(I, kTileK) <= kOneLds;
-    const bool few = M * top_k * ceil_div(I, kTileRows) <= (M == 1 ? 4 * cus - 1 : 2 * cus) &&
+    const int64_t first = M * top_k * ceil_div(I, kTileRows);
+    const bool few = (M > 1 ? first <= 2 * cus : top_k <= 2 || first * (top_k + 8) <= 40 * cus) &&
                      M * ceil_div(H, kDownRows) <= 4 * cus;
     p.one = fits && (mode == 0 ? few : mode == 1);
     const int64_t slots = std::min(E, M * top_k);
