@@ -94,7 +94,9 @@ struct Weights {
 };
 
 // One row.  A workgroup takes one strip; its waves take the strip's tiles in
-// turn, D of them on their way, and add their sums in LDS in wave order.  The
+// turn, each asked for D tiles ahead, and add their sums in LDS in wave order.
+// (Compiled, a round of D begins with a wait for every load of the round before, its
+// last one among them: other waves hide the latency more than D does.)  The
 // row is staged once (kRowChunk values at a time, zeros past its end), so the
 // loop loads weights alone and knows no ragged tile.  Every row of the first
 // operand is that row, so all results of a lane are the same: one is scaled.
@@ -147,7 +149,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4a8_row_kernel(W4Launch a) {
             }
         };
         // While no load can be past the end none is asked for it: a load that may
-        // be skipped makes the compiler wait for all before it.
+        // be skipped makes the compiler wait for all before it at every tile.
         int i = 0;
         for (; i + 2 * D <= n; i += D) {
 #pragma unroll
@@ -307,16 +309,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void w4a8_few_kernel(W4Launch a) {
 // are 16 bytes apart from that, so that the stores of a row's chunks fall in
 // different banks.  Rows start anywhere, so they are staged through registers.
 //
-// Bound by the multiply-adds of the results (64 x 5120 x 27648, groups of 64:
-// some 120 vector instructions a tile, 8 of them on the matrix pipe; 27 us, of
-// which the instructions are 14 and the weights 15, side by side).  Each strip
+// Bound by the results' conversions and multiply-adds and by the loop's waits (64 x
+// 5120 x 27648, groups of 64: some 105 vector instructions a tile, 8 of them on the
+// matrix pipe; 27 us, of which the instructions are 12 and the weights 15, side by
+// side; half of the waves' cycles are waits).  Each strip
 // reading its rows from the L2 by itself took 106 us for that product.
 constexpr int kChunkBytes = 272;
 
 template <int P, int MB, bool ZEROS, int GROUPS>
 __global__ __launch_bounds__(256 * GROUPS, 2) void w4a8_tile_kernel(W4Launch a) {
     constexpr int STAGE = MB * 8 * kChunkBytes, PER = (MB * 128 + 255) / 256;
-    constexpr int D = 2;                     // tiles of a wave on their way
+    constexpr int D = 2;                     // tiles that a wave's weights are asked for ahead
     __shared__ __attribute__((aligned(16))) uint8_t stages[GROUPS][2][STAGE];
     const int tid = int(threadIdx.x) & 255, lane = tid & 63, r = lane & 15, c = lane >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -388,7 +391,9 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void w4a8_tile_kernel(W4Launch a) 
         }
     };
 
-    // Weights D tiles ahead; rows D + 1, the nearest of them in the other stage.
+    // Weights are asked for D tiles ahead; rows D + 1, the nearest of them in the other
+    // stage.  (Compiled, all weights asked for are waited for once in a round of D, ahead
+    // of its stages' stores: load_x may take its ragged side, which has loads of its own.)
     Weights<P> d[D];
     v4u xv[D][PER];
     const auto tile = [&](int i) { return t0 + group + i * GROUPS; };
@@ -403,7 +408,7 @@ __global__ __launch_bounds__(256 * GROUPS, 2) void w4a8_tile_kernel(W4Launch a) 
         if (j < n) load_x(tile(j), xv[j % D]);
     __syncthreads();
     // While no load can be past the end none is asked for it: a load that may
-    // be skipped makes the compiler wait for all before it.
+    // be skipped makes the compiler wait for all before it at every tile.
     static_assert(D % 2 == 0, "stages and weight sets turn together");
     int i = 0;
     for (; i + 2 * D < (t1 - t0) / GROUPS; i += D) {
