@@ -879,14 +879,14 @@ void set_moe_mode(int mode) { g_mode.store(mode, std::memory_order_relaxed); }
 // and 1280 of the second launch, 25.4 and 23.5; 32 of 1024 x 512, two taken: twelve
 // tokens, 384 and 768, 14.2 and 17.0, 24 tokens 22.9 and 18.0).
 //
-// One token shares no expert.  Of one or two, together is the slower at every
-// size whose hidden rows fit LDS: its products have a strip of few experts to a
-// workgroup, and its other launches nothing to do (8 experts of 512 x 40960, one
-// taken, 1280 workgroups, 30.0 and 45.3, of 5120 x 12288 25.2 and 30.2; two taken, 512 x
-// 20480, 27.1 and 29.9, 5120 x 20480 52.9 and 54.2; the other way within 6%, at
-// 8192 x 13600: 49.2 and 46.4).  Of more, every workgroup of the first launch takes
-// up to top_k maxima one after the other, on top of a work that is worth some
-// eight of them, so their sum is what is bounded (16 of 2560 x 6400, four taken,
+// One token shares no expert.  Where it takes one or two, together is the slower
+// wherever the hidden rows fit LDS, but for a few sizes within 6%: its products have a
+// strip of few experts to a workgroup, and its other launches little to do (8 experts
+// of 512 x 40960, one taken, 1280 workgroups, 30.0 and 45.3, of 5120 x 12288 25.2 and
+// 30.2; two taken, 512 x 20480, 27.1 and 29.9, 5120 x 20480 52.9 and 54.2; 5 of
+// 8192 x 13600, two taken, 49.2 and 46.4).  Where it takes more, every workgroup of
+// the first launch takes up to top_k maxima one after the other, on top of work that
+// is worth some eight of them, so their sum is bounded (16 of 2560 x 6400, four taken,
 // 800 workgroups, 24.3 and 25.7, 2560 x 8192, 1024, 28.5 and 28.0; 32 of 512 x 2048,
 // eight taken, 512, 16.2 and 17.0, 512 x 4096, 1024, 23.9 and 18.7, 2048 x 2560,
 // 640, 20.2 and 22.2, 2048 x 4096, 1024, 27.4 and 25.7; 64 of 2048 x 768, sixteen
